@@ -23,7 +23,7 @@ from .build import LIB as _LIB_PATH
 MS_OK, MS_ERR_ARG, MS_ERR_BUDGET, MS_ERR_NO_PAGES, MS_ERR_CUDA, MS_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 MS_ERR_SCRATCH = -6
 STATUS_BAD_SLOT, STATUS_BAD_POSITION, STATUS_BAD_PAGE, STATUS_TIMEOUT, STATUS_BAD_META = 1, 2, 4, 8, 16
-STATUS_INTERNAL = 32
+STATUS_INTERNAL, STATUS_NO_PAGES, STATUS_NONFINITE = 32, 64, 128
 PAGE_SIZE = 16
 
 _ERR_NAMES = {MS_ERR_ARG: "MS_ERR_ARG", MS_ERR_BUDGET: "MS_ERR_BUDGET", MS_ERR_NO_PAGES: "MS_ERR_NO_PAGES",
@@ -160,6 +160,23 @@ def lib() -> ctypes.CDLL:
             ("ms_graph_run", [_VP, _I32P, _I32P, _I32P, _I32P, _I32P, _I32P, ctypes.c_int32, ctypes.c_int32,
                               ctypes.c_int32, _VP, _I32P]),
             ("ms_graph_read_status", [_VP, _VP, _I32P])):
+        getattr(h, name).restype = ctypes.c_int
+        getattr(h, name).argtypes = args
+    h.ms_q4_block_bytes.restype = ctypes.c_int64
+    h.ms_q4_block_bytes.argtypes = [ctypes.c_int32]
+    for name, args in (
+            ("ms_kv_append_rope_q4", [_VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int32, _VP,
+                                      ctypes.c_int32, _VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                      ctypes.c_int32, _VP, _VP]),
+            ("ms_kv_read_q4", [_VP, ctypes.c_int32, _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int32, ctypes.c_int32,
+                               ctypes.c_int32, _VP, _VP]),
+            ("ms_mixed_step_attention_q4", [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                            ctypes.c_float, _VP, _VP, ctypes.c_size_t, _VP]),
+            ("ms_build_batch_metadata_device", [_VP, _VP, ctypes.c_int32, _VP, ctypes.c_int32, _VP, ctypes.c_int32,
+                                                _VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP,
+                                                _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int64, _VP, _VP, _VP])):
         getattr(h, name).restype = ctypes.c_int
         getattr(h, name).argtypes = args
     h.ms_graph_workspace_size.restype = ctypes.c_size_t
@@ -718,6 +735,184 @@ def mixed_step_attention_noalloc(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_
                                                PAGE_SIZE, float(scale), _ptr(out), _ptr(dev_status),
                                                _stream(stream))
     _check(rc, "ms_mixed_step_attention_noalloc")
+
+
+# ---------------------------------------------------------------------------- 4-bit cache, metadata on the GPU
+
+def q4_block_bytes(D: int) -> int:
+    """Bytes of one page of one KV head of a 4-bit cache (ms_q4_block_bytes): the last dimension of a pool
+    [pages, H_kv, q4_block_bytes(D)] of dtype uint8."""
+    n = int(lib().ms_q4_block_bytes(int(D)))
+    if n == 0:
+        raise ValueError(f"D must be 64 or 128, got {D}")
+    return n
+
+
+def _pool_q4(kv_cache, D: int) -> int:
+    """Check a 4-bit pool for head dim D; returns its H_kv."""
+    import torch
+    if kv_cache is None or kv_cache.dim() != 3:
+        raise ValueError("kv_cache must be [pages, H_kv, q4_block_bytes(D)]")
+    _dev(kv_cache, "kv_cache", torch.uint8, (kv_cache.shape[0], kv_cache.shape[1], q4_block_bytes(D)))
+    return kv_cache.shape[1]
+
+
+def _on_current_gpu(names: str, *tensors) -> None:
+    """_on_one_gpu, and that GPU the current one: the library launches on the current device."""
+    import torch
+    _on_one_gpu(names, *tensors)
+    dev = next(t for t in tensors if t is not None).get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def kv_append_rope_q4(q, k, v, positions, slot_mapping, cos_tab, sin_tab, kv_cache, q_rot=None, dev_status=None,
+                      stream=None) -> None:
+    """Rotate q, k at absolute positions; append k, v into the 4-bit pool (ms_kv_append_rope_q4)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H_q, D], got {tuple(q.shape)}")
+    T, H_q, D = q.shape
+    H_kv = _pool_q4(kv_cache, D)
+    if q_rot is None:
+        q_rot = q
+    _dev(q, "q", torch.bfloat16)
+    _dev(k, "k", torch.bfloat16, (T, H_kv, D))
+    _dev(v, "v", torch.bfloat16, (T, H_kv, D))
+    _dev(q_rot, "q_rot", torch.bfloat16, (T, H_q, D))
+    _dev(positions, "positions", torch.int32, min_numel=T)
+    _dev(slot_mapping, "slot_mapping", torch.int32, min_numel=T)
+    if cos_tab.dim() != 2:
+        raise ValueError("cos_tab must be [max_pos, D/2]")
+    _dev(cos_tab, "cos_tab", torch.float32, (cos_tab.shape[0], D // 2))
+    _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
+    if dev_status is not None:
+        _dev(dev_status, "dev_status", torch.int32, min_numel=1)
+    _on_current_gpu("q k v q_rot positions slot_mapping cos_tab sin_tab kv_cache dev_status", q, k, v, q_rot, positions,
+                    slot_mapping, cos_tab, sin_tab, kv_cache, dev_status)
+    rc = lib().ms_kv_append_rope_q4(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(slot_mapping), T, _ptr(cos_tab),
+                                    _ptr(sin_tab), cos_tab.shape[0], _ptr(kv_cache), kv_cache.shape[0], _ptr(q_rot),
+                                    H_q, H_kv, D, PAGE_SIZE, _ptr(dev_status), _stream(stream))
+    _check(rc, "ms_kv_append_rope_q4")
+
+
+def kv_read_q4(kv_cache, slots, k_out, v_out, dev_status=None, stream=None) -> None:
+    """The rows at ``slots`` of a 4-bit pool as bf16 into ``k_out`` and ``v_out`` [n, H_kv, D] (ms_kv_read_q4)."""
+    import torch
+    if k_out.dim() != 3:
+        raise ValueError(f"k_out must be [n, H_kv, D], got {tuple(k_out.shape)}")
+    n, H_kv, D = k_out.shape
+    if _pool_q4(kv_cache, D) != H_kv:
+        raise ValueError(f"kv_cache has {kv_cache.shape[1]} KV heads, k_out {H_kv}")
+    _dev(k_out, "k_out", torch.bfloat16)
+    _dev(v_out, "v_out", torch.bfloat16, k_out.shape)
+    _dev(slots, "slots", torch.int32, min_numel=n)
+    if dev_status is not None:
+        _dev(dev_status, "dev_status", torch.int32, min_numel=1)
+    _on_current_gpu("kv_cache slots k_out v_out dev_status", kv_cache, slots, k_out, v_out, dev_status)
+    rc = lib().ms_kv_read_q4(_ptr(kv_cache), kv_cache.shape[0], _ptr(slots), n, _ptr(k_out), _ptr(v_out), H_kv, D,
+                             PAGE_SIZE, _ptr(dev_status), _stream(stream))
+    _check(rc, "ms_kv_read_q4")
+
+
+def mixed_step_attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables,
+                            context_total: int, out, workspace, bt_offsets=None, scale: float = None,
+                            stream=None) -> None:
+    """Causal attention of every packed row over its pages of a 4-bit pool (ms_mixed_step_attention_q4).
+    ``block_tables`` is the padded [rows, stride] table, or, with ``bt_offsets`` given, the ragged page list."""
+    import torch
+    if q_rot.dim() != 3:
+        raise ValueError(f"q_rot must be [T, H_q, D], got {tuple(q_rot.shape)}")
+    T, H_q, D = q_rot.shape
+    H_kv = _pool_q4(kv_cache, D)
+    _dev(q_rot, "q_rot", torch.bfloat16)
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must be 1-D with rows + 1 entries")
+    S = cu_seqlens_q.shape[0] - 1
+    _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    _dev(q_start_pos, "q_start_pos", torch.int32, min_numel=S)
+    _dev(context_lens, "context_lens", torch.int32, min_numel=S)
+    if bt_offsets is None:
+        stride = block_tables.shape[1] if block_tables.dim() == 2 else block_tables.shape[0] // max(S, 1)
+        _dev(block_tables, "block_tables", torch.int32, min_numel=S * stride)
+        bt_len = 0
+    else:
+        _dev(bt_offsets, "bt_offsets", torch.int32, min_numel=S + 1)
+        _dev(block_tables, "block_tables", torch.int32, min_numel=1)
+        stride, bt_len = 0, block_tables.numel()
+    _dev(out, "out", torch.bfloat16, (T, H_q, D))
+    _dev(workspace, "workspace", None)
+    _on_current_gpu("q_rot kv_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace", q_rot,
+                    kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out, workspace)
+    if scale is None:
+        scale = float(D) ** -0.5
+    rc = lib().ms_mixed_step_attention_q4(_ptr(q_rot), _ptr(kv_cache), kv_cache.shape[0], _ptr(cu_seqlens_q),
+                                          _ptr(q_start_pos), _ptr(context_lens), _ptr(block_tables), _ptr(bt_offsets),
+                                          bt_len, stride, S, T, int(context_total), H_q, H_kv, D, PAGE_SIZE,
+                                          float(scale), _ptr(out), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "ms_mixed_step_attention_q4")
+
+
+def build_batch_metadata_device(cached_lens, new_tokens, page_tables, num_pages: int, cu_seqlens_q, q_start_pos,
+                                context_lens, positions, slot_mapping, block_tables=None, bt_offsets=None,
+                                bt_pages=None, free_pages=None, free_count=None, free_state=None, info=None,
+                                dev_status=None, stream=None) -> None:
+    """A step's metadata on the GPU from the requests' lengths (ms_build_batch_metadata_device).
+
+    The table comes padded into ``block_tables`` [rows, stride], or ragged into ``bt_offsets`` [rows + 1] and
+    ``bt_pages``.  With ``free_pages``, ``free_count`` [1] and ``free_state`` [2] the rows take the pages that they
+    lack from the end of the free list, and ``free_state[0]`` receives the count that is left (``free_count`` may be
+    ``free_state[:1]``)."""
+    import torch
+    if page_tables.dim() != 2:
+        raise ValueError(f"page_tables must be [rows, stride], got {tuple(page_tables.shape)}")
+    R, table_stride = page_tables.shape
+    i32 = torch.int32
+    _dev(page_tables, "page_tables", i32)
+    _dev(cached_lens, "cached_lens", i32, (R,))
+    _dev(new_tokens, "new_tokens", i32, (R,))
+    _dev(cu_seqlens_q, "cu_seqlens_q", i32, (R + 1,))
+    _dev(q_start_pos, "q_start_pos", i32, min_numel=R)
+    _dev(context_lens, "context_lens", i32, min_numel=R)
+    if positions.dim() != 1:
+        raise ValueError(f"positions must be 1-D, got {tuple(positions.shape)}")
+    cap_tokens = positions.shape[0]
+    _dev(positions, "positions", i32)
+    _dev(slot_mapping, "slot_mapping", i32, (cap_tokens,))
+    stride = cap_pages = 0
+    if (block_tables is None) == (bt_offsets is None) or (bt_offsets is None) != (bt_pages is None):
+        raise ValueError("give block_tables, or bt_offsets and bt_pages")
+    if block_tables is not None:
+        if block_tables.dim() != 2:
+            raise ValueError(f"block_tables must be [rows, stride], got {tuple(block_tables.shape)}")
+        stride = block_tables.shape[1]
+        _dev(block_tables, "block_tables", i32, (R, stride))
+    else:
+        _dev(bt_offsets, "bt_offsets", i32, (R + 1,))
+        _dev(bt_pages, "bt_pages", i32, min_numel=1)
+        cap_pages = bt_pages.numel()
+    if len({free_pages is None, free_count is None, free_state is None}) != 1:
+        raise ValueError("free_pages, free_count and free_state come together")
+    if free_pages is not None:
+        _dev(free_pages, "free_pages", i32, min_numel=1)
+        _dev(free_count, "free_count", i32, min_numel=1)
+        _dev(free_state, "free_state", i32, min_numel=2)
+    if info is not None:
+        _dev(info, "info", i32, min_numel=4)
+    if dev_status is not None:
+        _dev(dev_status, "dev_status", i32, min_numel=1)
+    _on_current_gpu("page_tables cached_lens new_tokens cu_seqlens_q q_start_pos context_lens positions slot_mapping "
+                    "block_tables bt_offsets bt_pages free_pages free_count free_state info dev_status", page_tables,
+                    cached_lens, new_tokens, cu_seqlens_q, q_start_pos, context_lens, positions, slot_mapping,
+                    block_tables, bt_offsets, bt_pages, free_pages, free_count, free_state, info, dev_status)
+    rc = lib().ms_build_batch_metadata_device(
+        _ptr(cached_lens), _ptr(new_tokens), R, _ptr(page_tables), table_stride, _ptr(free_pages),
+        0 if free_pages is None else free_pages.numel(), _ptr(free_count), _ptr(free_state), int(num_pages), cap_tokens,
+        _ptr(cu_seqlens_q), _ptr(q_start_pos), _ptr(context_lens), _ptr(positions), _ptr(slot_mapping),
+        _ptr(block_tables), stride, _ptr(bt_offsets), _ptr(bt_pages), cap_pages, _ptr(info), _ptr(dev_status),
+        _stream(stream))
+    _check(rc, "ms_build_batch_metadata_device")
 
 
 def test_attention_stall(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables,

@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmixed_step.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["sched.cpp", "engine.cpp", "graph.cpp", "append_rope.cu", "attention.cu"]
+SOURCES = ["sched.cpp", "engine.cpp", "graph.cpp", "append_rope.cu", "attention.cu",
+           "append_q4.cu", "attention_q4.cu", "metadata.cu"]
 
 
 def _nvcc() -> str:

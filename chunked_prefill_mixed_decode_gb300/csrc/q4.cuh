@@ -1,0 +1,75 @@
+// The 4-bit K/V page: layout, encoding and decoding, shared by the kernels
+// that write, read back and attend over a 4-bit cache.
+//
+// Encoding.  A cached row of one token and KV head is cut into groups of 32
+// consecutive elements.  With a = max |x| of a group,
+//     s = r5(a / 7),    code = rint(x / s) in -7..7,    value = s * code,
+// where r5 rounds the fp32 quotient to five significant bits (nearest, ties
+// to even).  A code has at most three significant bits (or is a power of
+// two), so s * code has at most eight: every value a page can hold is exactly
+// a bf16, and tensor-core operands made from it carry no further rounding.
+// Rounding the scale to nearest rather than up costs no clipping: |x / s| <=
+// 7 (1 + 1/32) still rounds to 7, half a step away at most.
+//
+// Layout.  Page `pg` of KV head `h` is the 18 D-byte block at
+// ((pg * H_kv) + h) * 18 D, with NG = D / 32 groups to a row:
+//     K codes   [16 rows][D / 2 bytes]
+//     V codes   [16 rows][D / 2 bytes]
+//     K scales  [16 rows][NG] bf16
+//     V scales  [16 rows][NG] bf16
+// A nibble holds code + 8.  Element d = 32 g + 8 t + e (group g, quarter t,
+// e < 8) of a row sits, counted in nibbles from the row's start, at
+//     K:  (t NG + g) 8 + (e odd) 4 + e / 2
+//     V:  ((2 t + (e odd)) NG + g) 4 + e / 2
+// Tokens never share a byte, so an append writes whole bytes.  Either order
+// makes (w >> 4 i) & 0x000f000f a pair that an MMA fragment wants: for K the
+// neighbouring elements (2 i, 2 i + 1) of quarter t, whose 4 NG bytes one lane
+// loads at once; for V, after a byte permute joins the words of two tokens,
+// element 2 i + odd of both tokens.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace {
+
+constexpr int kQ4Page = 16;
+constexpr int kQ4Group = 32;
+
+__host__ __device__ constexpr int q4_block_bytes(int D) { return 18 * D; }
+
+template <int D>
+struct Q4 {
+  static constexpr int NG = D / kQ4Group;
+  static constexpr int ROW = D / 2;  // code bytes of a row
+  static constexpr int V_OFF = kQ4Page * ROW;
+  static constexpr int KS_OFF = 2 * kQ4Page * ROW;
+  static constexpr int VS_OFF = KS_OFF + kQ4Page * NG * 2;
+  static constexpr int BYTES = q4_block_bytes(D);
+  static_assert(VS_OFF + kQ4Page * NG * 2 == BYTES, "block layout");
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Scale of a group whose largest magnitude is `a` (finite): zero where a / 7
+// is below the smallest normal number (the whole group is then stored as
+// zeros), and held to the largest scale whose codes stay finite in bf16.
+__device__ __forceinline__ float q4_scale(float a) {
+  const float r = __fdiv_rn(a, 7.f);
+  if (!(r >= 1.17549435e-38f)) return 0.f;
+  uint32_t u = __float_as_uint(r);
+  u = (u + 0x3ffffu + ((u >> 19) & 1u)) & ~0x7ffffu;
+  return fminf(__uint_as_float(u), 1.125f * 4.2535295865117308e37f);  // 1.125 * 2^125
+}
+
+// x / s is exact enough in fp32: x has 8 significant bits and s has 5, so a
+// quotient that is not exactly halfway between two codes is at least 2^-13
+// away from it.
+__device__ __forceinline__ uint32_t q4_nibble(float x, float s) {
+  return s > 0.f ? static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x, s)) + 8) : 8u;
+}
+
+}  // namespace

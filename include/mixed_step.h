@@ -69,7 +69,9 @@ enum {
   MS_STATUS_BAD_PAGE = 4,      /* block_tables entry outside the page pool */
   MS_STATUS_TIMEOUT = 8,       /* a bounded in-kernel wait gave up */
   MS_STATUS_BAD_META = 16,     /* inconsistent row metadata (lengths, offsets) */
-  MS_STATUS_INTERNAL = 32      /* an internal invariant failed (shared-memory alignment) */
+  MS_STATUS_INTERNAL = 32,     /* an internal invariant failed (shared-memory alignment) */
+  MS_STATUS_NO_PAGES = 64,     /* the free list or a page table cannot hold a step's tokens */
+  MS_STATUS_NONFINITE = 128    /* an infinity or NaN met by the 4-bit append */
 };
 
 /* One request as the scheduler sees it.
@@ -383,6 +385,119 @@ MS_API int ms_test_attention_split(const void* q_rot, const void* k_cache, const
                                    int32_t num_tokens, int64_t context_total, int32_t H_q, int32_t H_kv, int32_t D,
                                    int32_t page_size, float scale, void* out, void* workspace, size_t ws_bytes,
                                    int32_t chunk_ctas, ms_stream_t stream);
+
+/* ---- 4-bit K/V cache (device) ---------------------------------------------
+ * A cache of 4.5 bits per element instead of 16.  A row of one token and KV
+ * head is cut into groups of 32 consecutive elements; with a = max |x| of a
+ * group,
+ *     s = r5(a / 7),   code = rint(x / s) in -7..7,   value = s * code,
+ * r5 rounding the fp32 quotient to five significant bits (nearest, ties to
+ * even), x / s the fp32 quotient.  Every value is exactly a bf16.  A group
+ * whose a / 7 is below the smallest normal fp32 number is stored as zeros, s
+ * is at most 1.125 * 2^125, and a group that holds an infinity or a NaN is
+ * stored as zeros with MS_STATUS_NONFINITE recorded: pages hold finite values
+ * only.
+ *
+ * The pool is one array of bytes, [num_pages][H_kv][18 D]: the block of a page
+ * and KV head holds the codes of its 16 K rows (D / 2 bytes each), those of
+ * its 16 V rows, the K scales (bf16 [16][D / 32]), then the V scales.  A nibble
+ * is code + 8; with NG = D / 32, element d = 32 g + 8 t + e (e < 8) of a row
+ * sits, counted in nibbles from the row's start (low nibble of a byte first),
+ * at (t NG + g) 8 + (e odd) 4 + e / 2 for K and at
+ * ((2 t + (e odd)) NG + g) 4 + e / 2 for V.  The pages have no counterpart. */
+
+/* ms_q4_block_bytes -- 18 D, the bytes of one page of one KV head; 0 for a D
+ * other than 64 or 128. */
+MS_API int64_t ms_q4_block_bytes(int32_t D);
+
+/* ms_kv_append_rope_q4 -- ms_kv_append_rope into a 4-bit cache: q_rot is bit
+ * for bit the same; the rotated, bf16-rounded k[t] and the raw v[t] are stored
+ * in 4 bits at slot_mapping[t].  Slots, positions, alignment, dev_status and
+ * errors as there; MS_STATUS_NONFINITE as above.  Two tokens of one call with
+ * the same slot leave either's bytes, or a mixture, there.
+ *   kv_cache  device, the 4-bit pool of num_pages pages, 16-byte aligned
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_kv_append_rope_q4(const void* q, const void* k, const void* v,
+                                const int32_t* positions, const int32_t* slot_mapping, int32_t T,
+                                const float* cos_tab, const float* sin_tab, int32_t max_pos,
+                                void* kv_cache, int32_t num_pages, void* q_rot,
+                                int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size,
+                                int32_t* dev_status, ms_stream_t stream);
+
+/* ms_kv_read_q4 -- the rows at n slots of a 4-bit cache as bf16: k_out[i] and
+ * v_out[i] ([n, H_kv, D]) get the values that slot slots[i] holds (exactly).
+ * For handing a cached prefix to a bf16 cache, or looking at one.  Slot -1
+ * reads as zeros; any other slot outside the pool reads as zeros and records
+ * MS_STATUS_BAD_SLOT when dev_status is given.  A slot may repeat.
+ * All tensor pointers 16-byte aligned.  n == 0 is a no-op.
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_kv_read_q4(const void* kv_cache, int32_t num_pages, const int32_t* slots, int32_t n,
+                         void* k_out, void* v_out, int32_t H_kv, int32_t D, int32_t page_size,
+                         int32_t* dev_status, ms_stream_t stream);
+
+/* ms_mixed_step_attention_q4 -- the attention of ms_mixed_step_attention
+ * (block_tables padded with bt_stride, bt_offsets == NULL) or of
+ * ms_mixed_step_attention_ragged (block_tables = bt_pages with bt_len entries,
+ * bt_offsets given) over a 4-bit cache: the same rows, causal bounds, pad
+ * rows, workspace (ms_attention_workspace_size), status bits, limits and
+ * errors, with K[j] and V[j] the values that the cache holds.  Scores and
+ * softmax statistics in fp32; the weights of V are rounded to bf16 before
+ * their products, as in the bf16 call.
+ *   kv_cache  device, the 4-bit pool of num_pages pages, 16-byte aligned
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
+                                      const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                      const int32_t* context_lens, const int32_t* block_tables,
+                                      const int32_t* bt_offsets, int64_t bt_len, int32_t bt_stride,
+                                      int32_t num_rows, int32_t num_tokens, int64_t context_total,
+                                      int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, float scale,
+                                      void* out, void* workspace, size_t ws_bytes, ms_stream_t stream);
+
+/* ---- Step metadata on the GPU ----------------------------------------------
+ * ms_build_batch_metadata_device -- the metadata of a step (what
+ * ms_build_batch_metadata writes on the host) from the requests' lengths, on
+ * the GPU, so that a step needs no host data and can be captured and replayed.
+ * Row s is request s with c = cached_lens[s] cached tokens and
+ * d = new_tokens[s] new ones; the caller chose d (there is no packing here).
+ *   cached_lens, new_tokens  device int32 [num_rows]; 1 <= num_rows <= 8192
+ *   page_tables   device int32 [num_rows, table_stride], the requests' physical
+ *                 pages in logical order
+ *   free_pages    device int32 [free_cap], the pages no request holds, taken
+ *                 from the end; free_count device int32, how many there are.
+ *                 A request then holds exactly ceil(c / 16) pages and takes
+ *                 ceil((c + d) / 16) - ceil(c / 16) more, in row order; they
+ *                 are written into page_tables.  free_state device int32 [2],
+ *                 zeroed once before its first use: word 0 receives the new
+ *                 count (free_count may point to it), word 1 is the library's.
+ *                 All three NULL: page_tables already holds every page.
+ *   num_pages     pages of the pool
+ * Outputs (device, caller-allocated):
+ *   cu_seqlens_q [num_rows + 1], q_start_pos, context_lens [num_rows];
+ *   positions, slot_mapping [cap_tokens]  tokens past the step's total get
+ *                 position 0 and slot -1 (pad tokens)
+ *   block_tables [num_rows, bt_stride] padded with -1 (bt_offsets and bt_pages
+ *                 NULL), or bt_offsets [num_rows + 1] and bt_pages [cap_pages]
+ *                 (block_tables NULL; entries past bt_offsets[num_rows] are
+ *                 left as they were)
+ *   info          device int32 [4] or NULL: tokens, pages in use, rows with
+ *                 d == 1, pages taken from the free list
+ * A row with d == 0 becomes a pad row: q_start_pos = context_lens = 0 and no
+ * pages.  A step that fails a check on the device becomes one of pad rows
+ * only, takes no page, and records why in dev_status (or NULL):
+ * MS_STATUS_BAD_META (a negative length, c + d past INT32_MAX, more tokens
+ * than cap_tokens, more pages than bt_stride or cap_pages, a free count
+ * outside 0..free_cap), MS_STATUS_NO_PAGES (a row longer than table_stride
+ * pages, or the free list too short).  A page id outside the pool gets slot
+ * -1 and records MS_STATUS_BAD_PAGE.  Calls that share free_state must not
+ * overlap on the GPU.
+ * Errors: MS_ERR_ARG (also cap_tokens above 2^21), MS_ERR_CUDA. */
+MS_API int ms_build_batch_metadata_device(
+    const int32_t* cached_lens, const int32_t* new_tokens, int32_t num_rows, int32_t* page_tables,
+    int32_t table_stride, const int32_t* free_pages, int32_t free_cap, const int32_t* free_count,
+    int32_t* free_state, int32_t num_pages, int32_t cap_tokens, int32_t* cu_seqlens_q, int32_t* q_start_pos,
+    int32_t* context_lens, int32_t* positions, int32_t* slot_mapping, int32_t* block_tables, int32_t bt_stride,
+    int32_t* bt_offsets, int32_t* bt_pages, int64_t cap_pages, int32_t* info, int32_t* dev_status,
+    ms_stream_t stream);
 
 /* ---- Multi-round engine (host) ------------------------------------------
  * A page pool with full-input admission and a plan/commit round driver over

@@ -18,6 +18,8 @@ in the pages' order and notation:
   and the paged K/V append through ``slot_mapping`` (zwjcode section 06);
 * ``attention`` -- causal attention of every query at absolute position p over
   keys 0..p read through the block table (zwjcode sections 02 and 07);
+* ``q4``        -- the 4-bit cache's rounding and bytes, and step metadata built
+  from request lengths;
 * ``engine``    -- a multi-round driver over a page pool that reserves a
   request's full input plus its new tokens at admission (zwjcode section 11;
   "Splitting Prefill From Decode Inside a Step").
@@ -31,10 +33,12 @@ from .schedule import (BudgetError, NoPagesError, schedule, batch_metadata, comm
 from .rope import bf16_to_f64, f32_to_bf16_bits, rope_tables, rope_rotate, kv_append
 from .attention import attention_rows, attention_all
 from .engine import AdmissionError, Engine
+from .q4 import metadata_from_lengths, q4_read, q4_round, q4_values, q4_write
 
 __all__ = [
     "BudgetError", "NoPagesError", "schedule", "batch_metadata", "commit_round", "DECODE_FIRST",
     "PREFILL_FIRST", "FAIR_SHARE",
     "bf16_to_f64", "f32_to_bf16_bits", "rope_tables", "rope_rotate", "kv_append",
     "attention_rows", "attention_all", "AdmissionError", "Engine",
+    "metadata_from_lengths", "q4_read", "q4_round", "q4_values", "q4_write",
 ]

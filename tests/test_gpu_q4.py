@@ -1,0 +1,660 @@
+"""The 4-bit cache on the GPU against plain 64-bit forms.
+
+Bytes, whole numbers and q_rot are compared bit for bit.  Attention has a bound
+from its arithmetic, per element: the output's rounding to bf16, half a step,
+2^-8 |ref|; the rounding of each weight (a probability times V's scale) to bf16,
+2^-8 of the sum A of p |v|; and 2^-10 A for everything in fp32.  The largest part
+of that last term is the scores': a decode row's products carry code + 128, so a
+score is off by at most about 2^-22 * 136 * sum |q| * s * scale, which for q ~
+N(0, 1), s = 0.45 and D = 128 is 2e-4, and twice that for a probability.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from chunked_prefill_mixed_decode_gb300 import build
+    build.build()
+    import chunked_prefill_mixed_decode_gb300 as ms
+    from chunked_prefill_mixed_decode_gb300 import step
+    return torch, ms, step
+
+
+def _i32(torch, a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------- append and read
+
+def _append(env, q, k, v, positions, slots, pool, max_pos):
+    torch, ms, step = env
+    H_q, D = q.shape[1:]
+    cos, sin = step.rope_tables_device(max_pos, D, "cuda")
+    q_rot = torch.full_like(q, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ms.kv_append_rope_q4(q, k, v, _i32(torch, positions), _i32(torch, slots), cos, sin, pool, q_rot=q_rot,
+                         dev_status=status)
+    return q_rot, ms.read_status(status)
+
+
+def _oracle_append(q, k, v, positions, slots, pool, ok):
+    """The oracle's bytes after the append of the tokens marked ok, and q_rot bits (or None) per token."""
+    D = q.shape[-1]
+    H_kv = k.shape[1]
+    kb, vb, qb = (workloads.bf16_bits(x) for x in (k, v, q))
+    cos, sin = oracle.rope_tables(np.maximum(positions, 0), D)
+    kr, qr = oracle.rope_rotate(kb, cos, sin), oracle.rope_rotate(qb, cos, sin)
+    out = pool.copy()
+    for t, s in enumerate(slots):
+        if ok[t]:
+            for h in range(H_kv):
+                oracle.q4_write(out, s, h, oracle.bf16_to_f64(kr[t, h]), False)
+                oracle.q4_write(out, s, h, oracle.bf16_to_f64(vb[t, h]), True)
+    return out, qr
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,T", [(4, 2, 64, 1), (8, 1, 128, 1), (8, 8, 128, 33), (40, 40, 64, 7),
+                                          (32, 8, 128, 129), (3, 1, 64, 50), (16, 2, 64, 257)])
+def test_append_bytes(env, H_q, H_kv, D, T):
+    """Random slots over pages that other tokens share; what no token names keeps its bytes."""
+    torch, ms, step = env
+    rng = np.random.default_rng(T + D)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q, k, v = (torch.randn(T, H, D, generator=g, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+    pages = 2 + 2 * (-(-T // 16))
+    before = rng.integers(0, 256, (pages, H_kv, 18 * D)).astype(np.uint8)
+    pool = torch.from_numpy(before.copy()).cuda()
+    slots = rng.permutation(16 * pages)[:T]
+    positions = rng.integers(0, 5000, T)
+    q_rot, status = _append(env, q, k, v, positions, slots, pool, 5000)
+    assert status == 0
+    want, qr = _oracle_append(q, k, v, positions, slots, before, [True] * T)
+    np.testing.assert_array_equal(workloads.bf16_bits(q_rot), qr)
+    np.testing.assert_array_equal(pool.cpu().numpy(), want)
+    # and the same rows read back, twice each and in another order
+    sl = np.concatenate([slots, slots[::-1]])
+    ko, vo = (torch.empty(2 * T, H_kv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ms.kv_read_q4(pool, _i32(torch, sl), ko, vo)
+    K, V = oracle.q4_read(want, D)
+    np.testing.assert_array_equal(oracle.bf16_to_f64(workloads.bf16_bits(ko)), K[sl // 16, :, sl % 16])
+    np.testing.assert_array_equal(oracle.bf16_to_f64(workloads.bf16_bits(vo)), V[sl // 16, :, sl % 16])
+
+
+def test_append_values_at_the_edges(env):
+    """Zeros, the smallest and the largest magnitudes, exact ties of the codes and of the scale, infinities and NaN."""
+    torch, ms, step = env
+    D = 128
+    rows = [np.zeros(D), np.full(D, 2.0 ** -126), np.full(D, 2.0 ** -133), np.full(D, 3.3895313892515355e38),
+            np.r_[7.0, np.arange(127) / 2 % 7], np.r_[115.5, np.full(127, 8.0)], np.r_[-122.5, np.full(127, 9.0)],
+            np.r_[7 * 2.0 ** -126, np.full(127, 2.0 ** -127)], np.full(D, -2.0 ** -124)]
+    bad = [np.r_[np.inf, np.ones(127)], np.r_[np.ones(40), np.nan, np.ones(87)], np.r_[np.ones(127), -np.inf]]
+    x = torch.tensor(np.array(rows + bad), dtype=torch.float32, device="cuda").to(torch.bfloat16)[:, None]
+    n = len(rows)
+    for part, flag in ((x[:n], 0), (x[n:], ms.STATUS_NONFINITE)):
+        part = part.contiguous()
+        T = part.shape[0]
+        pool = torch.full((1, 1, 18 * D), 0x33, dtype=torch.uint8, device="cuda")
+        before = pool.cpu().numpy()
+        _, status = _append(env, part, part, part, [0] * T, list(range(T)), pool, 1)  # position 0: no rotation
+        assert status == flag
+        want, _ = _oracle_append(part, part, part, np.zeros(T, int), range(T), before, [True] * T)
+        np.testing.assert_array_equal(pool.cpu().numpy(), want)
+    for r in range(len(bad)):  # one bad row at a time: whichever group holds it, it is reported
+        one = x[n + r:n + r + 1].contiguous()
+        pool = torch.zeros((1, 1, 18 * D), dtype=torch.uint8, device="cuda")
+        ones = torch.ones_like(one)
+        assert _append(env, ones, one, ones, [0], [0], pool, 1)[1] == ms.STATUS_NONFINITE
+        assert _append(env, ones, ones, one, [0], [0], pool, 1)[1] == ms.STATUS_NONFINITE
+
+
+def test_append_and_read_bad_slots_and_positions(env):
+    torch, ms, step = env
+    D, H_q, H_kv, pages = 64, 4, 2, 3
+    q, k, v = (torch.randn(6, H, D, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+    for slots, positions, flag in (([0, -1, 47, 5, -1, 9], [1] * 6, 0), ([0, 48, 47, 5, 6, 9], [1] * 6, 1),
+                                   ([0, -2, 47, 5, 6, 9], [1] * 6, 1), ([0, 1, 2, 3, 4, 5], [0, 9, 10, 3, -1, 2], 2)):
+        pool = torch.full((pages, H_kv, 18 * D), 0x21, dtype=torch.uint8, device="cuda")
+        before = pool.cpu().numpy()
+        q_rot, status = _append(env, q, k, v, positions, slots, pool, 10)
+        assert status == flag
+        in_table = [0 <= p < 10 for p in positions]
+        ok = [0 <= s < 16 * pages and i for s, i in zip(slots, in_table)]
+        want, qr = _oracle_append(q, k, v, np.clip(positions, 0, 9), slots, before, ok)
+        np.testing.assert_array_equal(pool.cpu().numpy(), want)
+        got = workloads.bf16_bits(q_rot)
+        for t in range(6):  # a token outside the table writes nothing at all
+            np.testing.assert_array_equal(got[t], qr[t] if in_table[t] else np.full_like(got[t], 0x40E0))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ko, vo = (torch.ones(3, H_kv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ms.kv_read_q4(pool, _i32(torch, [-1, 4, -1]), ko, vo, dev_status=status)
+    assert ms.read_status(status) == 0 and not ko[0].any() and not vo[2].any() and ko[1].any()
+    for bad in (-2, 48, 2 ** 31 - 1, -2 ** 31):
+        ms.kv_read_q4(pool, _i32(torch, [3, bad, 4]), ko, vo, dev_status=status)
+        assert ms.read_status(status) == ms.STATUS_BAD_SLOT and not ko[1].any() and ko[2].any()
+    empty = torch.empty(0, H_kv, D, dtype=torch.bfloat16, device="cuda")
+    ms.kv_read_q4(pool, _i32(torch, [0]), empty, empty)
+
+
+# ---------------------------------------------------------------------------- metadata from lengths
+
+def _meta_case(rng, R, max_c, max_d, p_idle=0.1):
+    c = rng.integers(0, max_c + 1, R)
+    d = np.where(rng.random(R) < 0.6, 1, rng.integers(0, max_d + 1, R))
+    d[rng.random(R) < p_idle] = 0
+    return c, d
+
+
+class Meta:
+    """Buffers and one call of build_batch_metadata_device; outputs start at a value no call writes."""
+
+    def __init__(self, env, c, d, stride, cap, ragged, alloc, bt_stride=None, cap_pages=None, num_pages=None, count=None,
+                 seed=0, alias=False):
+        self.torch, self.ms, _ = env
+        torch = self.torch
+        R = len(c)
+        rng = np.random.default_rng(seed)
+        held = -(-np.asarray(c, dtype=np.int64) // 16)
+        need = np.where(np.asarray(d) > 0, -(-(np.asarray(c, dtype=np.int64) + d) // 16), 0)
+        total = int(held.sum() + np.maximum(need - held, 0).sum())
+        self.num_pages = total + 10 if num_pages is None else num_pages
+        ids = rng.permutation(max(self.num_pages, total + 10))
+        self.tab = np.full((R, stride), -7, dtype=np.int64)
+        at = 0
+        for s in range(R):
+            n = min(stride, int(held[s] if alloc else max(held[s], need[s])))
+            self.tab[s, :n] = ids[at:at + n]
+            at += n
+        self.free = ids[at:] if alloc else None
+        self.count = (len(self.free) if count is None else count) if alloc else 0
+        E = lambda *n: torch.full(n, -99, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.c, self.d = _i32(torch, c), _i32(torch, d)
+        self.tables = _i32(torch, self.tab)
+        self.out = {"cu_seqlens_q": E(R + 1), "q_start_pos": E(R), "context_lens": E(R), "positions": E(cap),
+                    "slot_mapping": E(cap)}
+        if ragged:
+            self.out["bt_offsets"] = E(R + 1)
+            self.out["bt_pages"] = E(max(int(need.sum()) if cap_pages is None else cap_pages, 1))
+        else:
+            self.out["block_tables"] = E(R, stride if bt_stride is None else bt_stride)
+        self.kw = {}
+        if alloc:
+            self.state = torch.tensor([self.count, 0], dtype=torch.int32, device="cuda")
+            fc = self.state[:1] if alias else torch.tensor([self.count], dtype=torch.int32, device="cuda")
+            if not alias:
+                self.state[0] = -5
+            self.kw = dict(free_pages=_i32(torch, self.free), free_count=fc, free_state=self.state)
+        self.info = E(4)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(self, stream=None):
+        self.ms.build_batch_metadata_device(self.c, self.d, self.tables, self.num_pages, **self.out, info=self.info,
+                                            dev_status=self.status, stream=stream, **self.kw)
+
+    def check(self, flag=0):
+        assert self.ms.read_status(self.status) == flag
+        c, d = self.c.cpu().numpy(), self.d.cpu().numpy()
+        cap = self.out["positions"].numel()
+        ref = oracle.metadata_from_lengths(c, d, self.tab, cap, self.free, self.count)
+        for k in ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping"):
+            np.testing.assert_array_equal(self.out[k].cpu().numpy(), ref[k], err_msg=k)
+        if "bt_offsets" in self.out:
+            np.testing.assert_array_equal(self.out["bt_offsets"].cpu().numpy(), ref["bt_offsets"])
+            n = len(ref["bt_pages"])
+            np.testing.assert_array_equal(self.out["bt_pages"][:n].cpu().numpy(), ref["bt_pages"])
+            assert (self.out["bt_pages"][n:] == -99).all()
+        else:
+            bt = self.out["block_tables"].cpu().numpy()
+            for s in range(len(c)):
+                row = ref["bt_pages"][ref["bt_offsets"][s]:ref["bt_offsets"][s + 1]]
+                np.testing.assert_array_equal(bt[s], row + [-1] * (bt.shape[1] - len(row)))
+        np.testing.assert_array_equal(self.tables.cpu().numpy(), ref["tables"])
+        assert self.info.tolist() == ref["info"]
+        if self.free is not None:
+            assert self.state.tolist() == [ref["free_count"], 0]
+
+    def check_refused(self, flag):
+        """The step became one of pad rows; no page was taken."""
+        assert self.ms.read_status(self.status) == flag
+        for k in ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "bt_offsets"):
+            assert k not in self.out or not self.out[k].any(), k
+        assert (self.out["slot_mapping"] == -1).all()
+        if "block_tables" in self.out:
+            assert (self.out["block_tables"] == -1).all()
+        else:
+            assert (self.out["bt_pages"] == -99).all()
+        np.testing.assert_array_equal(self.tables.cpu().numpy(), self.tab)
+        assert self.info.tolist() == [0, 0, 0, 0]
+        if self.free is not None:
+            assert self.state.tolist() == [self.count, 0]
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("alloc", [False, True])
+@pytest.mark.parametrize("R,max_c,max_d", [(1, 40, 20), (3, 0, 5), (33, 300, 40), (511, 700, 3), (513, 64, 900),
+                                           (8192, 100, 2)])
+def test_metadata(env, R, max_c, max_d, alloc, ragged):
+    rng = np.random.default_rng(R + max_c)
+    c, d = _meta_case(rng, R, max_c, max_d)
+    if R == 1:
+        d[:] = max_d
+    stride = -(-(max_c + max_d + 16) // 16)
+    m = Meta(env, c, d, stride, int(d.sum()) + 13, ragged, alloc, seed=R, alias=R % 2 == 0)
+    m.call()
+    m.check()
+
+
+def test_metadata_long_rows_and_exact_capacities(env):
+    """Rows of 130000 tokens, a chunk of 9000, capacities with nothing to spare and a free list used up."""
+    c, d = np.array([130000, 0, 131071, 16, 15]), np.array([1, 9000, 1, 1, 1])
+    for ragged in (False, True):
+        m = Meta(env, c, d, 8192, int(d.sum()), ragged, True, count=1 + 563 + 1, seed=5)
+        m.free = m.free[:m.count]
+        m.call()
+        m.check()
+
+
+def test_metadata_idle_rows_only(env):
+    for alloc in (False, True):
+        m = Meta(env, [100, 0, 7], [0, 0, 0], 8, 5, False, alloc)
+        m.call()
+        m.check()
+        m = Meta(env, [100, 0, 7], [0, 0, 0], 8, 5, True, alloc, cap_pages=4)
+        m.call()
+        m.check()
+
+
+def test_metadata_refusals_on_the_device(env):
+    torch, ms, _ = env
+    META, NOPG = ms.STATUS_BAD_META, ms.STATUS_NO_PAGES
+    for ragged in (False, True):
+        for c, d, kw, flag in (([5, -1], [1, 1], {}, META), ([5, 6], [1, -3], {}, META),
+                               ([2 ** 31 - 1, 6], [1, 1], {}, META), ([5, 6], [9, 9], dict(cap=17), META),
+                               ([5, 200], [1, 1], dict(stride=12, bt_stride=32), NOPG),
+                               ([5, 2 ** 31 - 2], [1, 1], {}, META | NOPG),
+                               ([16, 32, 48], [1, 1, 1], dict(alloc=True, count=2), NOPG),
+                               ([16, 32, 48], [1, 1, 1], dict(alloc=True, count=-1), META | NOPG),
+                               ([16, 32, 48], [1, 1, 1], dict(alloc=True, count=100000), META),
+                               ([5, 40], [1, 1], dict(bt_stride=2, cap_pages=3), META)):
+            small = [min(max(x, 0), 300) for x in c]
+            m = Meta(env, small, d, kw.get("stride", 32), kw.get("cap", 24), ragged, kw.get("alloc", False),
+                     bt_stride=kw.get("bt_stride"), cap_pages=kw.get("cap_pages", 30), count=kw.get("count"))
+            if kw.get("alloc"):
+                m.state[0] = m.count
+            m.c = _i32(torch, c)
+            m.call()
+            m.check_refused(flag)
+
+
+def test_metadata_bad_page_gets_no_slot(env):
+    torch, ms, _ = env
+    m = Meta(env, [20, 3, 40], [1, 14, 2], 4, 20, False, False)
+    m.tables[1, 1] = m.num_pages
+    m.call()
+    assert ms.read_status(m.status) == ms.STATUS_BAD_PAGE
+    slots = m.out["slot_mapping"].tolist()
+    assert slots[14] == -1 and min(slots[:14]) >= 0 and min(slots[15:17]) >= 0
+
+
+def test_metadata_replayed_as_the_lengths_grow(env):
+    """One captured call replayed token by token: pages come from the free list as rows cross page ends."""
+    torch, ms, _ = env
+    c0, d = np.array([14, 31, 0, 47]), np.array([1, 1, 1, 0])
+    m = Meta(env, c0, d, 8, 4, True, True, cap_pages=20, alias=True, seed=3)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        m.call()
+        m.c += m.d
+    for n in range(40):
+        m.out["bt_pages"].fill_(-99)
+        graph.replay()
+        torch.cuda.synchronize()
+        m.c -= m.d  # check() reads the lengths that the call saw
+        m.check()
+        m.c += m.d
+        m.tab, m.count = m.tables.cpu().numpy().astype(np.int64), int(m.state[0])
+
+
+# ---------------------------------------------------------------------------- attention
+
+def _pool(torch, pages, H_kv, D, seed, sigma=1.0):
+    """A pool of rows that the append could have written (random codes -7..7, scales of five bits), and its values."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    NG = D // 32
+    x = torch.randn(pages, H_kv, 2, 16 * D, generator=g, device="cuda") * 2.6 + 8
+    nib = x.round().clamp(1, 15).to(torch.uint8)
+    codes = nib[..., 0::2] | (nib[..., 1::2] << 4)
+    s = torch.rand(pages, H_kv, 2, 16 * NG, generator=g, device="cuda") * 0.3 + 0.15
+    u = (s * sigma).view(torch.int32) & ~0x7FFFF
+    sc = u.view(torch.float32).to(torch.bfloat16).view(torch.uint8)
+    return torch.cat([codes.reshape(pages, H_kv, -1), sc.reshape(pages, H_kv, -1)], -1).contiguous()
+
+
+def _values(torch, pool, D):
+    """K and V values [pages, H, 16, D] of a pool (fp64, GPU), by the oracle's nibble places."""
+    from oracle.q4 import nibble_index
+    out = []
+    NG = D // 32
+    for w in (0, 1):
+        b = pool[..., w * 8 * D:(w + 1) * 8 * D].reshape(*pool.shape[:2], 16, D // 2)
+        n = torch.tensor([nibble_index(D, d, w == 1) for d in range(D)], device="cuda")
+        code = ((b[..., n // 2].int() >> (4 * (n % 2))) & 15).double() - 8
+        sc = pool[..., 16 * D + w * 32 * NG:16 * D + (w + 1) * 32 * NG].contiguous().view(torch.bfloat16).double()
+        out.append(code * sc.view(*pool.shape[:2], 16, NG).repeat_interleave(32, -1))
+    return out
+
+
+class Attn:
+    def __init__(self, env, rows, H_q, H_kv, D, seed=0, ragged=False, sigma=1.0, qscale=1.0, slack_tokens=0, extra_stride=0,
+                 pool=None):
+        torch, ms, step = env
+        self.torch, self.ms = torch, ms
+        self.rows, self.H_q, self.H_kv, self.D, self.ragged = rows, H_q, H_kv, D, ragged
+        rng = np.random.default_rng(seed)
+        need = [-(-(c + d) // 16) for c, d in rows]
+        total = max(sum(need), 1)
+        self.pool = _pool(torch, total + 2, H_kv, D, seed, sigma) if pool is None else pool
+        ids = rng.permutation(total + 2)
+        self.pages, at = [], 0
+        for n in need:
+            self.pages.append(ids[at:at + n])
+            at += n
+        S = len(rows)
+        stride = max(max(need), 1) + extra_stride
+        bt = np.full((S, stride), -1)
+        for s, pg in enumerate(self.pages):
+            bt[s, :len(pg)] = pg
+        cu = np.concatenate([[0], np.cumsum([d for _, d in rows])])
+        self.T = int(cu[-1])
+        self.bt = _i32(torch, bt)
+        self.off = _i32(torch, np.concatenate([[0], np.cumsum(need)]))
+        self.bt_pages = _i32(torch, np.concatenate(self.pages) if sum(need) else [0])
+        self.cu, self.cun = _i32(torch, cu), cu
+        self.start = _i32(torch, [c for c, _ in rows])
+        self.ctx = _i32(torch, [c + d for c, d in rows])
+        self.total = sum(c + d for c, d in rows)
+        g = torch.Generator(device="cuda").manual_seed(seed + 1)
+        n = self.T + slack_tokens
+        self.q = (torch.randn(n, H_q, D, generator=g, device="cuda") * qscale).to(torch.bfloat16)
+        self.out = torch.full((n, H_q, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        w = ms.attention_workspace_size(S, n, self.total, H_q, H_kv, D)
+        self.ws = torch.zeros(w, dtype=torch.uint8, device="cuda")
+
+    def call(self, scale=None, stream=None, out=None, ws=None):
+        self.ms.mixed_step_attention_q4(self.q, self.pool, self.cu, self.start, self.ctx,
+                                        self.bt_pages if self.ragged else self.bt, self.total,
+                                        self.out if out is None else out, self.ws if ws is None else ws,
+                                        bt_offsets=self.off if self.ragged else None, scale=scale, stream=stream)
+
+    def reference(self, scale=None):
+        """Per token and head in 64 bits: softmax(scale q K) V, and the sum A of p |v|."""
+        torch = self.torch
+        scale = self.D ** -0.5 if scale is None else scale
+        G = self.H_q // self.H_kv
+        ref = torch.zeros(self.T, self.H_q, self.D, dtype=torch.float64, device="cuda")
+        A = torch.zeros_like(ref)
+        for s, (c, d) in enumerate(self.rows):
+            if d == 0:
+                continue
+            pg = torch.tensor(np.asarray(self.pages[s]), device="cuda")
+            K, V = (x.permute(1, 0, 2, 3).reshape(self.H_kv, -1, self.D)[:, :c + d]
+                    for x in _values(torch, self.pool[pg], self.D))
+            q = self.q[self.cun[s]:self.cun[s + 1]].double().view(d, self.H_kv, G, self.D).permute(1, 2, 0, 3)
+            z = torch.einsum("hgtd,hnd->hgtn", q, K) * scale
+            seen = torch.arange(c + d, device="cuda")[None] <= c + torch.arange(d, device="cuda")[:, None]
+            p = torch.softmax(z.masked_fill(~seen, -float("inf")), -1)
+            for dst, x in ((ref, V), (A, V.abs())):
+                dst[self.cun[s]:self.cun[s + 1]] = torch.einsum("hgtn,hnd->thgd", p, x).reshape(d, self.H_q, self.D)
+        return ref, A
+
+    def check(self, scale=None, out=None):
+        torch = self.torch
+        assert self.ms.read_status(self.ws) == 0
+        out = self.out if out is None else out
+        ref, A = self.reference(scale)
+        got = out[:self.T].double()
+        assert torch.isfinite(got).all()
+        err, bound = (got - ref).abs(), 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -10) * A + 1e-30
+        worst = (err / bound).max().item() if self.T else 0.0
+        assert worst <= 1, worst
+        assert (out[self.T:] == 5.0).all()
+        return worst
+
+
+SHAPES = [(4, 2, 64), (3, 3, 64), (8, 1, 64), (4, 1, 64), (2, 2, 128), (4, 2, 128), (8, 2, 128), (8, 1, 128), (16, 2, 128)]
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", SHAPES)
+@pytest.mark.parametrize("ragged", [False, True])
+def test_decode_rows(env, H_q, H_kv, D, ragged):
+    """Contexts on both sides of every page and window end, from a single key to several thousand."""
+    ctx = [0, 1, 14, 15, 16, 17, 30, 31, 32, 47, 63, 64, 65, 127, 255, 256, 511, 512, 513, 700, 1023, 2047, 4097, 6000]
+    a = Attn(env, [(c, 1) for c in ctx], H_q, H_kv, D, seed=D + H_q, ragged=ragged)
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", SHAPES)
+def test_chunk_rows(env, H_q, H_kv, D):
+    """Chunks of 2 tokens up, at page-aligned and odd offsets, one alone longer than a pair of query tiles."""
+    a = Attn(env, [(0, 2), (1, 3), (15, 2), (16, 16), (63, 65), (64, 64), (130, 33), (0, 300), (777, 129), (1000, 513)], H_q,
+             H_kv, D, seed=D + H_q)
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,seed", [(8, 2, 128, 1), (4, 4, 64, 2), (8, 1, 64, 3), (32, 8, 128, 4)])
+def test_mixed_rows_with_pads(env, H_q, H_kv, D, seed):
+    """Decodes, chunks and rows without tokens, in any order; tokens that no row covers stay as they were."""
+    rng = np.random.default_rng(seed)
+    rows = []
+    for _ in range(40):
+        c = int(rng.integers(0, 3000))
+        rows.append((c, int(rng.choice([0, 1, 1, 1, int(rng.integers(2, 150))]))))
+    for ragged in (False, True):
+        a = Attn(env, rows, H_q, H_kv, D, seed=seed, ragged=ragged, slack_tokens=9, extra_stride=3)
+        a.call()
+        a.check()
+
+
+def test_many_rows(env):
+    """8192 rows, and rows of one key."""
+    rng = np.random.default_rng(9)
+    a = Attn(env, [(int(c), 1) for c in rng.integers(0, 40, 8192)], 2, 1, 64, seed=9)
+    a.call()
+    a.check()
+
+
+def test_long_decode_row(env):
+    """One row of 131072 keys: many splits, joined at the end."""
+    a = Attn(env, [(131071, 1), (3, 1)], 4, 1, 128, seed=10, ragged=True)
+    a.call()
+    a.check()
+
+
+@pytest.mark.parametrize("qscale,sigma,scale", [(30.0, 1.0, None), (1.0, 1e-4, None), (1.0, 2.0 ** 14, 2.0 ** -18), (0.0, 1.0, None)])
+def test_sharp_and_flat_scores(env, qscale, sigma, scale):
+    """Scores in the hundreds, and all equal; cached values far below and above one."""
+    for D in (64, 128):
+        a = Attn(env, [(900, 1), (5, 1), (300, 140), (0, 20)], 8, 2, D, seed=11, qscale=qscale, sigma=sigma)
+        a.call(scale=scale)
+        if qscale > 1:  # the scores' own fp32 error grows with them: 2^-22 * 136 * sum |q| * s * scale
+            assert a.ms.read_status(a.ws) == 0
+            ref, A = a.reference(scale)
+            e_s = 2 * 2.0 ** -22 * 136 * qscale * D * 0.8 * 0.45 * D ** -0.5
+            bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -10 + 2 * e_s) * A
+            assert ((a.out.double() - ref).abs() <= bound).all()
+        else:
+            a.check(scale=scale)
+
+
+def test_stale_bytes_past_the_context_are_not_read_as_values(env):
+    """Every slot past a row's context holds code -8 and a NaN scale; so does every page of the pool that no row owns."""
+    torch, ms, _ = env
+    for D, H_q, H_kv in ((64, 4, 2), (128, 8, 2), (128, 2, 2)):
+        a = Attn(env, [(0, 1), (16, 1), (37, 1), (600, 1), (100, 5), (200, 150), (3, 2)], H_q, H_kv, D, seed=12)
+        ref_pool = a.pool.clone()
+        NG = D // 32
+        live = torch.zeros(a.pool.shape[0], 16, dtype=torch.bool, device="cuda")
+        for s, (c, d) in enumerate(a.rows):
+            for i, pg in enumerate(a.pages[s]):
+                live[int(pg), :min(16, c + d - 16 * i)] = True
+        p = a.pool
+        for off, w in ((0, D // 2), (8 * D, D // 2)):
+            v = p[..., off:off + 16 * w].reshape(*p.shape[:2], 16, w)
+            v[~live[:, None].expand(-1, H_kv, -1)] = 0
+            p[..., off:off + 16 * w] = v.reshape(*p.shape[:2], -1)
+        for off in (16 * D, 16 * D + 32 * NG):
+            v = p[..., off:off + 32 * NG].reshape(*p.shape[:2], 16, 2 * NG)
+            v[~live[:, None].expand(-1, H_kv, -1)] = 0xFF
+            p[..., off:off + 32 * NG] = v.reshape(*p.shape[:2], -1)
+        a.call()
+        got = a.out.clone()
+        assert torch.isfinite(got.float()).all()
+        a.pool = ref_pool
+        a.check()
+
+
+def test_bad_pages_and_bad_metadata(env):
+    torch, ms, _ = env
+    for bad in (-1, 10 ** 6):
+        a = Attn(env, [(100, 1), (40, 1), (100, 30)], 4, 2, 128, seed=13)
+        for s in (0, 2):
+            a.bt[s, 2] = bad
+        a.call()
+        assert ms.read_status(a.ws) == ms.STATUS_BAD_PAGE
+        ref, A = a.reference()
+        assert ((a.out[1].double() - ref[1]).abs() <= 2.0 ** -7 * A[1] + 2.0 ** -7 * ref[1].abs()).all()
+    for field, row, value in (("ctx", 0, 7), ("start", 1, -1), ("cu", 1, 5000), ("ctx", 2, 2 ** 31 - 1)):
+        a = Attn(env, [(100, 1), (40, 1), (100, 30)], 4, 2, 64, seed=14)
+        getattr(a, field)[row] = value
+        a.call()
+        assert ms.read_status(a.ws) == ms.STATUS_BAD_META
+    # a good call on the same workspace afterwards
+    b = Attn(env, [(100, 1), (40, 1), (100, 30)], 4, 2, 64, seed=14)
+    b.ws = a.ws
+    b.call()
+    b.check()
+
+
+def test_page_ids_past_32_bit_offsets(env):
+    """A pool of more than 4 GB: the last pages' byte offsets do not fit in 32 bits."""
+    torch, ms, _ = env
+    D, H_kv = 128, 8
+    pages = (1 << 32) // (H_kv * 18 * D) + 200
+    pool = torch.zeros(pages, H_kv, 18 * D, dtype=torch.uint8, device="cuda")
+    few = _pool(torch, 64, H_kv, D, 15)
+    a = Attn(env, [(500, 1), (200, 90)], 32, H_kv, D, seed=15, pool=few)
+    a.pages = [pg + pages - 64 for pg in a.pages]
+    a.bt = torch.where(a.bt >= 0, a.bt + pages - 64, a.bt)
+    pool[-64:] = few
+    a.pool = pool
+    a.call()
+    a.check()
+    # and the append and the read-back there
+    slots = np.array([16 * pages - 1, 16 * pages - 37])
+    q, k, v = (torch.randn(2, H, D, device="cuda").to(torch.bfloat16) for H in (8, 8, 8))
+    _, status = _append(env, q, k, v, [3, 4], slots, pool, 8)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    ms.kv_read_q4(pool, _i32(torch, slots), ko, vo)
+    assert status == 0
+    np.testing.assert_array_equal(oracle.bf16_to_f64(workloads.bf16_bits(vo)),
+                                  oracle.q4_values(oracle.bf16_to_f64(workloads.bf16_bits(v))))
+
+
+def test_repeat_stream_and_replay_give_the_same_bits(env):
+    """The same call again, on another stream, and captured and replayed, on workspaces of their own."""
+    torch, ms, _ = env
+    a = Attn(env, [(3000, 1), (64, 1), (500, 200), (8000, 1)], 8, 2, 128, seed=16)
+    a.call()
+    torch.cuda.synchronize()
+    first = a.out.clone()
+    a.check()
+    side, ws2, out2 = torch.cuda.Stream(), torch.zeros_like(a.ws), torch.empty_like(a.out)
+    side.wait_stream(torch.cuda.current_stream())
+    a.call(stream=side, ws=ws2, out=out2)
+    side.synchronize()
+    assert torch.equal(out2, first)
+    graph, ws3, out3 = torch.cuda.CUDAGraph(), torch.zeros_like(a.ws), torch.empty_like(a.out)
+    with torch.cuda.graph(graph, stream=side):
+        a.call(ws=ws3, out=out3)
+    for _ in range(3):
+        out3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out3, first)
+
+
+# ---------------------------------------------------------------------------- together
+
+def test_decode_loop_captured_whole(env):
+    """Metadata from lengths, append, attention: captured once, replayed for 40 tokens with no host data in between.
+    Every step's cache bytes are the oracle's, and its outputs those of 64-bit attention over them."""
+    torch, ms, step = env
+    H_q, H_kv, D, R, pages, stride = 8, 2, 64, 5, 64, 12
+    c0 = [0, 13, 16, 40, 0]
+    new = [1, 1, 1, 1, 0]  # the last request is idle
+    ids = list(range(pages))
+    tab = np.full((R, stride), -1)
+    for s, c in enumerate(c0):
+        for j in range(-(-c // 16)):
+            tab[s, j] = ids.pop(0)
+    pool = _pool(torch, pages, H_kv, D, 17)
+    ref_pool = pool.cpu().numpy().copy()
+    c, d, tables = _i32(torch, c0), _i32(torch, new), _i32(torch, tab)
+    E = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    cap = 8
+    cu, start, ctx, positions, slots = E(R + 1), E(R), E(R), E(cap), E(cap)
+    bt, info, status = E(R, stride), E(4), E(1)
+    free = _i32(torch, ids)
+    state = torch.tensor([len(ids), 0], dtype=torch.int32, device="cuda")
+    cos, sin = step.rope_tables_device(16 * stride, D, "cuda")
+    q, k, v = (torch.zeros(cap, H, D, dtype=torch.bfloat16, device="cuda") for H in (H_q, H_kv, H_kv))
+    q_rot, out = torch.zeros_like(q), torch.zeros_like(q)
+    ws = torch.zeros(ms.attention_workspace_size(R, cap, 16 * pages, H_q, H_kv, D), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+
+    def one_step():
+        ms.build_batch_metadata_device(c, d, tables, pages, cu, start, ctx, positions, slots, block_tables=bt,
+                                       free_pages=free, free_count=state[:1], free_state=state, info=info,
+                                       dev_status=status)
+        ms.kv_append_rope_q4(q, k, v, positions, slots, cos, sin, pool, q_rot=q_rot, dev_status=status)
+        ms.mixed_step_attention_q4(q_rot, pool, cu, start, ctx, bt, 16 * pages, out, ws)
+        c.add_(d)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        one_step()
+    host_tab, host_c, count = tab.astype(np.int64), np.array(c0), len(ids)
+    for n in range(40):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ms.read_status(status) == 0 and ms.read_status(ws) == 0
+        m = oracle.metadata_from_lengths(host_c, new, host_tab, cap, free=ids, count=count)
+        host_tab, count = m["tables"], m["free_count"]
+        np.testing.assert_array_equal(slots.tolist(), m["slot_mapping"])
+        np.testing.assert_array_equal(tables.cpu().numpy(), host_tab)
+        ok = [s >= 0 for s in m["slot_mapping"]]
+        ref_pool, qr = _oracle_append(q, k, v, np.array(m["positions"]), m["slot_mapping"], ref_pool, ok)
+        np.testing.assert_array_equal(workloads.bf16_bits(q_rot)[:4], qr[:4])
+        np.testing.assert_array_equal(pool.cpu().numpy(), ref_pool)
+        a = Attn(env, [(int(x), y) for x, y in zip(host_c, new)], H_q, H_kv, D, pool=pool, slack_tokens=4)
+        a.pages = [host_tab[s, :-(-int(x + y) // 16)] if y else [] for s, (x, y) in enumerate(zip(host_c, new))]
+        a.q, a.T, a.ws = q_rot, 4, ws
+        a.out = torch.cat([out[:4], torch.full_like(out[:4], 5.0)])
+        a.check()
+        host_c = host_c + new
+    assert state.tolist() == [count, 0] and c.tolist() == list(host_c)
