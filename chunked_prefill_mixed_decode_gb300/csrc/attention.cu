@@ -39,11 +39,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
-#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>

@@ -83,6 +83,7 @@ struct AttnParams {
   int2* ch_items;   // per chunk item: (chunk row index, KV head << 16 | Q-tile pair counted from the last)
   // the attention kernel's alone
   const bf16* q_rot;
+  const uint8_t* kv_q4;   // 4-bit pool (q4.cuh), in the calls that take one
   const int32_t* bt;      // padded rows of bt_stride entries, or (bt_off given) every row's pages back to back
   bf16* out;
   float* part_ml;
@@ -914,6 +915,7 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.wait_limit_ns = stall_limit_ns > 0 ? static_cast<uint64_t>(stall_limit_ns) : 2000000000ull;
   p.scale_log2 = scale * 1.4426950408889634f;
 
+  p.kv_q4 = nullptr;
   p.force_chunk_ctas = -1;
   if (device_rates(&p.sm_mhz, &p.hbm_gbs, &p.l2_bytes) != MS_OK) return MS_ERR_CUDA;
   return MS_OK;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attention_step.cuh"
+#include "q4.cuh"
 
 namespace {
 
@@ -62,6 +63,148 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return ok != 0;
 }
 
+// ---- 4-bit pools: K and V tiles by warps instead of TMA
+
+constexpr int kDequantWarps = kTilePages;            // one per page of a tile
+constexpr int kDequantWarp0 = 4 + kSoftmaxWarps;     // warps 12-15
+
+// One lane's share of one page: two rows of K and of V (quarter t of each
+// group), and those rows' scales.
+template <int D>
+struct Q4Rows {
+  static constexpr int NG = Q4<D>::NG;
+  uint32_t k[2][NG], v[2][NG], ks[2][NG / 2], vs[2][NG / 2];
+};
+
+template <int N>
+__device__ __forceinline__ void ldg_words(const uint8_t* src, uint32_t* dst) {
+  if constexpr (N == 4) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+    dst[0] = x.x; dst[1] = x.y; dst[2] = x.z; dst[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    dst[0] = x.x; dst[1] = x.y;
+  } else {
+    dst[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  }
+}
+
+// Quarter t of one row (a word per group) as bf16 into a 128-byte-swizzled
+// tile: group g's eight elements are 16-byte chunk 4 g + t of the row, in slab
+// g / 2.
+template <int D, int SLAB>
+__device__ __forceinline__ void store_row_part(uint32_t row_addr, int key, int t, const uint32_t* words,
+                                               const uint32_t* scales) {
+  constexpr int NG = Q4<D>::NG;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const uint32_t s2 = __byte_perm(scales[g >> 1], 0, (g & 1) ? 0x3232 : 0x1010);
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = q4_scaled_pair(words[g], i, s2);
+    const uint32_t dst = row_addr + (g >> 1) * SLAB + ((((g & 1) * 4 + t) ^ (key & 7)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                 : "memory");
+  }
+}
+
+// Warp 12 + w fills page w of every K and V tile of the CTA's items.  Four
+// lanes share a row (16 bytes of codes each at D = 128); the eight lanes of one
+// 16-byte store wave hold rows r and r + 4, whose chunks land in different
+// halves of the 128-byte line, so the stores do not conflict.  Rows past the
+// row's context are written as zeros.  Returns false when a wait gave up.
+template <int D>
+__device__ __forceinline__ bool dequant_role(const AttnParams& p, uint8_t* smem, ChBars* bars,
+                                             const volatile int* abort_flag, uint64_t lim) {
+  using C = ChCfg<D>;
+  using Q = Q4<D>;
+  constexpr int NSL = C::NSL, NG = Q::NG, KVS = C::KVS;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDequantWarp0;
+  const int t = lane & 3, y = lane >> 2;
+  const int r0 = ((y & 1) << 2) | (y >> 1);  // and r0 + 8
+  const uint32_t sbase = smem_u32(smem);
+  int bk = 0;        // stage of the next tile
+  uint32_t ph = 0;   // parity of the stage's last release
+  bool first = true; // the stages' first round: nothing to wait for
+  for (int n = 0;; ++n) {
+    const int slot = n & 1;
+    if (!warp_wait(&bars->item_full[slot], (n >> 1) & 1, abort_flag, lim)) return false;
+    const ChItem& it = bars->items[slot];  // stable until this role arrives on item_empty
+    const int row = it.row;
+    if (row < 0) return true;
+    const int n_kt = it.n_kt, kv_max = max(it.kv_end[0], it.kv_end[1]);
+    const int n_pages = (kv_max + kPage - 1) / kPage;
+    const int32_t* btrow = row_table(p, row);
+    const uint8_t* pool = p.kv_q4 + static_cast<int64_t>(it.hk) * Q::BYTES;
+    const int64_t page_bytes = static_cast<int64_t>(p.H_kv) * Q::BYTES;
+    auto page_id = [&](int kt) { return kt * kTilePages + w < n_pages ? __ldg(btrow + kt * kTilePages + w) : 0; };
+    auto load = [&](int phys, Q4Rows<D>& x) {
+      if (phys < 0 || phys >= p.num_pages) {
+        if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
+        phys = 0;
+      }
+      const uint8_t* blk = pool + phys * page_bytes;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        ldg_words<NG>(blk + r * Q::ROW + t * 4 * NG, x.k[i]);
+        ldg_words<NG>(blk + Q::V_OFF + r * Q::ROW + t * 4 * NG, x.v[i]);
+        ldg_words<NG / 2>(blk + Q::KS_OFF + r * NG * 2, x.ks[i]);
+        ldg_words<NG / 2>(blk + Q::VS_OFF + r * NG * 2, x.vs[i]);
+      }
+    };
+    Q4Rows<D> cur, nxt;
+    load(page_id(0), cur);
+    int id_next = page_id(1);
+    for (int kt = 0; kt < n_kt; ++kt) {
+      if (kt + 1 < n_kt) load(id_next, nxt);
+      id_next = page_id(kt + 2);
+      const int keys = kv_max - kt * kKeys - w * kPage;  // of this page
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (r0 + 8 * i >= keys) {  // past the context: scales of zero (the codes are finite whatever they hold)
+#pragma unroll
+          for (int j = 0; j < NG / 2; ++j) cur.ks[i][j] = cur.vs[i][j] = 0u;
+        }
+      if (!first && !warp_wait(&bars->k_empty[bk], ph, abort_flag, lim)) return false;
+      if (keys > 0) {
+        const uint32_t kbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + w * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + 8 * i;
+          store_row_part<D, kKVSlab>(kbase + r * 128, r, t, cur.k[i], cur.ks[i]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->k_full[bk]);
+      if (!first && !warp_wait(&bars->v_empty[bk], ph, abort_flag, lim)) return false;
+      if (keys > 0) {
+        const uint32_t vbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + NSL * kKVSlab + w * NSL * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + 8 * i;
+          uint32_t words[NG];  // even elements (first half of the bytes) below odd ones, group by group
+#pragma unroll
+          for (int g = 0; g < NG; ++g) words[g] = join_halves(cur.v[i][g >> 1], cur.v[i][NG / 2 + (g >> 1)], g & 1);
+          store_row_part<D, 2048>(vbase + r * 128, r, t, words, cur.vs[i]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->v_full[bk]);
+      cur = nxt;
+      if (++bk == KVS) {
+        bk = 0;
+        ph = first ? 0u : ph ^ 1u;
+        first = false;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[slot]);
+  }
+}
+
 // Chunk phase.  Warp 0 owns the work queue and streams Q and K/V with TMA (K
 // one tile ahead of V); warps 2-5 and 6-9 are two softmax groups, group t
 // owning Q tile t of the current pair, one query row per thread over 64-key
@@ -74,7 +217,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 // The two groups run a tile apart at most, so one group's exponentials
 // overlap the other group's MMAs.  Returns when the chunk queue is empty; the
 // caller owns TMEM and the barrier invalidation.
-template <int D, int G>
+//
+// Over a 4-bit pool (Q4) four more warps, 12-15, stand in for the TMA stream of
+// K and V: warp 12 + w reads page w of each tile straight from the pool into
+// registers, a tile ahead, and writes its values -- exactly bf16, so nothing
+// else of the phase changes -- into the same stages.
+template <int D, int G, bool Q4 = false>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
                                             const AttnParams& p, uint8_t* smem, uint32_t tmem) {
@@ -103,9 +251,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 2);  // one commit per S issuer
     for (int b = 0; b < 8; ++b) {  // all of them, so that all can be invalidated
-      mbar_init(&bars->k_full[b], 1);
+      mbar_init(&bars->k_full[b], Q4 ? kDequantWarps : 1);
       mbar_init(&bars->k_empty[b], 2);
-      mbar_init(&bars->v_full[b], 1);
+      mbar_init(&bars->v_full[b], Q4 ? kDequantWarps : 1);
       mbar_init(&bars->v_empty[b], 1);
     }
     for (int t = 0; t < 2; ++t)
@@ -116,7 +264,8 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->item_full[b], 1);
-      mbar_init(&bars->item_empty[b], 3 + 32 * kSoftmaxWarps);  // MMA issuers, softmax threads
+      // MMA issuers, softmax threads, dequantizing warps
+      mbar_init(&bars->item_empty[b], 3 + 32 * kSoftmaxWarps + (Q4 ? kDequantWarps : 0));
     }
     for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
     bars->abort = 0;
@@ -134,8 +283,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     // slab L % NSL; its V boxes likewise, one per page (lanes with slab 0).
     if (lane == 0) {
       prefetch_tmap(&tm_q);
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(NSL == 2 ? &tm_vp : &tm_v);
+      if constexpr (!Q4) {
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(NSL == 2 ? &tm_vp : &tm_v);
+      }
     }
     const int my_pg = lane / NSL, my_s = lane % NSL;
     const bool loader = lane < kTilePages * NSL;
@@ -227,6 +378,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + s * kQSlab, &tm_q, s * 64, it.hk * G, it.tb + it.tok0[t],
                     &bars->q_full);
       }
+      if constexpr (Q4) {  // K and V come from the dequantizing warps
+        g += it.n_kt;
+        continue;
+      }
       const int kv_max = max(it.kv_end[0], it.kv_end[1]);
       const int32_t* btrow = row_table(p, it.row);
       const int n_pages = (kv_max + kPage - 1) / kPage;
@@ -275,6 +430,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     if (lane == 0) {
       if (!ok && !stalled) *abort_flag = 1;
       // copies still in flight must land before the CTA moves on
+      if constexpr (Q4) g = 0;  // none of K or V
       for (int t = (g > KVS ? g - KVS : 0); t < g; ++t)
         mbar_wait(&bars->k_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
       for (int t = (g_v > KVS ? g_v - KVS : 0); t < g_v; ++t)
@@ -385,7 +541,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             break;
           }
           const int keys = min(kKeys, kv_max - j * kKeys);  // keys loaded in this tile
-          if ((keys & 15) != 0) {
+          if (!Q4 && (keys & 15) != 0) {
             // rows past the context in the last page may hold stale (even non-finite)
             // data: zero them in V so that P = 0 times V stays 0
             uint8_t* v0 = smem + v_off(bv);
@@ -594,6 +750,11 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_TIMEOUT);
+    }
+  }
+  if constexpr (Q4) {
+    if (warp >= kDequantWarp0) {
+      if (!dequant_role<D>(p, smem, bars, abort_flag, lim)) *abort_flag = 1;
     }
   }
   (void)n_items;

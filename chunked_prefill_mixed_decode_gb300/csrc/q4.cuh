@@ -72,4 +72,34 @@ __device__ __forceinline__ uint32_t q4_nibble(float x, float s) {
   return s > 0.f ? static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x, s)) + 8) : 8u;
 }
 
+// ---- decoding
+
+// Nibbles i and i + 4 of a code word as the bf16 pair 128 + nibble (the nibble
+// lands in the low mantissa bits of 128): one shift and one three-input logic
+// instruction for two values.
+__device__ __forceinline__ uint32_t q4_pair128(uint32_t w, int i) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+  return r;
+}
+
+// The same pair as codes (nibble - 8), exact.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, int i) {
+  const uint32_t r = q4_pair128(w, i), c = 0x43084308u;  // 136
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// A pair of values, scale (twice) * code, exact.
+__device__ __forceinline__ uint32_t q4_scaled_pair(uint32_t w, int i, uint32_t s2) {
+  const uint32_t r = q4_pair(w, i);
+  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&s2));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Half h (0 low, 1 high) of `a` below the same half of `b`.
+__device__ __forceinline__ uint32_t join_halves(uint32_t a, uint32_t b, int h) {
+  return __byte_perm(a, b, h == 0 ? 0x5410 : 0x7632);
+}
+
 }  // namespace
