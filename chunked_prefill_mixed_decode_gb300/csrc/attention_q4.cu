@@ -6,7 +6,7 @@
 //   chunk rows (d > 1): chunk_phase with four more warps, which read pages and
 //     write their values into the shared-memory tiles.
 //   decode rows (d = 1): 16 worker warps, each with a private ring of pages in
-//     shared memory filled by 16-byte asynchronous copies.  A page of K and V is
+//     shared memory filled by bulk copies, one a page.  A page of K and V is
 //     2.25 KB instead of 8 KB, so the time goes into instructions rather than
 //     bytes, and the codes go into the tensor cores undecoded as far as the
 //     algebra allows.  With x the codes of a group, n = x + 8 its nibbles and s
@@ -38,22 +38,19 @@ constexpr int kQ4Threads = 32 * (kDequantWarp0 + kDequantWarps);
 constexpr float kQ4TileCycles = 5820.f;
 constexpr float kQ4DecodeBytesPerCycle = 24.f;
 
+// A worker warp's shared memory: a ring of NST stages of two pages each, and the
+// records of the items in flight (at most one per page that is).
 template <int D>
 struct DecQ4 {
   static constexpr int WARPS = kQ4Threads / 32;
-  static constexpr int NST = 4;  // ring stages per warp
-  static constexpr int STAGE = Q4<D>::BYTES;
-  static constexpr int SMEM = WARPS * NST * STAGE;
+  static constexpr int NST = 3;
+  static constexpr int PAGE = Q4<D>::BYTES;
+  static constexpr int STAGE = 2 * PAGE;
+  static constexpr int RECS = 8;  // a power of two above 2 NST
+  static constexpr int REC_OFF = WARPS * NST * STAGE;
+  static constexpr int BAR_OFF = REC_OFF + WARPS * RECS * 32;
+  static constexpr int SMEM = BAR_OFF + WARPS * NST * 8;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
@@ -65,181 +62,267 @@ __device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(dst[0]) : "r"(src) : "memory");
 }
 
-// D = A B + C with C = (c0, c1) in both row halves
-__device__ __forceinline__ void mma_16816_bf16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
-                                                    float c1) {
+// D = A B, from zero
+__device__ __forceinline__ void mma_16816_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%11,%10,%11};"
+      "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Where the pages of the work items come from: the issue side of a warp's ring.
+// Part i of a number as the sum of three bf16 (24 bits of it): the rounded
+// number, the rounded remainder, and what is left.
+__device__ __forceinline__ float bf16_part(float x, int i) {
+  for (int j = 0; j < i; ++j) x -= __bfloat162float(__float2bfloat16_rn(x));
+  return __bfloat162float(__float2bfloat16_rn(x));
+}
+
+// What the consumer needs of an item, kept in shared memory from the moment its
+// pages are asked for.
+struct __align__(16) ItemRec {
+  int tok, hk, k, part, ns, np, rem, pad;  // rem: keys from the item's first page to the row's end
+};
+
+constexpr int kNoItem = 5;  // look-ahead stage: the queue is empty
+
+// The issue side of a warp's ring.
 struct IssueCursor {
-  const int32_t* btr;  // the item's first page-table entry
-  int hk, np, next;    // KV head, pages, next page to issue
-  int ids, ids_next;   // lane j: page ids of this window of 32 pages and of the next
+  const uint8_t* base;  // the pool at the item's KV head
+  const int32_t* btr;   // the item's first page-table entry
+  int left, next;       // pages not yet asked for, pages asked for
+  int ids, ids_next;    // lane j: page ids of this window of 32 pages and of the next
 };
 
-// What the consumer needs of an item, broadcast by shuffles from the lane that
-// holds it: lane i of every warp keeps the record of item slot i.
-struct ItemRec {
-  int tok, hk, k, part, ns, np, rem;  // rem: keys from the item's first page to the row's end
-};
-
+// Decode phase: every warp is independent and pulls items (row, KV head, span
+// of pages) until the queue is empty.  It takes its pages in pairs: one wait,
+// one maximum and one vote for 32 keys.
 template <int D, int G>
-__device__ __noinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem) {
+__device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem) {
   using Q = Q4<D>;
   using C = DecQ4<D>;
   constexpr int NG = Q::NG, NST = C::NST, NK = D / 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
+  // Row of a page that MMA token gq stands for: tokens 2 and 3, and 6 and 7, trade places, so that
+  // the four rows that one load of V touches lie on both halves of the 128-byte lines
+  const int ra = gq ^ ((gq >> 1) & 1);
   const uint32_t ring = smem_u32(dsmem) + warp * NST * C::STAGE;
+  ItemRec* recs = reinterpret_cast<ItemRec*>(dsmem + C::REC_OFF) + warp * C::RECS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(dsmem + C::BAR_OFF) + warp * NST;
+  if (lane == 0) {
+    for (int i = 0; i < NST; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   const int n_items = p.hdr[H_NDEC_ITEMS];
-  const int split = p.hdr[H_SPLIT];
-  const int64_t page_bytes = static_cast<int64_t>(p.H_kv) * Q::BYTES;
 
-  // the id of the item after the one being issued is fetched one item ahead
-  auto dequeue = [&]() -> int {
-    int v = 0;
-    if (lane == 0) v = atomicAdd(p.hdr + H_DEC_CTR, 1);
-    return __shfl_sync(0xffffffffu, v, 0);
+  // The next item is looked up while the current one runs, one dependent load
+  // per step: its id (stage 0), its entry (1), its row (2), the row's lengths
+  // (3), its first page ids (4).  The loaded words sit in one register, a lane
+  // each: 0 the id, 1 and 2 the entry (decode row, piece), 3 to 5 the row and
+  // its records, 6 to 8 its context, token and first table entry.
+  int nd = 0, nids = 0, stage_n = 0;
+  auto word = [&](int i) { return __shfl_sync(0xffffffffu, nd, i); };
+  auto dequeue = [&]() {
+    if (lane == 0) nd = atomicAdd(p.hdr + H_DEC_CTR, 1);
+    stage_n = 0;
   };
-  ItemRec rec{};          // this lane's item record
-  IssueCursor iss{};
-  int n_issued = 0;       // items whose issue has begun
-  int next_id = dequeue();
-  bool more = next_id < n_items;
-  auto begin_item = [&]() {
-    const int e = next_id / p.H_kv;
-    const int2 kl = __ldg(p.dec_items + e);  // (decode row index, split within the row)
-    const int row = __ldg(p.dec_rows + kl.x);
-    const int ctx = __ldg(p.ctx_lens + row);
-    iss.hk = next_id - e * p.H_kv;
-    const int p0 = kl.y * split;
-    iss.np = min(split, (ctx + kPage - 1) / kPage - p0);
-    iss.next = 0;
-    iss.btr = row_table(p, row) + p0;
-    iss.ids = lane < iss.np ? __ldg(iss.btr + lane) : 0;
-    if (lane == (n_issued & (NST - 1))) {
-      rec.tok = __ldg(p.cu + row);
-      rec.hk = iss.hk;
-      rec.k = kl.x;
-      rec.part = __ldg(p.dec_part_base + kl.x) + kl.y * p.H_q + iss.hk * G;
-      rec.ns = __ldg(p.dec_nsplit + kl.x);
-      rec.np = iss.np;
-      rec.rem = ctx - p0 * kPage;
-    }
-    ++n_issued;
-    next_id = dequeue();
-    more = next_id < n_items;
+  auto item_pages = [&](int& p0, int& np) {
+    const int n_pages = (word(6) + kPage - 1) / kPage;
+    dec_piece(n_pages, p.hdr[H_SPLIT], p.hdr[H_GRADED], word(2), p0, np);
   };
-  // One page into stage `st`; a committed group even where nothing is left, so
-  // that the count of groups in flight stays fixed.  V's 16-byte chunks are
-  // swizzled within their 128-byte lines: the four rows that one load of the PV
-  // operand touches are two lines apart or on the same half of a line.
-  auto issue = [&](int st) {
-    if (iss.next >= iss.np && more) begin_item();
-    if (iss.next < iss.np) {
-      const int w = iss.next & 31;
-      if (w == 0) {
-        if (iss.next > 0) iss.ids = iss.ids_next;
-        const int j = iss.next + 32 + lane;
-        iss.ids_next = j < iss.np ? __ldg(iss.btr + j) : 0;
+  auto item_table = [&](int p0) -> const int32_t* {
+    const int off = word(8), row = word(3);
+    return p.bt + (p.bt_off != nullptr ? static_cast<int64_t>(off) : static_cast<int64_t>(row) * p.bt_stride) + p0;
+  };
+  auto look_ahead = [&]() {
+    if (stage_n == 0) {
+      const int id = word(0);
+      if (id >= n_items) {
+        stage_n = kNoItem;
+        return;
       }
-      int phys = __shfl_sync(0xffffffffu, iss.ids, w);
+      if (lane == 1 || lane == 2) nd = __ldg(reinterpret_cast<const int*>(p.dec_items + id / p.H_kv) + lane - 1);
+    } else if (stage_n == 1) {
+      const int k = word(1);
+      const int32_t* src = lane == 3 ? p.dec_rows : lane == 4 ? p.dec_part_base : p.dec_nsplit;
+      if (lane >= 3 && lane <= 5) nd = __ldg(src + k);
+    } else if (stage_n == 2) {
+      const int row = word(3);
+      const int32_t* src = lane == 6 ? p.ctx_lens : lane == 7 ? p.cu : p.bt_off;
+      if (lane == 6 || lane == 7 || (lane == 8 && src != nullptr)) nd = __ldg(src + row);
+    } else if (stage_n == 3) {
+      int p0, np;
+      item_pages(p0, np);
+      const int32_t* btr = item_table(p0);
+      if (lane < np) nids = __ldg(btr + lane);
+    } else {
+      return;
+    }
+    ++stage_n;
+  };
+  IssueCursor iss{};
+  int n_begun = 0;  // items whose issue has begun
+  dequeue();
+  auto begin_item = [&]() {
+    int p0, np;
+    item_pages(p0, np);
+    const int id = word(0), hk = id - id / p.H_kv * p.H_kv;
+    iss.left = np;
+    iss.next = 0;
+    iss.base = p.kv_q4 + hk * Q::BYTES;
+    iss.btr = item_table(p0);
+    iss.ids_next = nids;
+    const int tok = word(7), k = word(1), part = word(4) + word(2) * p.H_q + hk * G, ns = word(5);
+    const int rem = word(6) - p0 * kPage;
+    if (lane == 0) recs[n_begun & (C::RECS - 1)] = ItemRec{tok, hk, k, part, ns, np, rem, 0};
+    ++n_begun;
+    dequeue();
+  };
+  // The next pair of pages of an item (its last may be alone) into stage `st`,
+  // one bulk copy a page from lanes 0 and 1.
+  int in_flight = 0;
+  auto issue = [&](int st) {
+    if (iss.left == 0) {
+      while (stage_n < 4) look_ahead();
+      if (stage_n == 4) begin_item();
+    } else if (stage_n < 4) {
+      look_ahead();
+    }
+    if (iss.left == 0) return;
+    const int w = iss.next & 31, n = min(iss.left, 2);
+    if (w == 0) {
+      iss.ids = iss.ids_next;
+      iss.ids_next = lane + 32 < iss.left ? __ldg(iss.btr + iss.next + 32 + lane) : 0;
+    }
+    int phys = __shfl_sync(0xffffffffu, iss.ids, w + lane);  // lanes 0 and 1: the pair's pages
+    if (lane == 0) mbar_arrive_expect_tx(full + st, n * C::PAGE);
+    __syncwarp();
+    if (lane < n) {
       if (phys < 0 || phys >= p.num_pages) {
-        if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
+        atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
         phys = 0;
       }
-      const uint8_t* src = p.kv_q4 + phys * page_bytes + iss.hk * Q::BYTES + lane * 16;
-      const uint32_t dst = ring + st * C::STAGE;
-      constexpr int NC = Q::V_OFF / 512;  // chunks of K (and of V) per lane
-      const int sw = lane ^ (D == 128 ? (lane >> 2) & 6 : (lane >> 2) & 2);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        cp_async16(dst + lane * 16 + i * 512, src + i * 512);
-        cp_async16(dst + Q::V_OFF + sw * 16 + i * 512, src + Q::V_OFF + i * 512);
-      }
-      if (lane < (Q::BYTES - Q::KS_OFF) / 16) cp_async16(dst + Q::KS_OFF + lane * 16, src + Q::KS_OFF);
-      ++iss.next;
+      bulk_g2s(dsmem + (warp * NST + st) * C::STAGE + lane * C::PAGE,
+               iss.base + static_cast<int64_t>(phys) * p.H_kv * Q::BYTES, C::PAGE, full + st);
     }
-    cp_async_commit();
+    iss.next += n;
+    iss.left -= n;
+    ++in_flight;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < NST - 1; ++i) issue(i);
 
-  int st = 0;      // stage of the next page
-  for (int item = 0; item < n_issued; ++item) {
-    const int slot = item & (NST - 1);
-    const int np = __shfl_sync(0xffffffffu, rec.np, slot);
-    int rem = __shfl_sync(0xffffffffu, rec.rem, slot);
-    const int tok = __shfl_sync(0xffffffffu, rec.tok, slot), hk = __shfl_sync(0xffffffffu, rec.hk, slot);
+  bool failed = false;
+  uint32_t ph = 0;  // parity of the stages' current round
+  int st = 0;  // stage of the next pair
+  for (int item = 0; item < n_begun; ++item) {
+    const ItemRec* rec = recs + (item & (C::RECS - 1));
+    __syncwarp();
+    const int np = rec->np;
+    int rem = rec->rem;
     // B operand of S^T = K Q^T: lane (head gq, quarter tq) holds the eight elements of quarter tq
-    // of every group; and the accumulators' starts for heads 2 tq, 2 tq + 1
-    uint32_t qb[NG][4];
-    float cs[NG][2];
+    // of every group.  The offsets' share of the scores, sum_g s_g (-136 sum q_g), is a product
+    // over the groups too: its B operand holds -136 sum q_g in three bf16 parts, column by column
+    // the groups of part 0, of part 1, ..., against the row's scales as they are stored.
+    uint32_t qb[NG][4], ob0, ob1 = 0u;
+    {
+      const bf16* q = p.q_rot + (static_cast<int64_t>(rec->tok) * p.H_q + rec->hk * G + gq) * D + 8 * tq;
+      float off[NG];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (gq < G)
-        x = __ldg(reinterpret_cast<const uint4*>(p.q_rot + (static_cast<int64_t>(tok) * p.H_q + hk * G + gq) * D + 32 * g + 8 * tq));
-      qb[g][0] = x.x; qb[g][1] = x.y; qb[g][2] = x.z; qb[g][3] = x.w;
-      float sum = 0.f;
+      for (int g = 0; g < NG; ++g) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (gq < G) x = __ldg(reinterpret_cast<const uint4*>(q + 32 * g));
+        qb[g][0] = x.x; qb[g][1] = x.y; qb[g][2] = x.z; qb[g][3] = x.w;
+        float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += bf16_lo(qb[g][i]) + bf16_hi(qb[g][i]);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      cs[g][0] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * tq);
-      cs[g][1] = -136.f * __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
+        for (int i = 0; i < 4; ++i) sum += bf16_lo(qb[g][i]) + bf16_hi(qb[g][i]);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        off[g] = -136.f * sum;
+      }
+      if constexpr (NG == 4) {
+        const float x = tq & 1 ? off[2] : off[0], y = tq & 1 ? off[3] : off[1];
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(bf16_part(x, tq >> 1), bf16_part(y, tq >> 1));
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(bf16_part(x, 2), bf16_part(y, 2));
+        ob0 = *reinterpret_cast<const uint32_t*>(&lo);
+        if (tq < 2) ob1 = *reinterpret_cast<const uint32_t*>(&hi);
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(bf16_part(off[0], tq), bf16_part(off[1], tq));
+        ob0 = tq < 3 ? *reinterpret_cast<const uint32_t*>(&lo) : 0u;
+      }
     }
+    const float sl2 = p.scale_log2;
     float acc[NK][4];
 #pragma unroll
     for (int j = 0; j < NK; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    float mu0 = -INFINITY, mu1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 tq and 2 tq + 1
+    float mu0 = -INFINITY, mu1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 tq and 2 tq + 1 (mu in log2 units)
     constexpr float kRescaleLog2 = 8.f;  // raise the reference max only when it grows by 2^8
-    for (int pi = 0; pi < np; ++pi, rem -= kPage) {
-      cp_async_wait<NST - 2>();
-      __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
-      issue((st + NST - 1) & (NST - 1));
+    for (int pi = 0; pi < np; pi += 2, rem -= 2 * kPage) {
+      __syncwarp();  // every lane is done with the stage before
+      issue(st == 0 ? NST - 1 : st - 1);
+      if (!mbar_wait(full + st, ph, nullptr)) {
+        failed = true;
+        break;
+      }
+      --in_flight;
       const uint32_t stage = ring + st * C::STAGE;
-      st = (st + 1) & (NST - 1);
-      // S^T: lane holds (token gq, heads 2 tq, 2 tq + 1) and (token gq + 8, same heads)
-      uint32_t ka[NG], kb[NG], sa[NG / 2], sb[NG / 2];
-      lds_words<NG>(stage + gq * Q::ROW + tq * 4 * NG, ka);
-      lds_words<NG>(stage + (gq + 8) * Q::ROW + tq * 4 * NG, kb);
-      lds_words<NG / 2>(stage + Q::KS_OFF + gq * NG * 2, sa);
-      lds_words<NG / 2>(stage + Q::KS_OFF + (gq + 8) * NG * 2, sb);
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float c[4];
-        uint32_t a[4] = {q4_pair128(ka[g], 0), q4_pair128(kb[g], 0), q4_pair128(ka[g], 1), q4_pair128(kb[g], 1)};
-        mma_16816_bf16_from(c, a, qb[g][0], qb[g][1], cs[g][0], cs[g][1]);
-        uint32_t a2[4] = {q4_pair128(ka[g], 2), q4_pair128(kb[g], 2), q4_pair128(ka[g], 3), q4_pair128(kb[g], 3)};
-        mma_16816_bf16(c, a2, qb[g][2], qb[g][3]);
-        const float fa = g & 1 ? bf16_hi(sa[g >> 1]) : bf16_lo(sa[g >> 1]);
-        const float fb = g & 1 ? bf16_hi(sb[g >> 1]) : bf16_lo(sb[g >> 1]);
-        s0 = fmaf(fa, c[0], s0);
-        s1 = fmaf(fa, c[1], s1);
-        s2 = fmaf(fb, c[2], s2);
-        s3 = fmaf(fb, c[3], s3);
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1u;
       }
-      const float sl2 = p.scale_log2;
-      const bool va = gq < rem, vb = gq + 8 < rem;
-      s0 = va ? s0 * sl2 : -INFINITY;
-      s1 = va ? s1 * sl2 : -INFINITY;
-      s2 = vb ? s2 * sl2 : -INFINITY;
-      s3 = vb ? s3 * sl2 : -INFINITY;
-      float mh0 = fmaxf(s0, s2), mh1 = fmaxf(s1, s3);
+      const int n_half = pi + 1 < np ? 2 : 1;
+      // S^T: lane holds (row ra, heads 2 tq, 2 tq + 1) and (row ra + 8, same heads) of each page
+      float s[2][4];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mh0 = fmaxf(mh0, __shfl_xor_sync(0xffffffffu, mh0, o));
-        mh1 = fmaxf(mh1, __shfl_xor_sync(0xffffffffu, mh1, o));
+      for (int h = 0; h < 2; ++h) {
+        s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
+        if (h < n_half) {
+          const uint32_t pg = stage + h * C::PAGE;
+          uint32_t ka[NG], kb[NG], sa[NG / 2], sb[NG / 2];
+          lds_words<NG>(pg + ra * Q::ROW + tq * 4 * NG, ka);
+          lds_words<NG>(pg + (ra + 8) * Q::ROW + tq * 4 * NG, kb);
+          lds_words<NG / 2>(pg + Q::KS_OFF + ra * NG * 2, sa);
+          lds_words<NG / 2>(pg + Q::KS_OFF + (ra + 8) * NG * 2, sb);
+          const uint32_t s_a = NG == 4 && (tq & 1) ? sa[NG / 2 - 1] : sa[0], s_b = NG == 4 && (tq & 1) ? sb[NG / 2 - 1] : sb[0];
+          const uint32_t sc[4] = {s_a, s_b, s_a, s_b};
+          mma_16816_bf16_zero(s[h], sc, ob0, ob1);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            float c[4];
+            const uint32_t a[4] = {q4_pair128(ka[g], 0), q4_pair128(kb[g], 0), q4_pair128(ka[g], 1), q4_pair128(kb[g], 1)};
+            mma_16816_bf16_zero(c, a, qb[g][0], qb[g][1]);
+            const uint32_t a2[4] = {q4_pair128(ka[g], 2), q4_pair128(kb[g], 2), q4_pair128(ka[g], 3), q4_pair128(kb[g], 3)};
+            mma_16816_bf16(c, a2, qb[g][2], qb[g][3]);
+            const float fa = g & 1 ? bf16_hi(sa[g >> 1]) : bf16_lo(sa[g >> 1]);
+            const float fb = g & 1 ? bf16_hi(sb[g >> 1]) : bf16_lo(sb[g >> 1]);
+            s[h][0] = fmaf(fa, c[0], s[h][0]);
+            s[h][1] = fmaf(fa, c[1], s[h][1]);
+            s[h][2] = fmaf(fb, c[2], s[h][2]);
+            s[h][3] = fmaf(fb, c[3], s[h][3]);
+          }
+        }
       }
-      const bool g0 = mh0 > mu0 + kRescaleLog2, g1 = mh1 > mu1 + kRescaleLog2;
-      if (__any_sync(0xffffffffu, g0 || g1)) {
+      if (n_half == 1) s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
+      if (rem < 2 * kPage) {  // the row's last keys
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h * kPage + ra >= rem) s[h][0] = s[h][1] = -INFINITY;
+          if (h * kPage + ra + 8 >= rem) s[h][2] = s[h][3] = -INFINITY;
+        }
+      }
+      // the lanes compare their own scores with the reference maximum; only when one of them is
+      // past it by more than 2^8 do they look for the heads' maxima
+      float mh0 = fmaxf(fmax3(s[0][0], s[0][2], s[1][0]), s[1][2]) * sl2;
+      float mh1 = fmaxf(fmax3(s[0][1], s[0][3], s[1][1]), s[1][3]) * sl2;
+      if (__any_sync(0xffffffffu, mh0 > mu0 + kRescaleLog2 || mh1 > mu1 + kRescaleLog2)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mh0 = fmaxf(mh0, __shfl_xor_sync(0xffffffffu, mh0, o));
+          mh1 = fmaxf(mh1, __shfl_xor_sync(0xffffffffu, mh1, o));
+        }
+        const bool g0 = mh0 > mu0 + kRescaleLog2, g1 = mh1 > mu1 + kRescaleLog2;
         const float n0 = g0 ? mh0 : mu0, n1 = g1 ? mh1 : mu1;
         const float a0 = g0 ? ex2(mu0 - n0) : 1.f, a1 = g1 ? ex2(mu1 - n1) : 1.f;
 #pragma unroll
@@ -254,37 +337,55 @@ __device__ __noinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem
         mu0 = n0;
         mu1 = n1;
       }
-      const float p0 = ex2(s0 - mu0), p1 = ex2(s1 - mu1), p2 = ex2(s2 - mu0), p3 = ex2(s3 - mu1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      // O^T += V^T (P s)^T, group by group.  Rows past the context may hold any scale: their weight is 0.
-      uint32_t v[4][NG / 2], wa[NG / 2], wb[NG / 2];
-      {
-        const int swz = D == 128 ? 2 * tq : 2 * (tq >> 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
-          const int r = 2 * tq + (i & 1) + 8 * (i >> 1);
-          const int byte = r * Q::ROW + gq * 2 * NG;
-          lds_words<NG / 2>(stage + Q::V_OFF + (byte ^ (swz << 4)), v[i]);
-        }
-        lds_words<NG / 2>(stage + Q::VS_OFF + gq * NG * 2, wa);
-        lds_words<NG / 2>(stage + Q::VS_OFF + (gq + 8) * NG * 2, wb);
+      for (int h = 0; h < 2; ++h) {
+        s[h][0] = ex2(fmaf(s[h][0], sl2, -mu0));
+        s[h][1] = ex2(fmaf(s[h][1], sl2, -mu1));
+        s[h][2] = ex2(fmaf(s[h][2], sl2, -mu0));
+        s[h][3] = ex2(fmaf(s[h][3], sl2, -mu1));
+        l0 += s[h][0] + s[h][2];
+        l1 += s[h][1] + s[h][3];
       }
+      // O^T += V^T (P s)^T, page by page and group by group
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float fa = va ? (g & 1 ? bf16_hi(wa[g >> 1]) : bf16_lo(wa[g >> 1])) : 0.f;
-        const float fb = vb ? (g & 1 ? bf16_hi(wb[g >> 1]) : bf16_lo(wb[g >> 1])) : 0.f;
-        const __nv_bfloat162 h01 = __floats2bfloat162_rn(p0 * fa, p1 * fa), h23 = __floats2bfloat162_rn(p2 * fb, p3 * fb);
-        const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
-        const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
-        const uint32_t lo = join_halves(v[0][g >> 1], v[1][g >> 1], g & 1), hi = join_halves(v[2][g >> 1], v[3][g >> 1], g & 1);
+      for (int h = 0; h < 2; ++h) {
+        if (h >= n_half) break;
+        const uint32_t pg = stage + h * C::PAGE + Q::V_OFF;
+        uint32_t v[4][NG / 2], wa[NG / 2], wb[NG / 2];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t a[4] = {q4_pair(lo, 2 * m), q4_pair(lo, 2 * m + 1), q4_pair(hi, 2 * m), q4_pair(hi, 2 * m + 1)};
-          mma_16816_bf16(acc[2 * g + m], a, b0, b1);
+        for (int i = 0; i < 4; ++i) {  // MMA tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+          const int r = 2 * tq + ((i & 1) ^ (tq & 1)) + 8 * (i >> 1);
+          lds_words<NG / 2>(pg + r * Q::ROW + gq * 2 * NG, v[i]);
+        }
+        lds_words<NG / 2>(pg + Q::VS_OFF - Q::V_OFF + ra * NG * 2, wa);
+        lds_words<NG / 2>(pg + Q::VS_OFF - Q::V_OFF + (ra + 8) * NG * 2, wb);
+        if (rem < 2 * kPage) {  // rows past the context may hold any scale: their weight is 0
+#pragma unroll
+          for (int j = 0; j < NG / 2; ++j) {
+            if (h * kPage + ra >= rem) wa[j] = 0u;
+            if (h * kPage + ra + 8 >= rem) wb[j] = 0u;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float fa = g & 1 ? bf16_hi(wa[g >> 1]) : bf16_lo(wa[g >> 1]);
+          const float fb = g & 1 ? bf16_hi(wb[g >> 1]) : bf16_lo(wb[g >> 1]);
+          const float2 w01 = fmul2(make_float2(s[h][0], s[h][1]), make_float2(fa, fa));
+          const float2 w23 = fmul2(make_float2(s[h][2], s[h][3]), make_float2(fb, fb));
+          const __nv_bfloat162 h01 = __floats2bfloat162_rn(w01.x, w01.y), h23 = __floats2bfloat162_rn(w23.x, w23.y);
+          const uint32_t b0 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h01));
+          const uint32_t b1 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h23));
+          const uint32_t lo = join_halves(v[0][g >> 1], v[1][g >> 1], g & 1);
+          const uint32_t hi = join_halves(v[2][g >> 1], v[3][g >> 1], g & 1);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t a[4] = {q4_pair(lo, 2 * m), q4_pair(lo, 2 * m + 1), q4_pair(hi, 2 * m), q4_pair(hi, 2 * m + 1)};
+            mma_16816_bf16(acc[2 * g + m], a, b0, b1);
+          }
         }
       }
     }
+    if (failed) break;
     // O^T: lane holds elements 32 g + 8 (gq / 2) + 2 i + gq % 2 of heads 2 tq, 2 tq + 1, with i = 2 m in
     // acc[2 g + m][0, 1] and i = 2 m + 1 in acc[2 g + m][2, 3]
 #pragma unroll
@@ -292,8 +393,7 @@ __device__ __noinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    const int part = __shfl_sync(0xffffffffu, rec.part, slot), ns = __shfl_sync(0xffffffffu, rec.ns, slot);
-    const int k = __shfl_sync(0xffffffffu, rec.k, slot);
+    const int tok = rec->tok, hk = rec->hk, ns = rec->ns, part = rec->part;
     const int d0 = 8 * (gq >> 1) + (gq & 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -320,6 +420,7 @@ __device__ __noinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem
       }
     }
     if (ns > 1) {
+      const int k = rec->k;
       __threadfence();  // this split's records are visible before it is counted
       __syncwarp();
       int last = 0;
@@ -331,12 +432,25 @@ __device__ __noinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem
       }
     }
   }
-  cp_async_wait<0>();
+  if (failed) {
+    if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_TIMEOUT);
+    // let copies already in flight land before the CTA's shared memory is released
+    for (; in_flight > 0; --in_flight) {
+      mbar_wait(full + st, ph, nullptr, 200000000ull);
+      if (++st == NST) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  if (lane == 0)
+    for (int i = 0; i < NST; ++i) mbar_inval(full + i);
 }
 
 // One persistent CTA per SM, as attention_kernel.
 template <int D, int G>
-__global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __grid_constant__ CUtensorMap tm_q, AttnParams p) {
+__global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -376,7 +490,6 @@ __global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __gri
       if (aborted) break;
     } else if (!chunk && n_dec_items > 0) {
       decode_phase_q4<D, G>(p, smem);
-      fence_proxy_async_smem();  // the ring's copies are ordered before a chunk phase's TMA into the same memory
       __syncthreads();
     }
   }
@@ -420,6 +533,7 @@ extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* 
   if (rc != MS_OK || empty) return rc;
   p.kv_q4 = static_cast<const uint8_t*>(kv_cache);
   p.dec_workers = p.num_sms * (kQ4Threads / 32);
+  p.graded = 1;
   p.tile_cycles = kQ4TileCycles;
   p.dec_bytes_cycle = kQ4DecodeBytesPerCycle;
   p.key_bytes = q4_block_bytes(D) / 16.f;

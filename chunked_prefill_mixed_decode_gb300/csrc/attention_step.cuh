@@ -46,6 +46,7 @@ enum {
   H_NPART = 8,
   H_CHUNK_CTAS = 9,  // CTAs that start on chunk work (the rest start on decodes)
   H_CLOCK_MHZ = 10,  // SM clock the last call ran at (kept across calls; 0 in a fresh workspace)
+  H_GRADED = 11,     // decode rows end in pieces of falling size (dec_piece)
   H_WORDS = 64
 };
 
@@ -66,6 +67,7 @@ struct AttnParams {
   int32_t dec_workers;       // decode worker warps in the grid
   int32_t num_sms;
   int32_t clear_status;      // the prologue zeroes the status word first (scratch owned by the library)
+  int32_t graded;            // end decode rows in pieces of falling size where the workspace holds them
   int32_t force_chunk_ctas;  // test hook: CTAs that start on chunk work (-1: the cost model decides)
   float sm_mhz;              // cost model: the SM clock when no call has measured it yet,
   float hbm_gbs;             // and the HBM bandwidth that caps decode
@@ -141,9 +143,54 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
-// Work items of one row: decode splits of `split` pages, or pairs of 128-row Q tiles.
-__device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsigned split) {
-  if (!chunk) return static_cast<int>((static_cast<unsigned>(c + kPage) / kPage + split - 1) / split);
+// A decode row of n pages is cut into pieces of `split` pages.  Graded: whole
+// pieces as long as two fit, and the rest, which is below two pieces, as it is
+// where it is below one, else as about a half, a third and a sixth of it.  The
+// queue runs whole pieces first, then the halves, the thirds, the sixths, so
+// that the warps end on short pieces: with about three pieces a warp (64 rows
+// of 32 heads and 512 to 4096 keys on 152 SMs of 16 warps) the last piece
+// otherwise leaves a sixth of the warps' time idle.  A row has at most
+// n / split + 2 graded pieces.
+constexpr int kMinGradedSplit = 36;  // keeps n / 36 + 2 pieces within the workspace's n / 32 + 2
+
+struct DecCut {
+  unsigned whole, rest;  // whole pieces, pages after them
+  int tail;              // pieces of the rest: 1 or 3
+};
+
+__device__ __forceinline__ DecCut dec_cut(unsigned n, unsigned split) {
+  DecCut r;
+  r.whole = n >= 2 * split ? n / split - 1 : 0;
+  r.rest = n - r.whole * split;
+  r.tail = r.rest >= split ? 3 : 1;
+  return r;
+}
+
+__device__ __forceinline__ int dec_pieces(unsigned n, unsigned split, bool graded) {
+  if (!graded) return static_cast<int>((n + split - 1) / split);
+  const DecCut c = dec_cut(n, split);
+  return static_cast<int>(c.whole) + c.tail;
+}
+
+// pages [p0, p0 + np) of piece i of a row of n pages
+__device__ __forceinline__ void dec_piece(int n, int split, int graded, int i, int& p0, int& np) {
+  p0 = i * split;
+  np = min(split, n - p0);
+  if (!graded) return;
+  const DecCut c = dec_cut(static_cast<unsigned>(n), static_cast<unsigned>(split));
+  const int w = static_cast<int>(c.whole), rest = static_cast<int>(c.rest);
+  if (i < w) return;
+  p0 = w * split;
+  np = rest;
+  if (c.tail == 1) return;
+  const int a = (rest / 2 + 1) & ~1, b = ((rest - a) * 2 / 3 + 1) & ~1;  // even: pages go in pairs
+  p0 += i == w ? 0 : i == w + 1 ? a : a + b;
+  np = i == w ? a : i == w + 1 ? b : rest - a - b;
+}
+
+// Work items of one row: decode pieces, or pairs of 128-row Q tiles.
+__device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsigned split, bool graded) {
+  if (!chunk) return dec_pieces(static_cast<unsigned>(c + kPage) / kPage, split, graded);
   const int n_qt = (d + tpt - 1) / tpt;
   return (n_qt + 1) >> 1;
 }
@@ -266,7 +313,35 @@ __device__ __forceinline__ int decode_split(const AttnParams& p, int64_t dec_pag
                       : cdiv64(num, den);
   const int64_t min_split = p.G >= 4 ? (with_chunks ? 4 : 2) * kMinSplitPages : kMinSplitPages;
   split = split < min_split ? min_split : (split > kMaxSplitPages ? kMaxSplitPages : split);
+  if (p.graded) split = split < kMinGradedSplit ? kMinGradedSplit : split & ~int64_t{1};
   return static_cast<int>(split);
+}
+
+// Whether the decode rows' graded pieces fit in the workspace.
+__device__ __forceinline__ bool decode_graded(const AttnParams& p, int64_t dec_pages, int n_dec, int split) {
+  if (!p.graded) return false;
+  const int64_t most = dec_pages / split + 2 * static_cast<int64_t>(n_dec);
+  return most * p.H_kv <= p.max_dec_items && most * p.H_q <= p.max_partials;
+}
+
+// Entries of decode row q (queue order) in the item table: `before` items and
+// `before3` rows of three tail pieces come ahead of it.  Graded rows put their
+// whole pieces first, then every row's first tail piece, then the second, then
+// the third; n_whole, n_dec and n3 are the totals.
+__device__ __forceinline__ void write_dec_entries(const AttnParams& p, int q, int items, int before, int before3, bool graded,
+                                                  bool three, int n_whole, int n_dec, int n3) {
+  if (!graded) {
+    for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(q, i);
+    return;
+  }
+  const int whole = items - (three ? 3 : 1);
+  const int first = before - q - 2 * before3;  // whole pieces ahead
+  for (int i = 0; i < whole; ++i) p.dec_items[first + i] = make_int2(q, i);
+  p.dec_items[n_whole + q] = make_int2(q, whole);
+  if (three) {
+    p.dec_items[n_whole + n_dec + before3] = make_int2(q, whole + 1);
+    p.dec_items[n_whole + n_dec + n3 + before3] = make_int2(q, whole + 2);
+  }
 }
 
 // Header of a call whose metadata failed validation: status set, no work.
@@ -275,6 +350,7 @@ __device__ __forceinline__ void header_bad_meta(int32_t* hdr) {
   hdr[H_DEC_CTR] = hdr[H_CH_CTR] = 0;
   hdr[H_NDEC] = hdr[H_NDEC_ITEMS] = hdr[H_NCH] = hdr[H_NCH_ITEMS] = hdr[H_NPART] = 0;
   hdr[H_SPLIT] = kMinSplitPages;
+  hdr[H_GRADED] = 0;
   hdr[H_CHUNK_CTAS] = 0;
 }
 
@@ -313,6 +389,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int tpt = 128 / p.G;
   const unsigned bd = __ballot_sync(0xffffffffu, is_dec), bc = __ballot_sync(0xffffffffu, is_ch);
   const int n_dec = __popc(bd), n_ch = __popc(bc);
+  const bool graded = decode_graded(p, dec_pages, n_dec, split);
   // position in its list, then rank by key within the list (longest first):
   // the keys sit in shared memory by list position, zero-padded, read 16 bytes at a time
   __shared__ __align__(16) uint32_t s_key[2][32];
@@ -334,12 +411,14 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const uint4 v = k4[m];
     rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
   }
-  const int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
+  const int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split), graded) : 0;
+  const bool three = graded && is_dec && items >= 3;  // a row has one item or at least three
   const int q = (is_ch ? n_dec : 0) + rank;  // queue position
-  if (listed) s_items[q] = items;
+  if (listed) s_items[q] = items | (three ? 1 << 30 : 0);
   __syncwarp();
+  const unsigned b3 = __ballot_sync(0xffffffffu, (s_items[lane] >> 30) != 0);  // by queue position
   {  // exclusive prefix over queue positions, one per lane
-    const int v = s_items[lane];
+    const int v = s_items[lane] & ((1 << 30) - 1);
     int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -365,8 +444,11 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     p.dec_rows[rank] = lane;
     p.dec_part_base[rank] = static_cast<int32_t>(static_cast<int64_t>(before) * p.H_q);
     p.dec_nsplit[rank] = items;
-    if (!dec_over)
-      for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(rank, i);
+    if (!dec_over) {
+      const int n3 = __popc(b3);
+      write_dec_entries(p, rank, items, before, __popc(b3 & ((1u << rank) - 1u)), graded, three,
+                        dec_tot - n_dec - 2 * n3, n_dec, n3);
+    }
   }
   if (is_ch) p.ch_rows[rank] = lane;
   const SmSplit sp = chunk_cta_split(p, static_cast<float>(tiles), static_cast<float>(dec_pages),
@@ -398,6 +480,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_DEC_CTR] = 0;
     hdr[H_CH_CTR] = 0;
     hdr[H_SPLIT] = split;
+    hdr[H_GRADED] = graded;
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -492,6 +575,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   }
   // 2. decode split size
   const int split = decode_split(p, dec_pages, n_ch > 0);
+  const bool graded = decode_graded(p, dec_pages, n_dec, split);
   const int tpt = 128 / p.G;
   const unsigned split32 = static_cast<unsigned>(split);
   // 3. the two lists in input order: decode rows at lst[0, n_dec), chunk rows after them
@@ -542,16 +626,23 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     }
     const int row = lst[j], c = rc[row], d = rd[row];
     (ch ? p.ch_rows : p.dec_rows)[rank] = row;
-    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32);
+    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32, graded);
     if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(chunk_tiles(c, d, tpt)) * p.H_kv);
   }
   __syncthreads();
   // 6. exclusive prefix of the item counts in queue order (decode rows, then chunk rows)
-  int run = 0;
+  // (and, graded, of the decode rows with three tail pieces, where the keys were)
+  int run = 0, run3 = 0;
+  int32_t* pref3 = reinterpret_cast<int32_t*>(key);
   for (int base = 0; base < n_tot; base += nt) {  // uniform
     const int q = base + tid;
     const int v = q < n_tot ? pref[q] : 0;
     int tot;
+    if (graded) {
+      const int o3 = block_scan(q < n_dec && v >= 3, s_warp, tot);
+      if (q < n_dec) pref3[q] = run3 + o3;
+      run3 += tot;
+    }
     const int o = block_scan(v, s_warp, tot);
     if (q < n_tot) {
       pref[q] = run + o;
@@ -569,15 +660,15 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   const int64_t n_ch_items = static_cast<int64_t>(ch_tot) * p.H_kv;
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
   const bool ch_over = n_ch_items > p.max_ch_items;
-  // 7. item tables.  Decode rows, a thread per row: entry pref[q] + i -> (row
-  // k, split i), one entry per split (a work item is an entry and a KV head).
+  // 7. item tables.  Decode rows, a thread per row: (row k, split i), one entry
+  // per split (a work item is an entry and a KV head).
   // Then the SM split, which also orders the chunk items; chunk rows, a warp
   // per row: one entry per item, (row k, KV head and Q-tile pair).  Then the
   // split counters of every (decode row, KV head), zeroed 16 bytes at a time.
   for (int q = tid; q < n_dec && !dec_over; q += nt) {
     const int cnt = pref[q + 1] - pref[q];
-    int2* out = p.dec_items + pref[q];
-    for (int i = 0; i < cnt; ++i) out[i] = make_int2(q, i);
+    write_dec_entries(p, q, cnt, pref[q], graded ? pref3[q] : 0, graded, cnt >= 3, dec_tot - n_dec - 2 * run3, n_dec,
+                      run3);
   }
   if (warp == 0) {
     const SmSplit sp = chunk_cta_split(p, static_cast<float>(s_tiles), static_cast<float>(dec_pages),
@@ -610,6 +701,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_DEC_CTR] = 0;
       hdr[H_CH_CTR] = 0;
       hdr[H_SPLIT] = static_cast<int32_t>(split);
+      hdr[H_GRADED] = graded;
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }
@@ -911,6 +1003,7 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.G = G;
   p.num_sms = sms;
   p.clear_status = clear_status ? 1 : 0;
+  p.graded = 0;
   p.test_stall = stall_limit_ns > 0 ? 1 : 0;
   p.wait_limit_ns = stall_limit_ns > 0 ? static_cast<uint64_t>(stall_limit_ns) : 2000000000ull;
   p.scale_log2 = scale * 1.4426950408889634f;
