@@ -52,16 +52,6 @@ struct DecQ4 {
   static constexpr int SMEM = BAR_OFF + WARPS * NST * 8;
 };
 
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(dst[0]), "=r"(dst[1]), "=r"(dst[2]), "=r"(dst[3]) : "r"(src) : "memory");
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(dst[0]), "=r"(dst[1]) : "r"(src) : "memory");
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(dst[0]) : "r"(src) : "memory");
-}
-
 // D = A B, from zero
 __device__ __forceinline__ void mma_16816_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -485,7 +475,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __gri
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
       const bool aborted = bars->abort != 0;
       if (threadIdx.x == 0)
-        for (uint64_t* b = &bars->q_full; b <= &bars->mma_done[2]; ++b) mbar_inval(b);
+        for (uint64_t* b = &bars->q_full; b <= &bars->raw_empty[kRawStages - 1]; ++b) mbar_inval(b);
       __syncthreads();
       if (aborted) break;
     } else if (!chunk && n_dec_items > 0) {
@@ -506,7 +496,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __gri
 
 template <int D, int G>
 int launch_q4(const AttnParams& p, const CUtensorMap& tq, cudaStream_t st) {
-  constexpr int smem = ChCfg<D>::SMEM > DecQ4<D>::SMEM ? ChCfg<D>::SMEM : DecQ4<D>::SMEM;
+  constexpr int smem = ChQ4<D>::SMEM > DecQ4<D>::SMEM ? ChQ4<D>::SMEM : DecQ4<D>::SMEM;
   static_assert(smem <= 232448, "attention kernel exceeds the per-CTA shared-memory limit");
   const int slot = (D == 128 ? 4 : 0) + (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3);  // one bit per instance
   if (ensure_smem_limit(attention_q4_kernel<D, G>, slot, smem) != MS_OK) return MS_ERR_CUDA;

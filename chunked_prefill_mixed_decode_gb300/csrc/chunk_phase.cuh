@@ -36,6 +36,8 @@ struct ChItem {
   int t0[2];    // per Q tile: index of its first KV tile among all tiles its softmax group ran
 };
 
+constexpr int kRawStages = 3;  // tiles of 4-bit pages on their way to the dequantizing warps
+
 struct ChBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[8], k_empty[8];  // K stage: free once both S issuers' MMAs are done
@@ -43,6 +45,7 @@ struct ChBars {
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [Q tile][S/P buffer]
   uint64_t item_full[2], item_empty[2];
   uint64_t mma_done[3];
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // 4-bit pools: pages as they are stored
   uint32_t tmem;
   int abort;
   ChItem items[2];
@@ -68,25 +71,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 constexpr int kDequantWarps = kTilePages;            // one per page of a tile
 constexpr int kDequantWarp0 = 4 + kSoftmaxWarps;     // warps 12-15
 
-// One lane's share of one page: two rows of K and of V (quarter t of each
-// group), and those rows' scales.
+// The phase's shared memory over a 4-bit pool: the bf16 phase's, then the raw pages.
 template <int D>
-struct Q4Rows {
-  static constexpr int NG = Q4<D>::NG;
-  uint32_t k[2][NG], v[2][NG], ks[2][NG / 2], vs[2][NG / 2];
+struct ChQ4 {
+  static constexpr int RAW_OFF = ChCfg<D>::SMEM;
+  static constexpr int RAW_STAGE = kTilePages * Q4<D>::BYTES;
+  static constexpr int SMEM = RAW_OFF + kRawStages * RAW_STAGE;
 };
 
+// N words of shared memory, 4 N-byte aligned
 template <int N>
-__device__ __forceinline__ void ldg_words(const uint8_t* src, uint32_t* dst) {
-  if constexpr (N == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-    dst[0] = x.x; dst[1] = x.y; dst[2] = x.z; dst[3] = x.w;
-  } else if constexpr (N == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-    dst[0] = x.x; dst[1] = x.y;
-  } else {
-    dst[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-  }
+__device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(dst[0]), "=r"(dst[1]), "=r"(dst[2]), "=r"(dst[3])
+                 : "r"(src)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(dst[0]), "=r"(dst[1]) : "r"(src) : "memory");
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(dst[0]) : "r"(src) : "memory");
 }
 
 // Quarter t of one row (a word per group) as bf16 into a 128-byte-swizzled
@@ -99,105 +103,89 @@ __device__ __forceinline__ void store_row_part(uint32_t row_addr, int key, int t
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const uint32_t s2 = __byte_perm(scales[g >> 1], 0, (g & 1) ? 0x3232 : 0x1010);
+    const uint32_t c2 = q4_minus_24(s2);
     uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = q4_scaled_pair(words[g], i, s2);
+    for (int i = 0; i < 4; ++i) x[i] = q4_scaled_pair(words[g], i, s2, c2);
     const uint32_t dst = row_addr + (g >> 1) * SLAB + ((((g & 1) * 4 + t) ^ (key & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                  : "memory");
   }
 }
 
-// Warp 12 + w fills page w of every K and V tile of the CTA's items.  Four
-// lanes share a row (16 bytes of codes each at D = 128); the eight lanes of one
-// 16-byte store wave hold rows r and r + 4, whose chunks land in different
-// halves of the 128-byte line, so the stores do not conflict.  Rows past the
-// row's context are written as zeros.  Returns false when a wait gave up.
+// Warp 12 + w turns page w of every tile into K and V rows of the CTA's items.
+// Four lanes share a row (16 bytes of codes each at D = 128); the eight lanes
+// of one 16-byte access hold rows r and r ^ 5: they differ in bit 0, so the
+// loads cover both halves of a 128-byte line, and in bit 2, so that the stored
+// chunks land in different halves of the swizzled line.  Rows past the row's
+// context are written as zeros.  Returns false when a wait gave up.
 template <int D>
-__device__ __forceinline__ bool dequant_role(const AttnParams& p, uint8_t* smem, ChBars* bars,
-                                             const volatile int* abort_flag, uint64_t lim) {
+__device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const volatile int* abort_flag, uint64_t lim) {
   using C = ChCfg<D>;
   using Q = Q4<D>;
   constexpr int NSL = C::NSL, NG = Q::NG, KVS = C::KVS;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kDequantWarp0;
   const int t = lane & 3, y = lane >> 2;
-  const int r0 = ((y & 1) << 2) | (y >> 1);  // and r0 + 8
+  const int r0 = (y >> 1) ^ ((y & 1) * 5);  // and r0 + 8
   const uint32_t sbase = smem_u32(smem);
-  int bk = 0;        // stage of the next tile
-  uint32_t ph = 0;   // parity of the stage's last release
-  bool first = true; // the stages' first round: nothing to wait for
+  int bk = 0, br = 0;            // stages of the next tile: K/V and raw
+  uint32_t ph = 1, rph = 0;      // their parities: the K/V stage's last release, the raw stage's fill
   for (int n = 0;; ++n) {
     const int slot = n & 1;
     if (!warp_wait(&bars->item_full[slot], (n >> 1) & 1, abort_flag, lim)) return false;
     const ChItem& it = bars->items[slot];  // stable until this role arrives on item_empty
-    const int row = it.row;
-    if (row < 0) return true;
+    if (it.row < 0) return true;
     const int n_kt = it.n_kt, kv_max = max(it.kv_end[0], it.kv_end[1]);
-    const int n_pages = (kv_max + kPage - 1) / kPage;
-    const int32_t* btrow = row_table(p, row);
-    const uint8_t* pool = p.kv_q4 + static_cast<int64_t>(it.hk) * Q::BYTES;
-    const int64_t page_bytes = static_cast<int64_t>(p.H_kv) * Q::BYTES;
-    auto page_id = [&](int kt) { return kt * kTilePages + w < n_pages ? __ldg(btrow + kt * kTilePages + w) : 0; };
-    auto load = [&](int phys, Q4Rows<D>& x) {
-      if (phys < 0 || phys >= p.num_pages) {
-        if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
-        phys = 0;
-      }
-      const uint8_t* blk = pool + phys * page_bytes;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + 8 * i;
-        ldg_words<NG>(blk + r * Q::ROW + t * 4 * NG, x.k[i]);
-        ldg_words<NG>(blk + Q::V_OFF + r * Q::ROW + t * 4 * NG, x.v[i]);
-        ldg_words<NG / 2>(blk + Q::KS_OFF + r * NG * 2, x.ks[i]);
-        ldg_words<NG / 2>(blk + Q::VS_OFF + r * NG * 2, x.vs[i]);
-      }
-    };
-    Q4Rows<D> cur, nxt;
-    load(page_id(0), cur);
-    int id_next = page_id(1);
     for (int kt = 0; kt < n_kt; ++kt) {
-      if (kt + 1 < n_kt) load(id_next, nxt);
-      id_next = page_id(kt + 2);
       const int keys = kv_max - kt * kKeys - w * kPage;  // of this page
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (r0 + 8 * i >= keys) {  // past the context: scales of zero (the codes are finite whatever they hold)
-#pragma unroll
-          for (int j = 0; j < NG / 2; ++j) cur.ks[i][j] = cur.vs[i][j] = 0u;
-        }
-      if (!first && !warp_wait(&bars->k_empty[bk], ph, abort_flag, lim)) return false;
+      uint32_t k[2][NG], v[2][NG], ks[2][NG / 2], vs[2][NG / 2];
+      if (!mbar_wait_fast(&bars->raw_full[br], rph, abort_flag, 16, lim)) return false;
       if (keys > 0) {
-        const uint32_t kbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + w * 2048;
+        const uint32_t blk = sbase + ChQ4<D>::RAW_OFF + br * ChQ4<D>::RAW_STAGE + w * Q::BYTES;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = r0 + 8 * i;
-          store_row_part<D, kKVSlab>(kbase + r * 128, r, t, cur.k[i], cur.ks[i]);
+          lds_words<NG>(blk + r * Q::ROW + t * 4 * NG, k[i]);
+          lds_words<NG>(blk + Q::V_OFF + r * Q::ROW + t * 4 * NG, v[i]);
+          lds_words<NG / 2>(blk + Q::KS_OFF + r * NG * 2, ks[i]);
+          lds_words<NG / 2>(blk + Q::VS_OFF + r * NG * 2, vs[i]);
+          if (r >= keys) {  // past the context: scales of zero (the codes are finite whatever they hold)
+#pragma unroll
+            for (int j = 0; j < NG / 2; ++j) ks[i][j] = vs[i][j] = 0u;
+          }
         }
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->k_full[bk]);
-      if (!first && !warp_wait(&bars->v_empty[bk], ph, abort_flag, lim)) return false;
+      if (lane == 0) mbar_arrive(&bars->raw_empty[br]);
+      if (++br == kRawStages) {
+        br = 0;
+        rph ^= 1u;
+      }
+      // the stage's first round finds both barriers in their initial phase, which counts as released
+      if (!mbar_wait_fast(&bars->v_empty[bk], ph, abort_flag, 16, lim)) return false;
+      if (!mbar_wait_fast(&bars->k_empty[bk], ph, abort_flag, 16, lim)) return false;
       if (keys > 0) {
+        const uint32_t kbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + w * 2048;
         const uint32_t vbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + NSL * kKVSlab + w * NSL * 2048;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = r0 + 8 * i;
+          store_row_part<D, kKVSlab>(kbase + r * 128, r, t, k[i], ks[i]);
           uint32_t words[NG];  // even elements (first half of the bytes) below odd ones, group by group
 #pragma unroll
-          for (int g = 0; g < NG; ++g) words[g] = join_halves(cur.v[i][g >> 1], cur.v[i][NG / 2 + (g >> 1)], g & 1);
-          store_row_part<D, 2048>(vbase + r * 128, r, t, words, cur.vs[i]);
+          for (int g = 0; g < NG; ++g) words[g] = join_halves(v[i][g >> 1], v[i][NG / 2 + (g >> 1)], g & 1);
+          store_row_part<D, 2048>(vbase + r * 128, r, t, words, vs[i]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->v_full[bk]);
-      cur = nxt;
+      if (lane == 0) {
+        mbar_arrive(&bars->k_full[bk]);
+        mbar_arrive(&bars->v_full[bk]);
+      }
       if (++bk == KVS) {
         bk = 0;
-        ph = first ? 0u : ph ^ 1u;
-        first = false;
+        ph ^= 1u;
       }
     }
     __syncwarp();
@@ -218,10 +206,12 @@ __device__ __forceinline__ bool dequant_role(const AttnParams& p, uint8_t* smem,
 // overlap the other group's MMAs.  Returns when the chunk queue is empty; the
 // caller owns TMEM and the barrier invalidation.
 //
-// Over a 4-bit pool (Q4) four more warps, 12-15, stand in for the TMA stream of
-// K and V: warp 12 + w reads page w of each tile straight from the pool into
-// registers, a tile ahead, and writes its values -- exactly bf16, so nothing
-// else of the phase changes -- into the same stages.
+// Over a 4-bit pool (Q4) warp 0 brings the pages of a tile as they are stored,
+// one bulk copy a page, into a ring of their own, and four more warps, 12-15,
+// write their values -- exactly bf16, so nothing else of the phase changes --
+// into the K and V stages: warp 12 + w page w of each tile.  Loads from global
+// memory into the dequantizing warps' registers a tile ahead, without the ring,
+// cost a sixth of the rate (chunks of 3968 tokens at 0 and 6000, 32 / 8 heads).
 template <int D, int G, bool Q4 = false>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
@@ -268,6 +258,11 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       mbar_init(&bars->item_empty[b], 3 + 32 * kSoftmaxWarps + (Q4 ? kDequantWarps : 0));
     }
     for (int i = 0; i < 3; ++i) mbar_init(&bars->mma_done[i], 1);
+    if constexpr (Q4)
+      for (int i = 0; i < kRawStages; ++i) {
+        mbar_init(&bars->raw_full[i], 1);
+        mbar_init(&bars->raw_empty[i], kDequantWarps);
+      }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -288,8 +283,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         prefetch_tmap(NSL == 2 ? &tm_vp : &tm_v);
       }
     }
-    const int my_pg = lane / NSL, my_s = lane % NSL;
-    const bool loader = lane < kTilePages * NSL;
+    constexpr int kPageBytes = q4_block_bytes(D), kRawOff = ChQ4<D>::RAW_OFF;
+    // lane -> (page, slab); over a 4-bit pool a page is one copy
+    const int my_pg = Q4 ? lane : lane / NSL, my_s = Q4 ? 0 : lane % NSL;
+    const bool loader = lane < kTilePages * (Q4 ? 1 : NSL);
     int g = 0;               // CTA-global KV tile counter
     int g_v = 0;             // tiles whose V has been issued
     int n_done = 0;          // items taken by this CTA
@@ -378,10 +375,6 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + s * kQSlab, &tm_q, s * 64, it.hk * G, it.tb + it.tok0[t],
                     &bars->q_full);
       }
-      if constexpr (Q4) {  // K and V come from the dequantizing warps
-        g += it.n_kt;
-        continue;
-      }
       const int kv_max = max(it.kv_end[0], it.kv_end[1]);
       const int32_t* btrow = row_table(p, it.row);
       const int n_pages = (kv_max + kPage - 1) / kPage;
@@ -398,6 +391,21 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         if (loader && my_pg < npg && (phys < 0 || phys >= p.num_pages)) {
           atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
           phys = 0;
+        }
+        if constexpr (Q4) {  // the pages as they are stored, one bulk copy each
+          const int br = g % kRawStages;
+          if (g >= kRawStages && !lane0_wait(&bars->raw_empty[br], ((g / kRawStages) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[br], npg * kPageBytes);
+          __syncwarp();
+          if (lane < npg)
+            bulk_g2s(smem + kRawOff + (br * kTilePages + lane) * kPageBytes,
+                     p.kv_q4 + (static_cast<int64_t>(phys) * p.H_kv + it.hk) * kPageBytes, kPageBytes,
+                     &bars->raw_full[br]);
+          pg_cur = pg_nxt;
+          continue;
         }
         const int row0 = (phys * p.H_kv + it.hk) * kPage;
         // K of tile g: its stage was last read by the S MMAs of tile g - KVS
@@ -421,16 +429,22 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         pg_cur = pg_nxt;
       }
       if (!ok) break;
-      if (!load_v(g - 1, row0_prev, npg_prev)) {
-        ok = false;
-        break;
+      if constexpr (!Q4) {
+        if (!load_v(g - 1, row0_prev, npg_prev)) {
+          ok = false;
+          break;
+        }
+        g_v = g;
       }
-      g_v = g;
     }
     if (lane == 0) {
       if (!ok && !stalled) *abort_flag = 1;
       // copies still in flight must land before the CTA moves on
-      if constexpr (Q4) g = 0;  // none of K or V
+      if constexpr (Q4) {
+        for (int t = (g > kRawStages ? g - kRawStages : 0); t < g; ++t)
+          mbar_wait(&bars->raw_full[t % kRawStages], (t / kRawStages) & 1, nullptr, 200000000ull);
+        g = 0;  // none straight into the K and V stages
+      }
       for (int t = (g > KVS ? g - KVS : 0); t < g; ++t)
         mbar_wait(&bars->k_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
       for (int t = (g_v > KVS ? g_v - KVS : 0); t < g_v; ++t)
@@ -754,7 +768,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   }
   if constexpr (Q4) {
     if (warp >= kDequantWarp0) {
-      if (!dequant_role<D>(p, smem, bars, abort_flag, lim)) *abort_flag = 1;
+      if (!dequant_role<D>(smem, bars, abort_flag, lim)) *abort_flag = 1;
     }
   }
   (void)n_items;
