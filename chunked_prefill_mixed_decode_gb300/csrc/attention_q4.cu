@@ -38,18 +38,29 @@ constexpr int kQ4Threads = 32 * (kDequantWarp0 + kDequantWarps);
 constexpr float kQ4TileCycles = 5820.f;
 constexpr float kQ4DecodeBytesPerCycle = 24.f;
 
-// A worker warp's shared memory: a ring of NST stages of two pages each, and the
-// records of the items in flight (at most one per page that is).
+// Decode phase's shared memory: every warp's ring of NST stages of two pages,
+// what the teams know of their splits, the rings' barriers.
 template <int D>
 struct DecQ4 {
   static constexpr int WARPS = kQ4Threads / 32;
   static constexpr int NST = 3;
   static constexpr int PAGE = Q4<D>::BYTES;
   static constexpr int STAGE = 2 * PAGE;
-  static constexpr int RECS = 8;  // a power of two above 2 NST
-  static constexpr int REC_OFF = WARPS * NST * STAGE;
-  static constexpr int BAR_OFF = REC_OFF + WARPS * RECS * 32;
+  static constexpr int TEAM_OFF = WARPS * NST * STAGE;
+  static constexpr int BAR_OFF = TEAM_OFF + WARPS / 2 * 64;  // a Team each
   static constexpr int SMEM = BAR_OFF + WARPS * NST * 8;
+};
+
+// One split (row, KV head, pages [p0, p0 + np) of the row), as its team's first
+// warp looked it up; np == 0: the queue is empty.
+struct __align__(16) Split {
+  int row, k, hk, tok;   // k: the row's position among the decode rows
+  int p0, np, keys, ns;  // keys: from page p0 to the row's end; ns: splits of the row
+  int part;              // record of the split's first head
+};
+struct __align__(16) Team {
+  Split split;
+  int failed, last;  // a wait of the team gave up; the split is its row's last to finish
 };
 
 // D = A B, from zero
@@ -68,25 +79,23 @@ __device__ __forceinline__ float bf16_part(float x, int i) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
-// What the consumer needs of an item, kept in shared memory from the moment its
-// pages are asked for.
-struct __align__(16) ItemRec {
-  int tok, hk, k, part, ns, np, rem, pad;  // rem: keys from the item's first page to the row's end
-};
-
-constexpr int kNoItem = 5;  // look-ahead stage: the queue is empty
-
 // The issue side of a warp's ring.
 struct IssueCursor {
-  const uint8_t* base;  // the pool at the item's KV head
-  const int32_t* btr;   // the item's first page-table entry
+  const uint8_t* base;  // the pool at the split's KV head
+  const int32_t* btr;   // the warp's first page-table entry
   int left, next;       // pages not yet asked for, pages asked for
   int ids, ids_next;    // lane j: page ids of this window of 32 pages and of the next
 };
 
-// Decode phase: every warp is independent and pulls items (row, KV head, span
-// of pages) until the queue is empty.  It takes its pages in pairs: one wait,
-// one maximum and one vote for 32 keys.
+// Decode phase: teams of warps (2, 4, 8 or 16 of the CTA, as the prologue chose)
+// pull splits until the queue is empty.  Each warp of a team runs its share of
+// the split's pages by itself, in pairs -- one wait and one vote for 32 keys --
+// and the team joins the results in shared memory, where the rings were.  A warp
+// to a split would need no joining but many more splits: with few or long rows
+// its pages keep it for tens of microseconds while other warps idle, and one
+// warp joins the row's records at the end.  256 rows of 8 KV heads and 700 to
+// 16384 keys: 372 us with a warp to a split of 64 pages, 331 us with four to 320;
+// 61 rows of 1 to 5003 keys, 2 KV heads, D = 64: 55 us and (eight to 48) 21 us.
 template <int D, int G>
 __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem) {
   using Q = Q4<D>;
@@ -98,7 +107,6 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
   // the four rows that one load of V touches lie on both halves of the 128-byte lines
   const int ra = gq ^ ((gq >> 1) & 1);
   const uint32_t ring = smem_u32(dsmem) + warp * NST * C::STAGE;
-  ItemRec* recs = reinterpret_cast<ItemRec*>(dsmem + C::REC_OFF) + warp * C::RECS;
   uint64_t* full = reinterpret_cast<uint64_t*>(dsmem + C::BAR_OFF) + warp * NST;
   if (lane == 0) {
     for (int i = 0; i < NST; ++i) mbar_init(full + i, 1);
@@ -106,80 +114,11 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
   }
   __syncwarp();
   const int n_items = p.hdr[H_NDEC_ITEMS];
-
-  // The next item is looked up while the current one runs, one dependent load
-  // per step: its id (stage 0), its entry (1), its row (2), the row's lengths
-  // (3), its first page ids (4).  The loaded words sit in one register, a lane
-  // each: 0 the id, 1 and 2 the entry (decode row, piece), 3 to 5 the row and
-  // its records, 6 to 8 its context, token and first table entry.
-  int nd = 0, nids = 0, stage_n = 0;
-  auto word = [&](int i) { return __shfl_sync(0xffffffffu, nd, i); };
-  auto dequeue = [&]() {
-    if (lane == 0) nd = atomicAdd(p.hdr + H_DEC_CTR, 1);
-    stage_n = 0;
-  };
-  auto item_pages = [&](int& p0, int& np) {
-    const int n_pages = (word(6) + kPage - 1) / kPage;
-    dec_piece(n_pages, p.hdr[H_SPLIT], p.hdr[H_GRADED], word(2), p0, np);
-  };
-  auto item_table = [&](int p0) -> const int32_t* {
-    const int off = word(8), row = word(3);
-    return p.bt + (p.bt_off != nullptr ? static_cast<int64_t>(off) : static_cast<int64_t>(row) * p.bt_stride) + p0;
-  };
-  auto look_ahead = [&]() {
-    if (stage_n == 0) {
-      const int id = word(0);
-      if (id >= n_items) {
-        stage_n = kNoItem;
-        return;
-      }
-      if (lane == 1 || lane == 2) nd = __ldg(reinterpret_cast<const int*>(p.dec_items + id / p.H_kv) + lane - 1);
-    } else if (stage_n == 1) {
-      const int k = word(1);
-      const int32_t* src = lane == 3 ? p.dec_rows : lane == 4 ? p.dec_part_base : p.dec_nsplit;
-      if (lane >= 3 && lane <= 5) nd = __ldg(src + k);
-    } else if (stage_n == 2) {
-      const int row = word(3);
-      const int32_t* src = lane == 6 ? p.ctx_lens : lane == 7 ? p.cu : p.bt_off;
-      if (lane == 6 || lane == 7 || (lane == 8 && src != nullptr)) nd = __ldg(src + row);
-    } else if (stage_n == 3) {
-      int p0, np;
-      item_pages(p0, np);
-      const int32_t* btr = item_table(p0);
-      if (lane < np) nids = __ldg(btr + lane);
-    } else {
-      return;
-    }
-    ++stage_n;
-  };
   IssueCursor iss{};
-  int n_begun = 0;  // items whose issue has begun
-  dequeue();
-  auto begin_item = [&]() {
-    int p0, np;
-    item_pages(p0, np);
-    const int id = word(0), hk = id - id / p.H_kv * p.H_kv;
-    iss.left = np;
-    iss.next = 0;
-    iss.base = p.kv_q4 + hk * Q::BYTES;
-    iss.btr = item_table(p0);
-    iss.ids_next = nids;
-    const int tok = word(7), k = word(1), part = word(4) + word(2) * p.H_q + hk * G, ns = word(5);
-    const int rem = word(6) - p0 * kPage;
-    if (lane == 0) recs[n_begun & (C::RECS - 1)] = ItemRec{tok, hk, k, part, ns, np, rem, 0};
-    ++n_begun;
-    dequeue();
-  };
-  // The next pair of pages of an item (its last may be alone) into stage `st`,
+  // The next pair of the warp's pages (the last may be alone) into stage `st`,
   // one bulk copy a page from lanes 0 and 1.
   int in_flight = 0;
-  auto issue = [&](int st) {
-    if (iss.left == 0) {
-      while (stage_n < 4) look_ahead();
-      if (stage_n == 4) begin_item();
-    } else if (stage_n < 4) {
-      look_ahead();
-    }
+  auto issue_pair = [&](int st) {
     if (iss.left == 0) return;
     const int w = iss.next & 31, n = min(iss.left, 2);
     if (w == 0) {
@@ -201,24 +140,30 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
     iss.left -= n;
     ++in_flight;
   };
-#pragma unroll 1
-  for (int i = 0; i < NST - 1; ++i) issue(i);
-
   bool failed = false;
-  uint32_t ph = 0;  // parity of the stages' current round
-  int st = 0;  // stage of the next pair
-  for (int item = 0; item < n_begun; ++item) {
-    const ItemRec* rec = recs + (item & (C::RECS - 1));
-    __syncwarp();
-    const int np = rec->np;
-    int rem = rec->rem;
+  int st = 0;       // stage of the next pair
+  uint32_t ph = 0;  // its parity
+  auto next_stage = [&]() {
+    if (++st == NST) {
+      st = 0;
+      ph ^= 1u;
+    }
+  };
+  // The warp's pages, np of them with `rem` keys from the first to the row's end.  Leaves O^T in acc -- the lane holds elements 32 g + 8 (gq / 2) + 2 i +
+  // gq % 2 of heads 2 tq and 2 tq + 1, with i = 2 m in acc[2 g + m][0, 1] and
+  // i = 2 m + 1 in acc[2 g + m][2, 3] -- and those heads' reference maxima (in
+  // log2 units) and sums.
+  float acc[NK][4], mu0, mu1, l0, l1;
+  const float sl2 = p.scale_log2;
+  constexpr float kRescaleLog2 = 8.f;  // raise the reference max only when it grows by 2^8
+  auto run_pages = [&](int tok, int hk, int np, int rem) {
     // B operand of S^T = K Q^T: lane (head gq, quarter tq) holds the eight elements of quarter tq
     // of every group.  The offsets' share of the scores, sum_g s_g (-136 sum q_g), is a product
     // over the groups too: its B operand holds -136 sum q_g in three bf16 parts, column by column
     // the groups of part 0, of part 1, ..., against the row's scales as they are stored.
     uint32_t qb[NG][4], ob0, ob1 = 0u;
     {
-      const bf16* q = p.q_rot + (static_cast<int64_t>(rec->tok) * p.H_q + rec->hk * G + gq) * D + 8 * tq;
+      const bf16* q = p.q_rot + (static_cast<int64_t>(tok) * p.H_q + hk * G + gq) * D + 8 * tq;
       float off[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -243,25 +188,20 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
         ob0 = tq < 3 ? *reinterpret_cast<const uint32_t*>(&lo) : 0u;
       }
     }
-    const float sl2 = p.scale_log2;
-    float acc[NK][4];
 #pragma unroll
     for (int j = 0; j < NK; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    float mu0 = -INFINITY, mu1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 tq and 2 tq + 1 (mu in log2 units)
-    constexpr float kRescaleLog2 = 8.f;  // raise the reference max only when it grows by 2^8
+    mu0 = mu1 = -INFINITY;
+    l0 = l1 = 0.f;
     for (int pi = 0; pi < np; pi += 2, rem -= 2 * kPage) {
       __syncwarp();  // every lane is done with the stage before
-      issue(st == 0 ? NST - 1 : st - 1);
+      issue_pair(st == 0 ? NST - 1 : st - 1);
       if (!mbar_wait(full + st, ph, nullptr)) {
         failed = true;
         break;
       }
       --in_flight;
       const uint32_t stage = ring + st * C::STAGE;
-      if (++st == NST) {
-        st = 0;
-        ph ^= 1u;
-      }
+      next_stage();
       const int n_half = pi + 1 < np ? 2 : 1;
       // S^T: lane holds (row ra, heads 2 tq, 2 tq + 1) and (row ra + 8, same heads) of each page
       float s[2][4];
@@ -375,51 +315,130 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
         }
       }
     }
-    if (failed) break;
-    // O^T: lane holds elements 32 g + 8 (gq / 2) + 2 i + gq % 2 of heads 2 tq, 2 tq + 1, with i = 2 m in
-    // acc[2 g + m][0, 1] and i = 2 m + 1 in acc[2 g + m][2, 3]
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);
       l1 += __shfl_xor_sync(0xffffffffu, l1, o);
     }
-    const int tok = rec->tok, hk = rec->hk, ns = rec->ns, part = rec->part;
-    const int d0 = 8 * (gq >> 1) + (gq & 1);
+  };
+  const int d0 = 8 * (gq >> 1) + (gq & 1);  // the lane's first element
+
+  const int T = p.hdr[H_TEAM], team = warp / T, tw = warp - team * T, tt = threadIdx.x - team * T * 32;
+  static_assert(sizeof(Team) <= 64, "team words");
+  Team* tm = reinterpret_cast<Team*>(dsmem + C::TEAM_OFF) + team;
+  const Split* split = &tm->split;
+  float* s_acc = reinterpret_cast<float*>(dsmem + team * T * NST * C::STAGE);  // [warp][head][D]
+  float* s_ml = s_acc + T * G * D;                                             // [warp][head][max, sum]
+  static_assert(G * (D + 2) * 4 <= NST * C::STAGE, "a warp's joined results exceed its ring");
+  auto team_sync = [&]() { named_bar_sync(1 + team, T * 32); };
+  // The team's first warp looks the next split up: its id, its table entry, then
+  // the row's words together, each step while the team is at something else.
+  // The id is not taken before the team has run its pages: it would be held back
+  // from a team that is free sooner.
+  int id = 0;
+  int2 entry = make_int2(0, 0);
+  auto take_id = [&]() {
+    if (tt == 0) id = atomicAdd(p.hdr + H_DEC_CTR, 1);
+  };
+  auto load_entry = [&]() {
+    if (tw != 0) return;
+    id = __shfl_sync(0xffffffffu, id, 0);
+    if (id < n_items) entry = __ldg(p.dec_items + id / p.H_kv);  // (decode row and row, split)
+  };
+  auto load_split = [&]() {
+    if (tw != 0) return;
+    Split x{};
+    if (id < n_items) {
+      const int size = p.hdr[H_SPLIT];
+      x.hk = id % p.H_kv;
+      x.k = entry.x & 0xffff;
+      x.row = entry.x >> 16;
+      const int ctx = __ldg(p.ctx_lens + x.row);
+      x.tok = __ldg(p.cu + x.row);
+      x.ns = __ldg(p.dec_nsplit + x.k);
+      x.part = __ldg(p.dec_part_base + x.k) + entry.y * p.H_q + x.hk * G;
+      x.p0 = entry.y * size;
+      x.np = min(size, (ctx + kPage - 1) / kPage - x.p0);
+      x.keys = ctx - x.p0 * kPage;
+    }
+    if (lane == 0) tm->split = x;
+  };
+  if (tt == 0) tm->failed = 0;
+  take_id();
+  load_entry();
+  load_split();
+  team_sync();
+  while (split->np > 0) {
+    {
+      const int np = split->np, hk = split->hk;
+      const int share = 2 * ((np + 2 * T - 1) / (2 * T));  // pages to a warp, in pairs
+      const int w0 = tw * share, mine = max(0, min(share, np - w0));
+      iss.left = mine;
+      iss.next = 0;
+      iss.base = p.kv_q4 + hk * Q::BYTES;
+      iss.btr = row_table(p, split->row) + split->p0 + w0;
+      iss.ids_next = lane < mine ? __ldg(iss.btr + lane) : 0;
+#pragma unroll 1
+      for (int i = 0, s0 = st; i < NST - 1; ++i, s0 = s0 == NST - 1 ? 0 : s0 + 1) issue_pair(s0);
+      run_pages(split->tok, hk, mine, split->keys - w0 * kPage);
+    }
+    take_id();
+    const int tok = split->tok, hk = split->hk, k = split->k, ns = split->ns, part = split->part;
+    if (failed && lane == 0) tm->failed = 1;
+    team_sync();  // every warp is done with its ring, and with the split's words
+    if (tm->failed) {
+      failed = true;
+      break;
+    }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int hh = 2 * tq + e;
+    for (int x = 0; x < 2; ++x) {
+      const int hh = 2 * tq + x;
       if (hh >= G) continue;
-      const float L = e == 0 ? l0 : l1, M = e == 0 ? mu0 : mu1;
-      if (ns == 1) {
-        const float inv = 1.f / L;
-        bf16* dst = p.out + (static_cast<int64_t>(tok) * p.H_q + hk * G + hh) * D + d0;
+      float* dst = s_acc + (tw * G + hh) * D + d0;
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          dst[32 * (j >> 1) + 4 * (j & 1)] = __float2bfloat16_rn(acc[j][e] * inv);
-          dst[32 * (j >> 1) + 4 * (j & 1) + 2] = __float2bfloat16_rn(acc[j][2 + e] * inv);
-        }
-      } else {
-        const int64_t r = part + hh;
-        float* dst = p.part_acc + r * D + d0;
-#pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          dst[32 * (j >> 1) + 4 * (j & 1)] = acc[j][e];
-          dst[32 * (j >> 1) + 4 * (j & 1) + 2] = acc[j][2 + e];
-        }
-        if (gq == 0) *reinterpret_cast<float2*>(p.part_ml + r * 2) = make_float2(M, L);
+      for (int j = 0; j < NK; ++j) {
+        dst[32 * (j >> 1) + 4 * (j & 1)] = acc[j][x];
+        dst[32 * (j >> 1) + 4 * (j & 1) + 2] = acc[j][2 + x];
+      }
+      if (gq == 0) {
+        s_ml[(tw * G + hh) * 2] = x == 0 ? mu0 : mu1;
+        s_ml[(tw * G + hh) * 2 + 1] = x == 0 ? l0 : l1;
       }
     }
-    if (ns > 1) {
-      const int k = rec->k;
-      __threadfence();  // this split's records are visible before it is counted
-      __syncwarp();
-      int last = 0;
-      if (lane == 0) last = atomicAdd(p.dec_cnt + k * p.H_kv + hk, 1) == ns - 1;
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (last) {
-        __threadfence();
-        merge_splits<D>(p, k, hk * G, G, tok, ns, lane);
+    team_sync();
+    for (int c = tt; c < G * D; c += T * 32) {
+      const int hh = c / D;
+      float M = -INFINITY, L = 0.f, o = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < T; ++w) M = fmaxf(M, s_ml[(w * G + hh) * 2]);
+#pragma unroll 4
+      for (int w = 0; w < T; ++w) {
+        const float x = ex2(s_ml[(w * G + hh) * 2] - M);
+        L += x * s_ml[(w * G + hh) * 2 + 1];
+        o += x * s_acc[w * G * D + c];
       }
+      if (ns == 1) {
+        p.out[(static_cast<int64_t>(tok) * p.H_q + hk * G) * D + c] = __float2bfloat16_rn(o / L);
+      } else {
+        p.part_acc[static_cast<int64_t>(part) * D + c] = o;
+        if (c % D == 0) *reinterpret_cast<float2*>(p.part_ml + (static_cast<int64_t>(part) + hh) * 2) = make_float2(M, L);
+      }
+    }
+    fence_proxy_async_smem();  // the joined results are ordered before the next split's copies
+    load_entry();
+    if (ns > 1) {
+      __threadfence();  // this split's records are visible before it is counted
+      team_sync();
+      if (tt == 0) tm->last = atomicAdd(p.dec_cnt + k * p.H_kv + hk, 1) == ns - 1;
+      load_split();
+      team_sync();
+      if (tm->last) {
+        __threadfence();
+        for (int hh = tw; hh < G; hh += T) merge_splits<D, 16>(p, k, hk * G + hh, 1, tok, ns, lane);
+      }
+    } else {
+      load_split();
+      team_sync();
     }
   }
   if (failed) {
@@ -427,10 +446,7 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
     // let copies already in flight land before the CTA's shared memory is released
     for (; in_flight > 0; --in_flight) {
       mbar_wait(full + st, ph, nullptr, 200000000ull);
-      if (++st == NST) {
-        st = 0;
-        ph ^= 1u;
-      }
+      next_stage();
     }
   }
   __syncwarp();
@@ -523,7 +539,7 @@ extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* 
   if (rc != MS_OK || empty) return rc;
   p.kv_q4 = static_cast<const uint8_t*>(kv_cache);
   p.dec_workers = p.num_sms * (kQ4Threads / 32);
-  p.graded = 1;
+  p.dec_teams = 1;
   p.tile_cycles = kQ4TileCycles;
   p.dec_bytes_cycle = kQ4DecodeBytesPerCycle;
   p.key_bytes = q4_block_bytes(D) / 16.f;

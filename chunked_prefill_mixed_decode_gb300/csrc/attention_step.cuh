@@ -46,7 +46,7 @@ enum {
   H_NPART = 8,
   H_CHUNK_CTAS = 9,  // CTAs that start on chunk work (the rest start on decodes)
   H_CLOCK_MHZ = 10,  // SM clock the last call ran at (kept across calls; 0 in a fresh workspace)
-  H_GRADED = 11,     // decode rows end in pieces of falling size (dec_piece)
+  H_TEAM = 11,       // warps that share a decode item, where the kernel runs them in teams
   H_WORDS = 64
 };
 
@@ -67,7 +67,7 @@ struct AttnParams {
   int32_t dec_workers;       // decode worker warps in the grid
   int32_t num_sms;
   int32_t clear_status;      // the prologue zeroes the status word first (scratch owned by the library)
-  int32_t graded;            // end decode rows in pieces of falling size where the workspace holds them
+  int32_t dec_teams;         // decode items go to teams of warps (4-bit pools): choose split and team size
   int32_t force_chunk_ctas;  // test hook: CTAs that start on chunk work (-1: the cost model decides)
   float sm_mhz;              // cost model: the SM clock when no call has measured it yet,
   float hbm_gbs;             // and the HBM bandwidth that caps decode
@@ -143,54 +143,9 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
-// A decode row of n pages is cut into pieces of `split` pages.  Graded: whole
-// pieces as long as two fit, and the rest, which is below two pieces, as it is
-// where it is below one, else as about a half, a third and a sixth of it.  The
-// queue runs whole pieces first, then the halves, the thirds, the sixths, so
-// that the warps end on short pieces: with about three pieces a warp (64 rows
-// of 32 heads and 512 to 4096 keys on 152 SMs of 16 warps) the last piece
-// otherwise leaves a sixth of the warps' time idle.  A row has at most
-// n / split + 2 graded pieces.
-constexpr int kMinGradedSplit = 36;  // keeps n / 36 + 2 pieces within the workspace's n / 32 + 2
-
-struct DecCut {
-  unsigned whole, rest;  // whole pieces, pages after them
-  int tail;              // pieces of the rest: 1 or 3
-};
-
-__device__ __forceinline__ DecCut dec_cut(unsigned n, unsigned split) {
-  DecCut r;
-  r.whole = n >= 2 * split ? n / split - 1 : 0;
-  r.rest = n - r.whole * split;
-  r.tail = r.rest >= split ? 3 : 1;
-  return r;
-}
-
-__device__ __forceinline__ int dec_pieces(unsigned n, unsigned split, bool graded) {
-  if (!graded) return static_cast<int>((n + split - 1) / split);
-  const DecCut c = dec_cut(n, split);
-  return static_cast<int>(c.whole) + c.tail;
-}
-
-// pages [p0, p0 + np) of piece i of a row of n pages
-__device__ __forceinline__ void dec_piece(int n, int split, int graded, int i, int& p0, int& np) {
-  p0 = i * split;
-  np = min(split, n - p0);
-  if (!graded) return;
-  const DecCut c = dec_cut(static_cast<unsigned>(n), static_cast<unsigned>(split));
-  const int w = static_cast<int>(c.whole), rest = static_cast<int>(c.rest);
-  if (i < w) return;
-  p0 = w * split;
-  np = rest;
-  if (c.tail == 1) return;
-  const int a = (rest / 2 + 1) & ~1, b = ((rest - a) * 2 / 3 + 1) & ~1;  // even: pages go in pairs
-  p0 += i == w ? 0 : i == w + 1 ? a : a + b;
-  np = i == w ? a : i == w + 1 ? b : rest - a - b;
-}
-
-// Work items of one row: decode pieces, or pairs of 128-row Q tiles.
-__device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsigned split, bool graded) {
-  if (!chunk) return dec_pieces(static_cast<unsigned>(c + kPage) / kPage, split, graded);
+// Work items of one row: decode splits of `split` pages, or pairs of 128-row Q tiles.
+__device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsigned split) {
+  if (!chunk) return static_cast<int>((static_cast<unsigned>(c + kPage) / kPage + split - 1) / split);
   const int n_qt = (d + tpt - 1) / tpt;
   return (n_qt + 1) >> 1;
 }
@@ -313,35 +268,65 @@ __device__ __forceinline__ int decode_split(const AttnParams& p, int64_t dec_pag
                       : cdiv64(num, den);
   const int64_t min_split = p.G >= 4 ? (with_chunks ? 4 : 2) * kMinSplitPages : kMinSplitPages;
   split = split < min_split ? min_split : (split > kMaxSplitPages ? kMaxSplitPages : split);
-  if (p.graded) split = split < kMinGradedSplit ? kMinGradedSplit : split & ~int64_t{1};
   return static_cast<int>(split);
 }
 
-// Whether the decode rows' graded pieces fit in the workspace.
-__device__ __forceinline__ bool decode_graded(const AttnParams& p, int64_t dec_pages, int n_dec, int split) {
-  if (!p.graded) return false;
-  const int64_t most = dec_pages / split + 2 * static_cast<int64_t>(n_dec);
-  return most * p.H_kv <= p.max_dec_items && most * p.H_q <= p.max_partials;
+// Split and team size of decode rows that teams of 2, 4, 8 or 16 warps of a CTA
+// share split by split.  An estimate in microseconds for every pair of a team
+// size (lane / 8) and a split (lane % 8), the smallest wins:
+//     o max(1, x) + max(c P / W + 0.21 L, 0.45 L y) + 0.09 n max(1, G / team)
+// x: splits over teams; y: x, rounded up while there are two rounds at most;
+// P / W: pages per warp; L = min(split, longest row) / team: pages of a warp's
+// share; n: splits of the longest row, which one team joins; o = 16, 11, 9, 9.4 by
+// team size: the cost of a split around its pages; c = 1.15: a page's with the
+// SM full (D = 128).  Fitted to sweeps of 27 pairs over 28 steps (1 to 512 rows
+// of 1 to 32 KV heads, 1 to 131072 keys, 19 to 420 us): its choice is 2.3 % slower
+// than the best pair on average, 11 % but for one step (4 rows of 64K to 128K
+// keys: 20 %).  Called by whole warps.
+struct DecPlan {
+  int split, team;
+};
+
+// The pair that lane `lane` tries: 2, 4, 8, 16, 24, 32, 48 or 80 pages to a warp
+// (and 128 in teams of 2 and 4) that give a team 32 pages or more, which the
+// workspace's item and record counts allow.
+__device__ __forceinline__ DecPlan dec_candidate(int lane) {
+  const int small = 3 - (lane >> 3);  // sizes left out for this team
+  uint64_t sizes = 0x5030201810080402ull;
+  if (small > 0) sizes = (sizes >> (8 * small)) | ((small == 1 ? 0x5050505050505050ull : 0x8080808080808080ull) << (64 - 8 * small));
+  const int per_warp = static_cast<int>(sizes >> (8 * (lane & 7))) & 255;
+  const int team = 2 << (lane >> 3);
+  return {team * per_warp, team};
 }
 
-// Entries of decode row q (queue order) in the item table: `before` items and
-// `before3` rows of three tail pieces come ahead of it.  Graded rows put their
-// whole pieces first, then every row's first tail piece, then the second, then
-// the third; n_whole, n_dec and n3 are the totals.
-__device__ __forceinline__ void write_dec_entries(const AttnParams& p, int q, int items, int before, int before3, bool graded,
-                                                  bool three, int n_whole, int n_dec, int n3) {
-  if (!graded) {
-    for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(q, i);
-    return;
-  }
-  const int whole = items - (three ? 3 : 1);
-  const int first = before - q - 2 * before3;  // whole pieces ahead
-  for (int i = 0; i < whole; ++i) p.dec_items[first + i] = make_int2(q, i);
-  p.dec_items[n_whole + q] = make_int2(q, whole);
-  if (three) {
-    p.dec_items[n_whole + n_dec + before3] = make_int2(q, whole + 1);
-    p.dec_items[n_whole + n_dec + n3 + before3] = make_int2(q, whole + 2);
-  }
+__device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_pages, int n_dec, int max_pages,
+                                               bool with_chunks) {
+  if (!p.dec_teams || n_dec == 0) return {decode_split(p, dec_pages, with_chunks), 1};
+  const int lane = threadIdx.x & 31;
+  const DecPlan cand = dec_candidate(lane);
+  const float team = static_cast<float>(cand.team), split = static_cast<float>(cand.split);
+  const float P = static_cast<float>(dec_pages) * p.H_kv, n = static_cast<float>(n_dec);
+  const float W = static_cast<float>(p.dec_workers), mx = static_cast<float>(max_pages);
+  const float splits = fmaxf(n, __fdividef(static_cast<float>(dec_pages), split) + 0.5f * n) * p.H_kv;
+  const float x = __fdividef(splits * team, W), y = x <= 2.f ? ceilf(x) : x;
+  const float L = __fdividef(fminf(split, mx), team);
+  const float o = cand.team == 2 ? 16.f : cand.team == 4 ? 11.f : cand.team == 8 ? 9.f : 9.4f;
+  const float t = o * fmaxf(1.f, x) + fmaxf(1.15f * __fdividef(P, W) + 0.21f * L, 0.45f * L * y) +
+                  0.09f * __fdividef(mx, split) * fmaxf(1.f, __fdividef(static_cast<float>(p.G), team));
+  const unsigned best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | static_cast<unsigned>(lane));
+  return dec_candidate(static_cast<int>(best & 31u));
+}
+
+// First word of a decode row's table entries: its position k in the list, and for
+// teams, which look every word of a split up at once, its row above that.
+__device__ __forceinline__ int dec_entry(const AttnParams& p, int k, int row) {
+  return p.dec_teams ? k | (row << 16) : k;
+}
+
+// Warps that the decode items keep busy at a time, at most.
+__device__ __forceinline__ int dec_item_warps(int64_t items, int team) {
+  const int64_t n = items * team;
+  return n < 0x7fffffff ? static_cast<int>(n) : 0x7fffffff;
 }
 
 // Header of a call whose metadata failed validation: status set, no work.
@@ -350,7 +335,7 @@ __device__ __forceinline__ void header_bad_meta(int32_t* hdr) {
   hdr[H_DEC_CTR] = hdr[H_CH_CTR] = 0;
   hdr[H_NDEC] = hdr[H_NDEC_ITEMS] = hdr[H_NCH] = hdr[H_NCH_ITEMS] = hdr[H_NPART] = 0;
   hdr[H_SPLIT] = kMinSplitPages;
-  hdr[H_GRADED] = 0;
+  hdr[H_TEAM] = 1;
   hdr[H_CHUNK_CTAS] = 0;
 }
 
@@ -385,11 +370,12 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   }
   const bool is_dec = d == 1, is_ch = d > 1;
   const int64_t dec_pages = warp_sum31(is_dec ? (ctx + kPage - 1) / kPage : 0);
-  const int split = decode_split(p, dec_pages, __any_sync(0xffffffffu, is_ch));
   const int tpt = 128 / p.G;
   const unsigned bd = __ballot_sync(0xffffffffu, is_dec), bc = __ballot_sync(0xffffffffu, is_ch);
   const int n_dec = __popc(bd), n_ch = __popc(bc);
-  const bool graded = decode_graded(p, dec_pages, n_dec, split);
+  const int max_pages = __reduce_max_sync(0xffffffffu, is_dec ? (ctx + kPage - 1) / kPage : 0);
+  const DecPlan plan = decode_plan(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  const int split = plan.split;
   // position in its list, then rank by key within the list (longest first):
   // the keys sit in shared memory by list position, zero-padded, read 16 bytes at a time
   __shared__ __align__(16) uint32_t s_key[2][32];
@@ -411,14 +397,12 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const uint4 v = k4[m];
     rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
   }
-  const int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split), graded) : 0;
-  const bool three = graded && is_dec && items >= 3;  // a row has one item or at least three
+  const int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
   const int q = (is_ch ? n_dec : 0) + rank;  // queue position
-  if (listed) s_items[q] = items | (three ? 1 << 30 : 0);
+  if (listed) s_items[q] = items;
   __syncwarp();
-  const unsigned b3 = __ballot_sync(0xffffffffu, (s_items[lane] >> 30) != 0);  // by queue position
   {  // exclusive prefix over queue positions, one per lane
-    const int v = s_items[lane] & ((1 << 30) - 1);
+    const int v = s_items[lane];
     int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -444,16 +428,13 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     p.dec_rows[rank] = lane;
     p.dec_part_base[rank] = static_cast<int32_t>(static_cast<int64_t>(before) * p.H_q);
     p.dec_nsplit[rank] = items;
-    if (!dec_over) {
-      const int n3 = __popc(b3);
-      write_dec_entries(p, rank, items, before, __popc(b3 & ((1u << rank) - 1u)), graded, three,
-                        dec_tot - n_dec - 2 * n3, n_dec, n3);
-    }
+    if (!dec_over)
+      for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(dec_entry(p, rank, lane), i);
   }
   if (is_ch) p.ch_rows[rank] = lane;
   const SmSplit sp = chunk_cta_split(p, static_cast<float>(tiles), static_cast<float>(dec_pages),
                                      ch_over ? 0 : static_cast<int>(n_ch_items),
-                                     dec_over ? 0 : static_cast<int>(n_dec_items), static_cast<float>(chunk_keys),
+                                     dec_over ? 0 : dec_item_warps(n_dec_items, plan.team), static_cast<float>(chunk_keys),
                                      measured_mhz, lane);
   // the chunk rows' items (pairs x H_kv of them per row), the whole warp on one row at
   // a time; then the split counters, 16 bytes per store
@@ -480,7 +461,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_DEC_CTR] = 0;
     hdr[H_CH_CTR] = 0;
     hdr[H_SPLIT] = split;
-    hdr[H_GRADED] = graded;
+    hdr[H_TEAM] = plan.team;
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -499,7 +480,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   extern __shared__ __align__(16) int32_t psm[];
   __shared__ int s_warp[32];
   __shared__ long long s_sum[3][32];
-  __shared__ unsigned s_cnt[2][32];
+  __shared__ unsigned s_cnt[3][32];
   __shared__ unsigned long long s_tiles;
   __shared__ SmSplit s_split;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
@@ -522,7 +503,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   const int measured_mhz = warp == 0 ? hdr[H_CLOCK_MHZ] : 0;  // for the SM split, loaded early
   // 1. load and validate the rows; count decodes, chunks, context and decode pages
   int64_t my_ctx = 0, my_pages = 0, my_ch_keys = 0;
-  unsigned my_dec = 0, my_ch = 0;
+  unsigned my_dec = 0, my_ch = 0, my_max = 0;
   int my_bad = 0;
   for (int s = tid; s < S; s += nt) {
     const int32_t a = p.cu[s], b = p.cu[s + 1];
@@ -543,7 +524,11 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       my_ctx += ctx;
       my_dec += d == 1;
       my_ch += d > 1;
-      if (d == 1) my_pages += (ctx + kPage - 1) / kPage;
+      if (d == 1) {
+        const unsigned n = static_cast<unsigned>(ctx + kPage - 1) / kPage;
+        my_pages += n;
+        my_max = max(my_max, n);
+      }
       if (d > 1) my_ch_keys += ctx;
     }
   }
@@ -552,30 +537,33 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   my_ch_keys = warp_sum64(my_ch_keys);
   my_dec = __reduce_add_sync(0xffffffffu, my_dec);
   my_ch = __reduce_add_sync(0xffffffffu, my_ch);
+  my_max = __reduce_max_sync(0xffffffffu, my_max);
   if (lane == 0) {
     s_sum[0][warp] = my_ctx;
     s_sum[1][warp] = my_pages;
     s_sum[2][warp] = my_ch_keys;
     s_cnt[0][warp] = my_dec;
     s_cnt[1][warp] = my_ch;
+    s_cnt[2][warp] = my_max;
   }
   const int bad = __syncthreads_or(my_bad);
   int64_t ctx_sum = 0, dec_pages = 0, chunk_keys = 0;
-  int n_dec = 0, n_ch = 0;
+  int n_dec = 0, n_ch = 0, max_pages = 0;
   for (int j = 0; j < nw; ++j) {
     ctx_sum += s_sum[0][j];
     dec_pages += s_sum[1][j];
     chunk_keys += s_sum[2][j];
     n_dec += static_cast<int>(s_cnt[0][j]);
     n_ch += static_cast<int>(s_cnt[1][j]);
+    max_pages = max(max_pages, static_cast<int>(s_cnt[2][j]));
   }
   if (bad || ctx_sum > p.context_total) {
     if (tid == 0) header_bad_meta(hdr);
     return;
   }
   // 2. decode split size
-  const int split = decode_split(p, dec_pages, n_ch > 0);
-  const bool graded = decode_graded(p, dec_pages, n_dec, split);
+  const DecPlan plan = decode_plan(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  const int split = plan.split;
   const int tpt = 128 / p.G;
   const unsigned split32 = static_cast<unsigned>(split);
   // 3. the two lists in input order: decode rows at lst[0, n_dec), chunk rows after them
@@ -626,23 +614,16 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     }
     const int row = lst[j], c = rc[row], d = rd[row];
     (ch ? p.ch_rows : p.dec_rows)[rank] = row;
-    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32, graded);
+    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32);
     if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(chunk_tiles(c, d, tpt)) * p.H_kv);
   }
   __syncthreads();
   // 6. exclusive prefix of the item counts in queue order (decode rows, then chunk rows)
-  // (and, graded, of the decode rows with three tail pieces, where the keys were)
-  int run = 0, run3 = 0;
-  int32_t* pref3 = reinterpret_cast<int32_t*>(key);
+  int run = 0;
   for (int base = 0; base < n_tot; base += nt) {  // uniform
     const int q = base + tid;
     const int v = q < n_tot ? pref[q] : 0;
     int tot;
-    if (graded) {
-      const int o3 = block_scan(q < n_dec && v >= 3, s_warp, tot);
-      if (q < n_dec) pref3[q] = run3 + o3;
-      run3 += tot;
-    }
     const int o = block_scan(v, s_warp, tot);
     if (q < n_tot) {
       pref[q] = run + o;
@@ -660,20 +641,21 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   const int64_t n_ch_items = static_cast<int64_t>(ch_tot) * p.H_kv;
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
   const bool ch_over = n_ch_items > p.max_ch_items;
-  // 7. item tables.  Decode rows, a thread per row: (row k, split i), one entry
-  // per split (a work item is an entry and a KV head).
+  // 7. item tables.  Decode rows, a thread per row: entry pref[q] + i -> (row
+  // k, split i), one entry per split (a work item is an entry and a KV head).
   // Then the SM split, which also orders the chunk items; chunk rows, a warp
   // per row: one entry per item, (row k, KV head and Q-tile pair).  Then the
   // split counters of every (decode row, KV head), zeroed 16 bytes at a time.
   for (int q = tid; q < n_dec && !dec_over; q += nt) {
     const int cnt = pref[q + 1] - pref[q];
-    write_dec_entries(p, q, cnt, pref[q], graded ? pref3[q] : 0, graded, cnt >= 3, dec_tot - n_dec - 2 * run3, n_dec,
-                      run3);
+    int2* out = p.dec_items + pref[q];
+    const int x = dec_entry(p, q, p.dec_rows[q]);
+    for (int i = 0; i < cnt; ++i) out[i] = make_int2(x, i);
   }
   if (warp == 0) {
     const SmSplit sp = chunk_cta_split(p, static_cast<float>(s_tiles), static_cast<float>(dec_pages),
                                        ch_over ? 0 : static_cast<int>(n_ch_items),
-                                       dec_over ? 0 : static_cast<int>(n_dec_items), static_cast<float>(chunk_keys),
+                                       dec_over ? 0 : dec_item_warps(n_dec_items, plan.team), static_cast<float>(chunk_keys),
                                        measured_mhz, lane);
     if (lane == 0) s_split = sp;
   }
@@ -701,7 +683,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_DEC_CTR] = 0;
       hdr[H_CH_CTR] = 0;
       hdr[H_SPLIT] = static_cast<int32_t>(split);
-      hdr[H_GRADED] = graded;
+      hdr[H_TEAM] = plan.team;
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }
@@ -719,8 +701,8 @@ __global__ void __launch_bounds__(1024, 1) prologue_kernel(AttnParams p) {
 
 // Merge the ns split records of decode row k for query heads h0 .. h0+nh-1
 // into bf16 output (one warp; lane owns D/32 columns).  Records written by
-// other SMs are read past L1.
-template <int D>
+// other SMs are read past L1.  U: records in flight at a time.
+template <int D, int U = 4>
 __device__ __forceinline__ void merge_splits(const AttnParams& p, int k, int h0, int nh, int tok, int ns,
                                              int lane) {
   constexpr int EPL = D / 32;
@@ -745,7 +727,7 @@ __device__ __forceinline__ void merge_splits(const AttnParams& p, int k, int h0,
         L += w * ml.y;
       }
       const int nj = min(32, ns - j0);
-#pragma unroll 4
+#pragma unroll U
       for (int jj = 0; jj < nj; ++jj) {
         const float wj = __shfl_sync(0xffffffffu, w, jj);
         const float* src = p.part_acc + (base + static_cast<int64_t>(j0 + jj) * p.H_q) * D + lane * EPL;
@@ -1003,7 +985,7 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.G = G;
   p.num_sms = sms;
   p.clear_status = clear_status ? 1 : 0;
-  p.graded = 0;
+  p.dec_teams = 0;
   p.test_stall = stall_limit_ns > 0 ? 1 : 0;
   p.wait_limit_ns = stall_limit_ns > 0 ? static_cast<uint64_t>(stall_limit_ns) : 2000000000ull;
   p.scale_log2 = scale * 1.4426950408889634f;
