@@ -748,22 +748,35 @@ def q4_block_bytes(D: int) -> int:
     return n
 
 
+_Q4_BLOCK = {64: 1152, 128: 2304}  # ms_q4_block_bytes, without a call per step
+
+
 def _pool_q4(kv_cache, D: int) -> int:
     """Check a 4-bit pool for head dim D; returns its H_kv."""
     import torch
+    if D not in _Q4_BLOCK:
+        raise ValueError(f"D must be 64 or 128, got {D}")
     if kv_cache is None or kv_cache.dim() != 3:
         raise ValueError("kv_cache must be [pages, H_kv, q4_block_bytes(D)]")
-    _dev(kv_cache, "kv_cache", torch.uint8, (kv_cache.shape[0], kv_cache.shape[1], q4_block_bytes(D)))
-    return kv_cache.shape[1]
+    pages, H_kv, _ = kv_cache.shape
+    _dev(kv_cache, "kv_cache", torch.uint8, (pages, H_kv, _Q4_BLOCK[D]))
+    return H_kv
 
 
-def _on_current_gpu(names: str, *tensors) -> None:
-    """_on_one_gpu, and that GPU the current one: the library launches on the current device."""
+def _stream_of(stream, names: str, *tensors) -> int:
+    """The stream handle of a call on these tensors (None entries skipped): all of them on one GPU, and that GPU
+    the current one, on which the library launches.  None is the GPU's current stream."""
     import torch
-    _on_one_gpu(names, *tensors)
-    dev = next(t for t in tensors if t is not None).get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            _on_one_gpu(names, *tensors)  # raises, naming the tensor
+    current = torch._C._cuda_getDevice()
+    if dev != current:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 def kv_append_rope_q4(q, k, v, positions, slot_mapping, cos_tab, sin_tab, kv_cache, q_rot=None, dev_status=None,
@@ -788,11 +801,12 @@ def kv_append_rope_q4(q, k, v, positions, slot_mapping, cos_tab, sin_tab, kv_cac
     _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
     if dev_status is not None:
         _dev(dev_status, "dev_status", torch.int32, min_numel=1)
-    _on_current_gpu("q k v q_rot positions slot_mapping cos_tab sin_tab kv_cache dev_status", q, k, v, q_rot, positions,
-                    slot_mapping, cos_tab, sin_tab, kv_cache, dev_status)
-    rc = lib().ms_kv_append_rope_q4(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(slot_mapping), T, _ptr(cos_tab),
-                                    _ptr(sin_tab), cos_tab.shape[0], _ptr(kv_cache), kv_cache.shape[0], _ptr(q_rot),
-                                    H_q, H_kv, D, PAGE_SIZE, _ptr(dev_status), _stream(stream))
+    st = _stream_of(stream, "q k v q_rot positions slot_mapping cos_tab sin_tab kv_cache dev_status", q, k, v, q_rot,
+                    positions, slot_mapping, cos_tab, sin_tab, kv_cache, dev_status)
+    rc = lib().ms_kv_append_rope_q4(q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
+                                    slot_mapping.data_ptr(), T, cos_tab.data_ptr(), sin_tab.data_ptr(),
+                                    cos_tab.shape[0], kv_cache.data_ptr(), kv_cache.shape[0], q_rot.data_ptr(), H_q,
+                                    H_kv, D, PAGE_SIZE, _ptr(dev_status), st)
     _check(rc, "ms_kv_append_rope_q4")
 
 
@@ -809,9 +823,9 @@ def kv_read_q4(kv_cache, slots, k_out, v_out, dev_status=None, stream=None) -> N
     _dev(slots, "slots", torch.int32, min_numel=n)
     if dev_status is not None:
         _dev(dev_status, "dev_status", torch.int32, min_numel=1)
-    _on_current_gpu("kv_cache slots k_out v_out dev_status", kv_cache, slots, k_out, v_out, dev_status)
-    rc = lib().ms_kv_read_q4(_ptr(kv_cache), kv_cache.shape[0], _ptr(slots), n, _ptr(k_out), _ptr(v_out), H_kv, D,
-                             PAGE_SIZE, _ptr(dev_status), _stream(stream))
+    st = _stream_of(stream, "kv_cache slots k_out v_out dev_status", kv_cache, slots, k_out, v_out, dev_status)
+    rc = lib().ms_kv_read_q4(kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), n, k_out.data_ptr(),
+                             v_out.data_ptr(), H_kv, D, PAGE_SIZE, _ptr(dev_status), st)
     _check(rc, "ms_kv_read_q4")
 
 
@@ -842,15 +856,15 @@ def mixed_step_attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_
         stride, bt_len = 0, block_tables.numel()
     _dev(out, "out", torch.bfloat16, (T, H_q, D))
     _dev(workspace, "workspace", None)
-    _on_current_gpu("q_rot kv_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace", q_rot,
-                    kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out, workspace)
+    st = _stream_of(stream, "q_rot kv_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace",
+                    q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out, workspace)
     if scale is None:
         scale = float(D) ** -0.5
-    rc = lib().ms_mixed_step_attention_q4(_ptr(q_rot), _ptr(kv_cache), kv_cache.shape[0], _ptr(cu_seqlens_q),
-                                          _ptr(q_start_pos), _ptr(context_lens), _ptr(block_tables), _ptr(bt_offsets),
-                                          bt_len, stride, S, T, int(context_total), H_q, H_kv, D, PAGE_SIZE,
-                                          float(scale), _ptr(out), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    rc = lib().ms_mixed_step_attention_q4(q_rot.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+                                          cu_seqlens_q.data_ptr(), q_start_pos.data_ptr(), context_lens.data_ptr(),
+                                          block_tables.data_ptr(), _ptr(bt_offsets), bt_len, stride, S, T,
+                                          int(context_total), H_q, H_kv, D, PAGE_SIZE, float(scale), out.data_ptr(),
+                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
     _check(rc, "ms_mixed_step_attention_q4")
 
 
@@ -902,16 +916,16 @@ def build_batch_metadata_device(cached_lens, new_tokens, page_tables, num_pages:
         _dev(info, "info", i32, min_numel=4)
     if dev_status is not None:
         _dev(dev_status, "dev_status", i32, min_numel=1)
-    _on_current_gpu("page_tables cached_lens new_tokens cu_seqlens_q q_start_pos context_lens positions slot_mapping "
-                    "block_tables bt_offsets bt_pages free_pages free_count free_state info dev_status", page_tables,
-                    cached_lens, new_tokens, cu_seqlens_q, q_start_pos, context_lens, positions, slot_mapping,
-                    block_tables, bt_offsets, bt_pages, free_pages, free_count, free_state, info, dev_status)
+    st = _stream_of(stream, "page_tables cached_lens new_tokens cu_seqlens_q q_start_pos context_lens positions "
+                    "slot_mapping block_tables bt_offsets bt_pages free_pages free_count free_state info dev_status",
+                    page_tables, cached_lens, new_tokens, cu_seqlens_q, q_start_pos, context_lens, positions,
+                    slot_mapping, block_tables, bt_offsets, bt_pages, free_pages, free_count, free_state, info, dev_status)
     rc = lib().ms_build_batch_metadata_device(
-        _ptr(cached_lens), _ptr(new_tokens), R, _ptr(page_tables), table_stride, _ptr(free_pages),
+        cached_lens.data_ptr(), new_tokens.data_ptr(), R, page_tables.data_ptr(), table_stride, _ptr(free_pages),
         0 if free_pages is None else free_pages.numel(), _ptr(free_count), _ptr(free_state), int(num_pages), cap_tokens,
-        _ptr(cu_seqlens_q), _ptr(q_start_pos), _ptr(context_lens), _ptr(positions), _ptr(slot_mapping),
-        _ptr(block_tables), stride, _ptr(bt_offsets), _ptr(bt_pages), cap_pages, _ptr(info), _ptr(dev_status),
-        _stream(stream))
+        cu_seqlens_q.data_ptr(), q_start_pos.data_ptr(), context_lens.data_ptr(), positions.data_ptr(),
+        slot_mapping.data_ptr(), _ptr(block_tables), stride, _ptr(bt_offsets), _ptr(bt_pages), cap_pages, _ptr(info),
+        _ptr(dev_status), st)
     _check(rc, "ms_build_batch_metadata_device")
 
 

@@ -51,15 +51,20 @@ __device__ __forceinline__ int pages_of(int32_t n) {
   return static_cast<int>((static_cast<uint32_t>(n) + kPage - 1) / kPage);
 }
 
-// Row whose span of the prefix `p` (n + 1 entries) holds i < p[n]: the last
-// row with p[row] <= i, which skips empty rows.
-__device__ __forceinline__ int row_of(const int32_t* p, int n, int i) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p[mid] <= i) lo = mid; else hi = mid - 1;
+// Rows whose spans of the prefix `p` (n + 1 entries) hold i[0..U): the last row
+// with p[row] <= i, which skips empty rows.  U searches side by side, every one
+// of the same number of steps, so that their shared-memory loads overlap.
+template <int U>
+__device__ __forceinline__ void rows_of(const int32_t* p, int n, const int (&i)[U], int (&row)[U]) {
+#pragma unroll
+  for (int j = 0; j < U; ++j) row[j] = 0;
+  for (int step = 1 << (31 - __clz(n)); step > 0; step >>= 1) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int r = row[j] + step;
+      if (r < n && p[r] <= i[j]) row[j] = r;
+    }
   }
-  return lo;
 }
 
 __device__ __forceinline__ int64_t warp_inclusive(int64_t v) {
@@ -80,6 +85,7 @@ __global__ void __launch_bounds__(kMetaThreads) metadata_kernel(MetaArgs a) {
   int32_t* s_tok = sm;             // prefix of tokens, R + 1 entries
   int32_t* s_pg = s_tok + R + 1;   // prefix of pages in use
   int32_t* s_new = s_pg + R + 1;   // prefix of new pages
+  int32_t* s_c = s_new + R + 1;    // cached tokens
   if (tid == 0) s_dec = 0;
   const int fc = a.free_count != nullptr ? *a.free_count : 0;
 
@@ -144,6 +150,7 @@ __global__ void __launch_bounds__(kMetaThreads) metadata_kernel(MetaArgs a) {
   int64_t o_tok = b_tok + tok - my_tok, o_pg = b_pg + pg - my_pg, o_new = b_new + nw - my_nw;
   for (int r = r0; r < r1; ++r) {
     const int32_t c = a.cached[r], d = bad ? 0 : a.fresh[r];
+    s_c[r] = c;
     s_tok[r] = bad ? 0 : static_cast<int32_t>(o_tok);
     s_pg[r] = bad ? 0 : static_cast<int32_t>(o_pg);
     s_new[r] = bad ? 0 : static_cast<int32_t>(o_new);
@@ -179,55 +186,84 @@ __global__ void __launch_bounds__(kMetaThreads) metadata_kernel(MetaArgs a) {
   }
   __syncthreads();
 
-  // page j of row r
+  // page j of row r, of its `held` old pages or of the new ones after them
   auto page_at = [&](int r, int j) -> int32_t {
-    if (a.free_pages != nullptr) {
-      const int held = pages_of(a.cached[r]);
-      if (j >= held) return a.free_pages[fc - 1 - (s_new[r] + j - held)];
-    }
-    return a.tables[static_cast<int64_t>(r) * a.table_stride + j];
+    const int fresh = s_new[r + 1] - s_new[r], held = s_pg[r + 1] - s_pg[r] - fresh;
+    const int32_t* src = j < held || fresh == 0 ? a.tables + static_cast<int64_t>(r) * a.table_stride + j
+                                                : a.free_pages + (fc - 1 - (s_new[r] + j - held));
+    return *src;
   };
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kMetaThreads + tid;
-  const int64_t gstride = static_cast<int64_t>(gridDim.x) * kMetaThreads;
+  // the CTA's elements of an output, U to a thread at a time
+  constexpr int U = 4;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kMetaThreads * U + tid;
+  const int64_t first_tok = static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) * kMetaThreads * U + tid;  // from the other end
+  const int64_t gstride = static_cast<int64_t>(gridDim.x) * kMetaThreads * U;
   // 3. tokens; those past the total are pad tokens (position 0, no slot)
-  for (int64_t t = gid; t < a.cap_tokens; t += gstride) {
-    int32_t pos = 0, slot = -1;
-    if (t < tot_tok) {
-      const int r = row_of(s_tok, R, static_cast<int>(t));
-      pos = a.cached[r] + static_cast<int32_t>(t) - s_tok[r];
-      const int32_t p = page_at(r, pos / kPage);
-      if (p >= 0 && p < a.num_pages)
-        slot = p * kPage + pos % kPage;
-      else if (a.status != nullptr)
-        atomicOr(a.status, MS_STATUS_BAD_PAGE);
+  for (int64_t t0 = first_tok; t0 < a.cap_tokens; t0 += gstride) {
+    int t[U], r[U], pos[U], page[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) t[j] = static_cast<int>(min(t0 + j * kMetaThreads, static_cast<int64_t>(kMetaMaxTokens)));
+    rows_of<U>(s_tok, R, t, r);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      pos[j] = 0;
+      page[j] = -1;
+      if (t[j] < tot_tok) {
+        pos[j] = s_c[r[j]] + t[j] - s_tok[r[j]];
+        page[j] = page_at(r[j], pos[j] / kPage);
+      }
     }
-    a.positions[t] = pos;
-    a.slots[t] = slot;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (t[j] >= a.cap_tokens) continue;
+      const bool ok = page[j] >= 0 && page[j] < a.num_pages;
+      if (!ok && t[j] < tot_tok && a.status != nullptr) atomicOr(a.status, MS_STATUS_BAD_PAGE);
+      a.positions[t[j]] = pos[j];
+      a.slots[t[j]] = ok ? page[j] * kPage + pos[j] % kPage : -1;
+    }
   }
   // 4. the block table
   if (a.bt_pages != nullptr) {
-    for (int64_t i = gid; i < tot_pg; i += gstride) {
-      const int r = row_of(s_pg, R, static_cast<int>(i));
-      a.bt_pages[i] = page_at(r, static_cast<int>(i) - s_pg[r]);
+    for (int64_t i0 = first; i0 < tot_pg; i0 += gstride) {
+      int i[U], r[U], page[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) i[j] = static_cast<int>(min(i0 + j * kMetaThreads, tot_pg - 1));
+      rows_of<U>(s_pg, R, i, r);
+#pragma unroll
+      for (int j = 0; j < U; ++j) page[j] = page_at(r[j], i[j] - s_pg[r[j]]);
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (i0 + j * kMetaThreads < tot_pg) a.bt_pages[i[j]] = page[j];
     }
   } else {
     const int64_t n = static_cast<int64_t>(R) * a.bt_stride;
-    for (int64_t i = gid; i < n; i += gstride) {
-      const int r = static_cast<int>(i / a.bt_stride), j = static_cast<int>(i % a.bt_stride);
-      a.block_tables[i] = j < s_pg[r + 1] - s_pg[r] ? page_at(r, j) : -1;
+    for (int64_t i0 = first; i0 < n; i0 += gstride) {
+      int32_t page[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t i = min(i0 + j * kMetaThreads, n - 1);
+        const int r = static_cast<int>(i / a.bt_stride), c = static_cast<int>(i - static_cast<int64_t>(r) * a.bt_stride);
+        page[j] = c < s_pg[r + 1] - s_pg[r] ? page_at(r, c) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (i0 + j * kMetaThreads < n) a.block_tables[i0 + j * kMetaThreads] = page[j];
     }
   }
   // 5. the new pages into the requests' tables, and the free count
   if (a.free_pages == nullptr) return;
-  for (int64_t i = gid; i < tot_new; i += gstride) {
-    const int r = row_of(s_new, R, static_cast<int>(i));
-    const int held = pages_of(a.cached[r]);
-    a.tables[static_cast<int64_t>(r) * a.table_stride + held + (i - s_new[r])] = a.free_pages[fc - 1 - i];
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMetaThreads + tid; i0 < tot_new;
+       i0 += static_cast<int64_t>(gridDim.x) * kMetaThreads) {
+    const int i[1] = {static_cast<int>(i0)};
+    int r[1];
+    rows_of<1>(s_new, R, i, r);
+    a.tables[static_cast<int64_t>(r[0]) * a.table_stride + pages_of(s_c[r[0]]) + (i[0] - s_new[r[0]])] =
+        a.free_pages[fc - 1 - i[0]];
   }
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
-    // the counter wraps to 0 by itself, ready for the next call
+    // every thread of the CTA has used the count it read; the counter wraps to 0 by itself, ready for
+    // the next call
     if (atomicInc(reinterpret_cast<unsigned*>(a.free_state + 1), gridDim.x - 1) == gridDim.x - 1)
       a.free_state[0] = fc - static_cast<int32_t>(tot_new);
   }
@@ -254,7 +290,7 @@ extern "C" MS_API int ms_build_batch_metadata_device(
   MetaArgs a{cached_lens, new_tokens, page_tables, free_pages, free_count, free_state, cu_seqlens_q, q_start_pos,
              context_lens, positions, slot_mapping, block_tables, bt_offsets, bt_pages, info, dev_status,
              cap_pages, num_rows, table_stride, free_cap, num_pages, cap_tokens, bt_stride};
-  const int smem = 3 * (num_rows + 1) * 4;
+  const int smem = 4 * (num_rows + 1) * 4;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MS_ERR_CUDA;
@@ -263,7 +299,7 @@ extern "C" MS_API int ms_build_batch_metadata_device(
   const int sms = ms_num_sms();
   if (sms <= 0) return MS_ERR_CUDA;
   int64_t blocks = (most + 4 * kMetaThreads - 1) / (4 * kMetaThreads);
-  blocks = blocks < 1 ? 1 : blocks > sms ? sms : blocks;
+  blocks = blocks < 1 ? 1 : blocks > 2 * sms ? 2 * sms : blocks;  // every CTA scans the rows: no more than run at once
   metadata_kernel<<<static_cast<unsigned>(blocks), kMetaThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? MS_OK : MS_ERR_CUDA;
 }

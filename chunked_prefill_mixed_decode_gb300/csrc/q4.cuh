@@ -65,11 +65,16 @@ __device__ __forceinline__ float q4_scale(float a) {
   return fminf(__uint_as_float(u), 1.125f * 4.2535295865117308e37f);  // 1.125 * 2^125
 }
 
-// x / s is exact enough in fp32: x has 8 significant bits and s has 5, so a
-// quotient that is not exactly halfway between two codes is at least 2^-13
-// away from it.
-__device__ __forceinline__ uint32_t q4_nibble(float x, float s) {
-  return s > 0.f ? static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x, s)) + 8) : 8u;
+// Code + 8 of x for a group of scale s, r = 1 / s rounded (0 for s = 0): rint of
+// x / s without a division.  With x = X 2^e (X < 256) and s = m 2^f (m in
+// 16..31), a quotient q of at most 7.25 that is not exactly halfway between two
+// codes is |2 X - m (2 n + 1) 2^j| / (2 m 2^j) >= q / (2 X) > 2^-10 away from
+// halfway.  x r is off by 2^-22 relative at most, so rounding it to a multiple of
+// 2^-11 (adding and subtracting 6144) restores the exact halfway points and moves
+// nothing across one; the last addition rounds to a whole number, ties to even.
+__device__ __forceinline__ uint32_t q4_nibble(float x, float r) {
+  const float q = __fadd_rn(__fmaf_rn(x, r, 6144.f), -6144.f);
+  return __float_as_uint(__fadd_rn(q, 12582920.f)) & 15u;  // 1.5 * 2^23 + 8
 }
 
 // ---- decoding
@@ -108,6 +113,20 @@ __device__ __forceinline__ uint32_t q4_minus_24(uint32_t s2) {
   const uint32_t m24 = 0xc1c0c1c0u;
   const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&m24));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// N words of global memory, 4 N-byte aligned
+template <int N>
+__device__ __forceinline__ void ldg_words(const uint8_t* src, uint32_t* dst) {
+  if constexpr (N == 4) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+    dst[0] = x.x; dst[1] = x.y; dst[2] = x.z; dst[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    dst[0] = x.x; dst[1] = x.y;
+  } else {
+    dst[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+  }
 }
 
 // Half h (0 low, 1 high) of `a` below the same half of `b`.
