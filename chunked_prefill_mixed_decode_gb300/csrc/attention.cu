@@ -72,7 +72,7 @@ template <typename Idx>
 __global__ void __launch_bounds__(kAppendThreads) append_prologue_kernel(AppendArgs a, AttnParams p) {
   griddep_launch_dependents();  // the attention kernel may start its set-up
   if (blockIdx.x == 0) {
-    prologue_body(p);
+    prologue_body<false>(p);
     return;
   }
   append_rope_units<Idx>(a, static_cast<Idx>(blockIdx.x - 1) * kAppendThreads + threadIdx.x,
@@ -650,7 +650,7 @@ int attention_call(const void* q_rot, const void* k_cache, const void* v_cache, 
   L.p.force_chunk_ctas = force_chunk_ctas;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   *launched = true;  // from here on, kernels may be on the stream
-  const int rp = launch_prologue(L.p, st);
+  const int rp = launch_prologue<false>(L.p, st);
   return rp != MS_OK ? rp : launch_attention(L, st);
 }
 
@@ -716,7 +716,7 @@ extern "C" MS_API int ms_mixed_step(const void* q, const void* k, const void* v,
     rc = ms_kv_append_rope(q, k, v, positions, slot_mapping, num_tokens, cos_tab, sin_tab, max_pos, k_cache, v_cache,
                            num_pages, q_rot, H_q, H_kv, D, page_size, dev_status, stream);
     if (rc != MS_OK || empty) return rc;
-    rc = launch_prologue(L.p, st);
+    rc = launch_prologue<false>(L.p, st);
     return rc != MS_OK ? rc : launch_attention(L, st);
   }
   // CTA 0 runs the prologue beside the append's CTAs; plain stream order, so the

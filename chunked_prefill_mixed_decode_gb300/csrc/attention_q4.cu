@@ -539,7 +539,6 @@ extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* 
   if (rc != MS_OK || empty) return rc;
   p.kv_q4 = static_cast<const uint8_t*>(kv_cache);
   p.dec_workers = p.num_sms * (kQ4Threads / 32);
-  p.dec_teams = 1;
   p.tile_cycles = kQ4TileCycles;
   p.dec_bytes_cycle = kQ4DecodeBytesPerCycle;
   p.key_bytes = q4_block_bytes(D) / 16.f;
@@ -551,7 +550,7 @@ extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* 
   const cuuint32_t bq[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(128 / p.G)};
   if (!encode_bf16(enc, &tq, q_rot, 3, dq, sq, bq)) return MS_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = launch_prologue(p, st);
+  rc = launch_prologue<true>(p, st);
   if (rc != MS_OK) return rc;
   switch (D * 100 + p.G) {
     case 6401: return launch_q4<64, 1>(p, tq, st);

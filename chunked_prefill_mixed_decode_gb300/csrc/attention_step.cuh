@@ -67,7 +67,6 @@ struct AttnParams {
   int32_t dec_workers;       // decode worker warps in the grid
   int32_t num_sms;
   int32_t clear_status;      // the prologue zeroes the status word first (scratch owned by the library)
-  int32_t dec_teams;         // decode items go to teams of warps (4-bit pools): choose split and team size
   int32_t force_chunk_ctas;  // test hook: CTAs that start on chunk work (-1: the cost model decides)
   float sm_mhz;              // cost model: the SM clock when no call has measured it yet,
   float hbm_gbs;             // and the HBM bandwidth that caps decode
@@ -299,9 +298,10 @@ __device__ __forceinline__ DecPlan dec_candidate(int lane) {
   return {team * per_warp, team};
 }
 
+template <bool Teams>
 __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_pages, int n_dec, int max_pages,
                                                bool with_chunks) {
-  if (!p.dec_teams || n_dec == 0) return {decode_split(p, dec_pages, with_chunks), 1};
+  if (!Teams || n_dec == 0) return {decode_split(p, dec_pages, with_chunks), 1};
   const int lane = threadIdx.x & 31;
   const DecPlan cand = dec_candidate(lane);
   const float team = static_cast<float>(cand.team), split = static_cast<float>(cand.split);
@@ -319,8 +319,9 @@ __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_
 
 // First word of a decode row's table entries: its position k in the list, and for
 // teams, which look every word of a split up at once, its row above that.
-__device__ __forceinline__ int dec_entry(const AttnParams& p, int k, int row) {
-  return p.dec_teams ? k | (row << 16) : k;
+template <bool Teams>
+__device__ __forceinline__ int dec_entry(int k, int row) {
+  return Teams ? k | (row << 16) : k;
 }
 
 // Warps that the decode items keep busy at a time, at most.
@@ -335,13 +336,13 @@ __device__ __forceinline__ void header_bad_meta(int32_t* hdr) {
   hdr[H_DEC_CTR] = hdr[H_CH_CTR] = 0;
   hdr[H_NDEC] = hdr[H_NDEC_ITEMS] = hdr[H_NCH] = hdr[H_NCH_ITEMS] = hdr[H_NPART] = 0;
   hdr[H_SPLIT] = kMinSplitPages;
-  hdr[H_TEAM] = 1;
   hdr[H_CHUNK_CTAS] = 0;
 }
 
 // The prologue of a step of at most 32 rows: one warp, a row per lane, with
 // ballots and shuffles in place of shared memory and barriers.  Same outputs
 // as the block version below.
+template <bool Teams>
 __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int lane = threadIdx.x, S = p.num_rows;
   int32_t* hdr = p.hdr;
@@ -373,8 +374,8 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int tpt = 128 / p.G;
   const unsigned bd = __ballot_sync(0xffffffffu, is_dec), bc = __ballot_sync(0xffffffffu, is_ch);
   const int n_dec = __popc(bd), n_ch = __popc(bc);
-  const int max_pages = __reduce_max_sync(0xffffffffu, is_dec ? (ctx + kPage - 1) / kPage : 0);
-  const DecPlan plan = decode_plan(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  const int max_pages = Teams ? __reduce_max_sync(0xffffffffu, is_dec ? (ctx + kPage - 1) / kPage : 0) : 0;
+  const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
   const int split = plan.split;
   // position in its list, then rank by key within the list (longest first):
   // the keys sit in shared memory by list position, zero-padded, read 16 bytes at a time
@@ -429,7 +430,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     p.dec_part_base[rank] = static_cast<int32_t>(static_cast<int64_t>(before) * p.H_q);
     p.dec_nsplit[rank] = items;
     if (!dec_over)
-      for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(dec_entry(p, rank, lane), i);
+      for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(dec_entry<Teams>(rank, lane), i);
   }
   if (is_ch) p.ch_rows[rank] = lane;
   const SmSplit sp = chunk_cta_split(p, static_cast<float>(tiles), static_cast<float>(dec_pages),
@@ -461,7 +462,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_DEC_CTR] = 0;
     hdr[H_CH_CTR] = 0;
     hdr[H_SPLIT] = split;
-    hdr[H_TEAM] = plan.team;
+    if (Teams) hdr[H_TEAM] = plan.team;
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -476,6 +477,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
 // memory).  It runs once per step from a cold instruction cache, so its loops
 // stay rolled and its code short.  It reads only the row metadata, never the
 // appended K/V, so it may run alongside the append.
+template <bool Teams>
 __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   extern __shared__ __align__(16) int32_t psm[];
   __shared__ int s_warp[32];
@@ -496,7 +498,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   // (ahead of every status write of this call, all of which come after a barrier or from this thread)
   if (tid == 0 && p.clear_status) hdr[H_STATUS] = 0;
   if (S <= 32) {
-    if (warp == 0) prologue_warp(p);
+    if (warp == 0) prologue_warp<Teams>(p);
     return;
   }
   if (tid == 0) s_tiles = 0;
@@ -537,14 +539,14 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   my_ch_keys = warp_sum64(my_ch_keys);
   my_dec = __reduce_add_sync(0xffffffffu, my_dec);
   my_ch = __reduce_add_sync(0xffffffffu, my_ch);
-  my_max = __reduce_max_sync(0xffffffffu, my_max);
+  if (Teams) my_max = __reduce_max_sync(0xffffffffu, my_max);
   if (lane == 0) {
     s_sum[0][warp] = my_ctx;
     s_sum[1][warp] = my_pages;
     s_sum[2][warp] = my_ch_keys;
     s_cnt[0][warp] = my_dec;
     s_cnt[1][warp] = my_ch;
-    s_cnt[2][warp] = my_max;
+    if (Teams) s_cnt[2][warp] = my_max;
   }
   const int bad = __syncthreads_or(my_bad);
   int64_t ctx_sum = 0, dec_pages = 0, chunk_keys = 0;
@@ -555,14 +557,14 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     chunk_keys += s_sum[2][j];
     n_dec += static_cast<int>(s_cnt[0][j]);
     n_ch += static_cast<int>(s_cnt[1][j]);
-    max_pages = max(max_pages, static_cast<int>(s_cnt[2][j]));
+    if (Teams) max_pages = max(max_pages, static_cast<int>(s_cnt[2][j]));
   }
   if (bad || ctx_sum > p.context_total) {
     if (tid == 0) header_bad_meta(hdr);
     return;
   }
   // 2. decode split size
-  const DecPlan plan = decode_plan(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
   const int split = plan.split;
   const int tpt = 128 / p.G;
   const unsigned split32 = static_cast<unsigned>(split);
@@ -649,7 +651,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   for (int q = tid; q < n_dec && !dec_over; q += nt) {
     const int cnt = pref[q + 1] - pref[q];
     int2* out = p.dec_items + pref[q];
-    const int x = dec_entry(p, q, p.dec_rows[q]);
+    const int x = dec_entry<Teams>(q, Teams ? p.dec_rows[q] : 0);
     for (int i = 0; i < cnt; ++i) out[i] = make_int2(x, i);
   }
   if (warp == 0) {
@@ -683,7 +685,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_DEC_CTR] = 0;
       hdr[H_CH_CTR] = 0;
       hdr[H_SPLIT] = static_cast<int32_t>(split);
-      hdr[H_TEAM] = plan.team;
+      if (Teams) hdr[H_TEAM] = plan.team;
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }
@@ -693,9 +695,10 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
 // kernel before it on the stream (normally the append): it runs alongside that
 // kernel and waits for it before it exits, so the kernel after it sees the
 // append's writes.
+template <bool Teams>
 __global__ void __launch_bounds__(1024, 1) prologue_kernel(AttnParams p) {
   griddep_launch_dependents();
-  prologue_body(p);
+  prologue_body<Teams>(p);
   griddep_wait();
 }
 
@@ -985,7 +988,6 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.G = G;
   p.num_sms = sms;
   p.clear_status = clear_status ? 1 : 0;
-  p.dec_teams = 0;
   p.test_stall = stall_limit_ns > 0 ? 1 : 0;
   p.wait_limit_ns = stall_limit_ns > 0 ? static_cast<uint64_t>(stall_limit_ns) : 2000000000ull;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -999,11 +1001,12 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
 // The prologue as its own kernel, a programmatic dependent of the kernel
 // before it: about a thread per row (one warp up to 32 rows, else at least a
 // warp per scheduler).
-inline int launch_prologue(const AttnParams& p, cudaStream_t st) {
-  if (ensure_smem_limit(prologue_kernel, 8, prologue_words(kMaxRows) * 4) != MS_OK) return MS_ERR_CUDA;
+template <bool Teams>
+int launch_prologue(const AttnParams& p, cudaStream_t st) {
+  if (ensure_smem_limit(prologue_kernel<Teams>, 8, prologue_words(kMaxRows) * 4) != MS_OK) return MS_ERR_CUDA;
   const int S = p.num_rows;
   const int threads = S <= 32 ? 32 : S >= 1024 ? 1024 : S <= 128 ? 128 : (S + 31) / 32 * 32;
-  return launch_dependent(prologue_kernel, dim3(1), dim3(threads), prologue_words(S) * 4, st, p) == cudaSuccess
+  return launch_dependent(prologue_kernel<Teams>, dim3(1), dim3(threads), prologue_words(S) * 4, st, p) == cudaSuccess
              ? MS_OK
              : MS_ERR_CUDA;
 }
