@@ -71,13 +71,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_q4_kernel(AppendQ4Args 
   if (t >= a.T) return;
   const int g0 = static_cast<int>(w % args.chunks) * args.span, g1 = min(groups, g0 + args.span);
   const int pos = __ldg(a.positions + t), slot = __ldg(a.slot_mapping + t);
+  const bool slot_ok = slot >= 0 && static_cast<int64_t>(slot) < a.n_slots;
+  if (!slot_ok && slot != -1 && a.status && lane == 0) atomicOr(a.status, MS_STATUS_BAD_SLOT);  // -1: no write
   // a token at a position outside the table writes nothing: no q_rot, no K, no V
   if (pos < 0 || pos >= a.max_pos) {
     if (a.status && lane == 0) atomicOr(a.status, MS_STATUS_BAD_POSITION);
     return;
   }
-  const bool slot_ok = slot >= 0 && static_cast<int64_t>(slot) < a.n_slots;
-  if (!slot_ok && slot != -1 && a.status && lane == 0) atomicOr(a.status, MS_STATUS_BAD_SLOT);  // -1: no write
   float c[kAppendVec], s[kAppendVec];
   {
     const float4* cp = reinterpret_cast<const float4*>(a.cos_tab + static_cast<int64_t>(pos) * half + i0);

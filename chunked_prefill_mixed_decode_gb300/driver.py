@@ -11,11 +11,12 @@ from __future__ import annotations
 import time
 
 from . import Engine, StepGraph, attention_workspace_size, mixed_step, read_status
-from .step import MetaStager
+from .step import MetaStager, run_step_q4
 
 
 class RoundDriver:
-    """Drives an Engine over caller-owned K/V page pools [num_pages, H_kv, 16, D] (bf16).
+    """Drives an Engine over caller-owned K/V page pools [num_pages, H_kv, 16, D] (bf16), or over one 4-bit pool
+    (step.kv_pool_q4) given as ``k_cache`` with ``v_cache`` None.
 
     ``step(q, k, v)`` takes the new tokens' activations (device bf16, at least
     ``num_tokens`` rows: q [T, H_q, D], k and v [T, H_kv, D]) in the planned
@@ -34,6 +35,9 @@ class RoundDriver:
         import torch
         self.engine = engine
         self.graph = None
+        self.q4 = v_cache is None
+        if self.q4 and graph_buckets:
+            raise ValueError("graph_buckets needs bf16 pools: a step over a 4-bit pool is captured with step.StepTables")
         self.k_cache, self.v_cache = k_cache, v_cache
         self.cos, self.sin = cos, sin
         self.H_q, self.H_kv, self.D = H_q, H_kv, D
@@ -91,10 +95,14 @@ class RoundDriver:
             batch = self.stager.stage(meta, self.stream)
             t_plan = time.perf_counter()
             self.ev0.record(self.stream)
-            mixed_step(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, self.cos, self.sin, self.k_cache,
-                       self.v_cache, self.q_rot[:T], batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
-                       batch.block_tables, batch.context_total, self.out[:T], self.workspace,
-                       dev_status=self.status, scale=self.scale, stream=self.stream)
+            if self.q4:
+                run_step_q4(q, k, v, batch, self.cos, self.sin, self.k_cache, self.out, self.workspace, q_rot=self.q_rot,
+                            dev_status=self.status, scale=self.scale, stream=self.stream)
+            else:
+                mixed_step(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, self.cos, self.sin, self.k_cache,
+                           self.v_cache, self.q_rot[:T], batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
+                           batch.block_tables, batch.context_total, self.out[:T], self.workspace,
+                           dev_status=self.status, scale=self.scale, stream=self.stream)
             self.ev1.record(self.stream)
             self.stream.synchronize()
             st = read_status(self.status, self.stream) | read_status(self.workspace, self.stream)

@@ -10,8 +10,8 @@ import dataclasses
 
 import numpy as np
 
-from . import (attention_workspace_size, mixed_step, mixed_step_attention, mixed_step_attention_ragged,
-               rope_table)
+from . import (attention_workspace_size, build_batch_metadata_device, kv_append_rope_q4, mixed_step,
+               mixed_step_attention, mixed_step_attention_q4, mixed_step_attention_ragged, q4_block_bytes, rope_table)
 
 META_KEYS = ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping", "block_tables")
 RAGGED_KEYS = ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping", "bt_offsets", "bt_pages")
@@ -152,6 +152,52 @@ def workspace_for(batch: DeviceBatch, H_q: int, H_kv: int, D: int, device):
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
+def kv_pool_q4(num_pages: int, H_kv: int, D: int, device):
+    """A 4-bit K/V pool of zeros: one uint8 tensor [num_pages, H_kv, q4_block_bytes(D)] in place of a K and a V pool."""
+    import torch
+    return torch.zeros((num_pages, H_kv, q4_block_bytes(D)), dtype=torch.uint8, device=device)
+
+
+class StepTables:
+    """A step's metadata built on the GPU from the requests' lengths, into buffers of fixed sizes.
+
+    ``page_tables`` [rows, stride] (device int32) are the requests' pages.  With ``free_pages`` (device int32, all of
+    them free at the start) a request holds exactly the pages of its cached tokens and ``build`` takes those that it
+    lacks from the end of the list; without, the tables already hold every page.  ``build`` enqueues one kernel and
+    returns a DeviceBatch over the buffers: ``max_tokens`` tokens (the ones past the step's own are pad tokens), and a
+    context bound of the whole pool.  Nothing in it depends on host data, so a step can be captured and replayed while
+    ``cached_lens`` and ``new_tokens`` change on the GPU.  ``info`` [4] and ``status`` [1] are those of
+    build_batch_metadata_device.
+    """
+
+    def __init__(self, page_tables, num_pages: int, max_tokens: int, free_pages=None):
+        import torch
+        rows, stride = page_tables.shape
+        dev = page_tables.device
+
+        def buf(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=dev)
+        self.page_tables, self.num_pages, self.free_pages = page_tables, int(num_pages), free_pages
+        self.cu_seqlens_q, self.q_start_pos, self.context_lens = buf(rows + 1), buf(rows), buf(rows)
+        self.positions, self.slot_mapping = buf(max_tokens), buf(max_tokens)
+        self.block_tables, self.info, self.status = buf(rows, stride), buf(4), buf(1)
+        self.free_state = None
+        if free_pages is not None:
+            self.free_state = torch.tensor([free_pages.numel(), 0], dtype=torch.int32, device=dev)
+        self.batch = DeviceBatch(self.cu_seqlens_q, self.q_start_pos, self.context_lens, self.positions,
+                                 self.slot_mapping, self.block_tables, rows, int(max_tokens), 0, 16 * self.num_pages, {})
+
+    def build(self, cached_lens, new_tokens, stream=None) -> DeviceBatch:
+        free = {}
+        if self.free_pages is not None:
+            free = {"free_pages": self.free_pages, "free_count": self.free_state[:1], "free_state": self.free_state}
+        build_batch_metadata_device(cached_lens, new_tokens, self.page_tables, self.num_pages, self.cu_seqlens_q,
+                                    self.q_start_pos, self.context_lens, self.positions, self.slot_mapping,
+                                    block_tables=self.block_tables, info=self.info, dev_status=self.status,
+                                    stream=stream, **free)
+        return self.batch
+
+
 def run_step(q, k, v, batch: DeviceBatch, cos, sin, k_cache, v_cache, out, workspace, q_rot=None,
              dev_status=None, scale=None, stream=None):
     """One step of one layer through ms_mixed_step (the append, then the attention, with the
@@ -175,3 +221,17 @@ def attend(q_rot, k_cache, v_cache, batch: DeviceBatch, out, workspace, scale=No
     else:
         mixed_step_attention(q_rot, k_cache, v_cache, batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
                              batch.block_tables, batch.context_total, out, workspace, scale=scale, stream=stream)
+
+
+def run_step_q4(q, k, v, batch: DeviceBatch, cos, sin, kv_cache, out, workspace, q_rot=None, dev_status=None,
+                scale=None, stream=None):
+    """run_step over a 4-bit pool: the append, then the attention; returns q_rot."""
+    if q_rot is None:
+        q_rot = q
+    T = batch.num_tokens
+    kv_append_rope_q4(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, cos, sin, kv_cache, q_rot=q_rot[:T],
+                      dev_status=dev_status, stream=stream)
+    mixed_step_attention_q4(q_rot[:T], kv_cache, batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
+                            batch.block_tables, batch.context_total, out[:T], workspace,
+                            bt_offsets=batch.bt_offsets if batch.ragged else None, scale=scale, stream=stream)
+    return q_rot

@@ -121,7 +121,8 @@ def test_append_and_read_bad_slots_and_positions(env):
     D, H_q, H_kv, pages = 64, 4, 2, 3
     q, k, v = (torch.randn(6, H, D, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
     for slots, positions, flag in (([0, -1, 47, 5, -1, 9], [1] * 6, 0), ([0, 48, 47, 5, 6, 9], [1] * 6, 1),
-                                   ([0, -2, 47, 5, 6, 9], [1] * 6, 1), ([0, 1, 2, 3, 4, 5], [0, 9, 10, 3, -1, 2], 2)):
+                                   ([0, -2, 47, 5, 6, 9], [1] * 6, 1), ([0, 1, 2, 3, 4, 5], [0, 9, 10, 3, -1, 2], 2),
+                                   ([0, 1, 99, 3, 4, 5], [0, 9, 10, 3, 1, 2], 3)):
         pool = torch.full((pages, H_kv, 18 * D), 0x21, dtype=torch.uint8, device="cuda")
         before = pool.cpu().numpy()
         q_rot, status = _append(env, q, k, v, positions, slots, pool, 10)
@@ -658,3 +659,86 @@ def test_decode_loop_captured_whole(env):
         a.check()
         host_c = host_c + new
     assert state.tolist() == [count, 0] and c.tolist() == list(host_c)
+
+
+def test_step_tables_and_run_step(env):
+    """The same loop through StepTables and run_step_q4: a prompt enters in chunks while others decode, lengths and
+    chunk sizes changing on the GPU under one captured step."""
+    torch, ms, step = env
+    H_q, H_kv, D, R, pages, stride, cap = 8, 1, 128, 3, 40, 12, 48
+    pool = step.kv_pool_q4(pages, H_kv, D, "cuda")
+    ref_pool = pool.cpu().numpy().copy()
+    page_tables = torch.full((R, stride), -1, dtype=torch.int32, device="cuda")
+    tables = step.StepTables(page_tables, pages, cap, free_pages=torch.arange(pages, dtype=torch.int32, device="cuda"))
+    c, d = _i32(torch, [0] * R), _i32(torch, [0] * R)
+    cos, sin = step.rope_tables_device(16 * stride, D, "cuda")
+    q, k, v = (torch.zeros(cap, H, D, dtype=torch.bfloat16, device="cuda") for H in (H_q, H_kv, H_kv))
+    q_rot, out = torch.zeros_like(q), torch.zeros_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = step.workspace_for(tables.batch, H_q, H_kv, D, "cuda")
+    graph = torch.cuda.CUDAGraph()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=st):
+        b = tables.build(c, d)
+        step.run_step_q4(q, k, v, b, cos, sin, pool, out, ws, q_rot=q_rot, dev_status=status)
+        c.add_(d)
+    host_c, host_tab, count = np.zeros(R, dtype=np.int64), np.full((R, stride), -1), pages
+    for n, new in enumerate([(30, 0, 0), (1, 40, 0), (1, 7, 0), (1, 1, 5), (1, 1, 33), (0, 1, 1), (46, 1, 1), (1, 1, 1)]):
+        d.copy_(_i32(torch, new))
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ms.read_status(status) == 0 and ms.read_status(ws) == 0 and ms.read_status(tables.status) == 0
+        m = oracle.metadata_from_lengths(host_c, new, host_tab, cap, free=list(range(pages)), count=count)
+        host_tab, count = m["tables"], m["free_count"]
+        np.testing.assert_array_equal(tables.slot_mapping.tolist(), m["slot_mapping"])
+        assert tables.info.tolist() == m["info"]
+        T = sum(new)
+        ok = [s >= 0 for s in m["slot_mapping"]]
+        ref_pool, _ = _oracle_append(q, k, v, np.array(m["positions"]), m["slot_mapping"], ref_pool, ok)
+        np.testing.assert_array_equal(pool.cpu().numpy(), ref_pool)
+        a = Attn(env, [(int(x) if y else 0, y) for x, y in zip(host_c, new)], H_q, H_kv, D, pool=pool)
+        a.pages = [host_tab[s, :-(-int(x + y) // 16)] if y else [] for s, (x, y) in enumerate(zip(host_c, new))]
+        a.q, a.ws, a.out = q_rot, ws, out[:T].clone()
+        a.check()
+        host_c = host_c + new
+    assert int(tables.free_state[0]) == count
+
+
+@pytest.mark.parametrize("H_q,H_kv,D,seed", [(4, 2, 64, 50), (8, 1, 128, 52)])
+def test_engine_rounds_over_a_4_bit_pool(env, H_q, H_kv, D, seed):
+    """Random arrivals through the engine and the round driver, pages freed and handed out again: the pool's bytes are
+    the oracle's after every round, the outputs those of 64-bit attention over them."""
+    torch, ms, step = env
+    from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
+    pages = 40
+    pool = step.kv_pool_q4(pages, H_kv, D, "cuda")
+    ref_pool = pool.cpu().numpy().copy()
+    cos, sin = step.rope_tables_device(pages * 16 + 1, D, "cuda")
+    eng = ms.Engine(pages, 40, max_chunk_per_request=24)
+    drv = RoundDriver(eng, pool, None, cos, sin, H_q, H_kv, D)
+    rng = np.random.default_rng(seed)
+    finished = 0
+    for rnd in range(25):
+        for _ in range(int(rng.integers(0, 3))):
+            try:
+                eng.add_request(int(rng.integers(1, 120)), int(rng.integers(2, 12)))
+            except ms.MixedStepError:
+                pass
+        if eng.stats()["num_live"] == 0:
+            continue
+        q, k, v = (torch.randn(40, H, D, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+        rec = drv.step(q, k, v)
+        m, T = rec["meta"], rec["meta"]["num_tokens"]
+        ref_pool, qr = _oracle_append(q[:T], k[:T], v[:T], m["positions"], m["slot_mapping"], ref_pool, [True] * T)
+        np.testing.assert_array_equal(pool.cpu().numpy(), ref_pool)
+        np.testing.assert_array_equal(workloads.bf16_bits(drv.q_rot[:T]), qr)
+        rows = [(int(c), int(n - c)) for c, n in zip(m["q_start_pos"], m["context_lens"])]
+        a = Attn(env, rows, H_q, H_kv, D, pool=pool)
+        a.pages = [m["block_tables"][s, :-(-(c + d) // 16)] for s, (c, d) in enumerate(rows)]
+        a.q, a.ws, a.out = drv.q_rot[:T], drv.workspace, drv.out[:T].clone()
+        a.check()
+        finished += len(rec["finished"])
+    assert finished >= 4

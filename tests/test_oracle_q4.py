@@ -193,3 +193,11 @@ def test_binding_refusals(ms):
     refuse("free_state", md, *args, block_tables=bt, free_pages=one, free_count=one, free_state=one)
     refuse("slot_mapping", md, one, one, bt, 4, cu, one, one, pos, pos[:2], block_tables=bt)
     refuse("cu_seqlens_q", md, one, one, bt, 4, one, one, one, pos, pos, block_tables=bt)
+
+
+def test_round_driver_refuses_graph_buckets_over_a_4_bit_pool(ms):
+    torch = pytest.importorskip("torch")
+    from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
+    pool = torch.zeros(4, 2, 1152, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="graph_buckets"):
+        RoundDriver(ms.Engine(4, 8), pool, None, torch.zeros(8, 32), torch.zeros(8, 32), 4, 2, 64, graph_buckets=[8])
