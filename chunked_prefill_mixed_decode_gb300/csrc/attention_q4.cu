@@ -5,16 +5,16 @@
 //
 //   chunk rows (d > 1): chunk_phase with four more warps, which read pages and
 //     write their values into the shared-memory tiles.
-//   decode rows (d = 1): 16 worker warps, each with a private ring of pages in
-//     shared memory filled by bulk copies, one a page.  A page of K and V is
-//     2.25 KB instead of 8 KB, so the time goes into instructions rather than
-//     bytes, and the codes go into the tensor cores undecoded as far as the
+//   decode rows (d = 1): 16 worker warps in teams, each warp with a private ring
+//     of pages in shared memory filled by bulk copies, one a page.  A page of K
+//     and V is 2.25 KB instead of 8 KB, so the time goes into instructions rather
+//     than bytes, and the codes go into the tensor cores undecoded as far as the
 //     algebra allows.  With x the codes of a group, n = x + 8 its nibbles and s
 //     its scale,
 //         q . K = sum_g s_g (q_g . x_g) = sum_g s_g (q_g . (128 + n_g) - 136 sum q_g):
 //     the operand is the bf16 pair 128 + n, one shift and one logic instruction
-//     for two values, and -136 sum q_g, fixed for an item, is the accumulator's
-//     start.  For V the scales go into the weights,
+//     for two values, and the offsets' share is one more product, of the scales as
+//     they are stored with the sums.  For V the scales go into the weights,
 //         O_d = sum_j (p_j s_jg) x_jd,
 //     and the codes are centred first (one subtraction for two values): an
 //     accumulator that carried 128 per weight through a long row would lose the
@@ -35,6 +35,8 @@
 namespace {
 
 constexpr int kQ4Threads = 32 * (kDequantWarp0 + kDequantWarps);
+// The cost model's rates (attention_step.cuh).  The split that they choose is
+// within 1 % of the best of 13 forced ones on six mixed steps (124 to 2140 us).
 constexpr float kQ4TileCycles = 5820.f;
 constexpr float kQ4DecodeBytesPerCycle = 24.f;
 
@@ -94,8 +96,16 @@ struct IssueCursor {
 // to a split would need no joining but many more splits: with few or long rows
 // its pages keep it for tens of microseconds while other warps idle, and one
 // warp joins the row's records at the end.  256 rows of 8 KV heads and 700 to
-// 16384 keys: 372 us with a warp to a split of 64 pages, 331 us with four to 320;
-// 61 rows of 1 to 5003 keys, 2 KV heads, D = 64: 55 us and (eight to 48) 21 us.
+// 16384 keys: 372 us with a warp to a split of 64 pages, 310 us with four to 512;
+// 61 rows of 1 to 5003 keys, 2 KV heads, D = 64: 55 us, and 20 us with eight to 32.
+//
+// What bounds it is instructions: about 360 a page and warp (2.25 KB of K and V
+// at D = 128), half of them on the logic pipe, which is 65 % busy, as are the
+// issue slots; DRAM delivers 4.8 TB/s, 0.70 of the measured copy rate (256 rows,
+// above).  Measured and not kept: shifts as multiplications (310 -> 362 to 388 us);
+// V's offset taken off by a product with -136 instead of before it (330 us);
+// one page at a time; 16-byte asynchronous copies by all lanes instead of a bulk
+// copy a page (346 us before the teams, 378 us).
 template <int D, int G>
 __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* dsmem) {
   using Q = Q4<D>;

@@ -211,7 +211,10 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
 // write their values -- exactly bf16, so nothing else of the phase changes --
 // into the K and V stages: warp 12 + w page w of each tile.  Loads from global
 // memory into the dequantizing warps' registers a tile ahead, without the ring,
-// cost a sixth of the rate (chunks of 3968 tokens at 0 and 6000, 32 / 8 heads).
+// took 740 us instead of 605 (chunks of 3968 tokens at 0 and 6000, 32 / 8 heads).
+// Measured and not kept: where items are few, one Q tile for both softmax groups,
+// every other K/V tile each: a 512-token chunk alone 58 -> 54 us, beside 64 decodes
+// 78 -> 94, and the branches cost the long chunks 4 % (605 -> 633 us).
 template <int D, int G, bool Q4 = false>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
