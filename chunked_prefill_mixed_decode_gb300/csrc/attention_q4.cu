@@ -37,7 +37,7 @@ namespace {
 constexpr int kQ4Threads = 32 * (kDequantWarp0 + kDequantWarps);
 // The cost model's rates (attention_step.cuh).  The split that they choose is
 // within 1 % of the best of 13 forced ones on six mixed steps (124 to 2140 us).
-constexpr float kQ4TileCycles = 5820.f;
+constexpr float kQ4TileCycles = 4900.f;
 constexpr float kQ4DecodeBytesPerCycle = 24.f;
 
 // Decode phase's shared memory: every warp's ring of NST stages of two pages,

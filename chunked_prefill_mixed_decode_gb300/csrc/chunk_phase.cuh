@@ -66,6 +66,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return ok != 0;
 }
 
+// As warp_wait, the whole warp polling a few times before the clock starts; every
+// lane takes the same branch.
+__device__ __forceinline__ bool warp_wait_fast(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                               uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort, limit_ns);
+}
+
 // ---- 4-bit pools: K and V tiles by warps instead of TMA
 
 constexpr int kDequantWarps = kTilePages;            // one per page of a tile
@@ -139,7 +149,9 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
     for (int kt = 0; kt < n_kt; ++kt) {
       const int keys = kv_max - kt * kKeys - w * kPage;  // of this page
       uint32_t k[2][NG], v[2][NG], ks[2][NG / 2], vs[2][NG / 2];
-      if (!mbar_wait_fast(&bars->raw_full[br], rph, abort_flag, 16, lim)) return false;
+      // Each lane waits by itself (a vote after every wait costs 5 % of the rate); one
+      // that gave up goes on within the stage's bounds, to the vote at the end of the tile.
+      bool ok = mbar_wait_fast(&bars->raw_full[br], rph, abort_flag, 16, lim);
       if (keys > 0) {
         const uint32_t blk = sbase + ChQ4<D>::RAW_OFF + br * ChQ4<D>::RAW_STAGE + w * Q::BYTES;
 #pragma unroll
@@ -162,8 +174,8 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
         rph ^= 1u;
       }
       // the stage's first round finds both barriers in their initial phase, which counts as released
-      if (!mbar_wait_fast(&bars->v_empty[bk], ph, abort_flag, 16, lim)) return false;
-      if (!mbar_wait_fast(&bars->k_empty[bk], ph, abort_flag, 16, lim)) return false;
+      ok &= mbar_wait_fast(&bars->v_empty[bk], ph, abort_flag, 16, lim);
+      ok &= mbar_wait_fast(&bars->k_empty[bk], ph, abort_flag, 16, lim);
       if (keys > 0) {
         const uint32_t kbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + w * 2048;
         const uint32_t vbase = sbase + C::KV_OFF + bk * 2 * NSL * kKVSlab + NSL * kKVSlab + w * NSL * 2048;
@@ -178,7 +190,7 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
         }
       }
       fence_proxy_async_smem();
-      __syncwarp();
+      if (!__all_sync(0xffffffffu, ok)) return false;
       if (lane == 0) {
         mbar_arrive(&bars->k_full[bk]);
         mbar_arrive(&bars->v_full[bk]);
@@ -209,12 +221,17 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
 // Over a 4-bit pool (Q4) warp 0 brings the pages of a tile as they are stored,
 // one bulk copy a page, into a ring of their own, and four more warps, 12-15,
 // write their values -- exactly bf16, so nothing else of the phase changes --
-// into the K and V stages: warp 12 + w page w of each tile.  Loads from global
-// memory into the dequantizing warps' registers a tile ahead, without the ring,
-// took 740 us instead of 605 (chunks of 3968 tokens at 0 and 6000, 32 / 8 heads).
-// Measured and not kept: where items are few, one Q tile for both softmax groups,
-// every other K/V tile each: a 512-token chunk alone 58 -> 54 us, beside 64 decodes
-// 78 -> 94, and the branches cost the long chunks 4 % (605 -> 633 us).
+// into the K and V stages: warp 12 + w page w of each tile.  Two chunks of 3968
+// tokens at 0 and 6000, 32 / 8 heads, D = 128: 501 us, 1.29 PFLOP/s, 0.69 of the
+// measured dense rate; the tensor pipe is 55 % and the issue slots 59 % busy.  A
+// tile pair takes about 1800 cycles, in which the softmax warps, the dequantizing
+// warps and the issuers are each busy nearly all the time: without any softmax
+// work it would take 482 us, without any dequantizing 487.
+// Measured and not kept, before the issue by elected lanes (605 us then): loads
+// from global memory into the dequantizing warps' registers a tile ahead, without
+// the ring (740 us); where items are few, one Q tile for both softmax groups, every
+// other K/V tile each (a 512-token chunk alone 58 -> 54 us, beside 64 decodes
+// 78 -> 94, and the branches cost the long chunks 4 %).
 template <int D, int G, bool Q4 = false>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
@@ -272,6 +289,24 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   __syncthreads();
   volatile int* abort_flag = &bars->abort;
   const uint64_t lim = p.wait_limit_ns;
+  // The MMA issuers.  Over a 4-bit pool a whole warp runs the loop and one elected lane
+  // issues, which takes the issue off the critical path: 605 -> 507 us for chunks of
+  // 3968 tokens at 0 and 6000, 32 / 8 heads.  Over a bf16 pool, where the same change
+  // measures 522 -> 527 us there and 2060 -> 2110 us beside long decodes (and 69 -> 61 us
+  // for D = 64), lane 0 runs it alone.
+  auto one = [&] { return !Q4 || elect_one(); };
+  auto join = [&] {
+    if constexpr (Q4) __syncwarp();
+  };
+  auto issue_wait = [&](uint64_t* bar, uint32_t parity) {
+    return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait_fast(bar, parity, abort_flag, 16, lim);
+  };
+  auto issue_wait_item = [&](uint64_t* bar, uint32_t parity) {
+    return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait(bar, parity, abort_flag, lim);
+  };
+  auto softmax_wait = [&](uint64_t* bar, uint32_t parity) {
+    return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : warp_wait(bar, parity, abort_flag, lim);
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- work queue + TMA producer
@@ -465,7 +500,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     // a k-step or a stage only moves the descriptor's start-address field
     // (bytes >> 4, 14 bits, no carry below 256 KB) by a constant.
     const int t = warp == 1 ? 0 : 1;
-    if (lane == 0) {
+    if (Q4 || lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(sbase + C::Q_OFF + t * C::Q_BYTES, 16, 1024);
       const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, 1024);
       const uint32_t s_tm = tmem + C::S_COL + 2 * t * 64;
@@ -475,7 +510,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const int slot = n & 1;
-        if (!mbar_wait(&bars->item_full[slot], (n >> 1) & 1, abort_flag, lim)) {
+        if (!issue_wait_item(&bars->item_full[slot], (n >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -484,19 +519,19 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         if (row < 0) break;
         const int nkt = it.nkt[t], t0 = it.t0[t], n_kt = it.n_kt;
         const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-        if (nkt > 0 && !mbar_wait(&bars->q_full, n & 1, abort_flag, lim)) {
+        if (nkt > 0 && !issue_wait_item(&bars->q_full, n & 1)) {
           ok = false;
           break;
         }
         for (int kt = 0; kt < n_kt; ++kt) {
-          if (!mbar_wait_fast(&bars->k_full[bk], kph, abort_flag, 16, lim)) {
+          if (!issue_wait(&bars->k_full[bk], kph)) {
             ok = false;
             break;
           }
           if (kt < nkt) {
             const int gt = t0 + kt, b = gt & 1;
             // S buffer b last held P of the group's tile gt - 2: its PV MMA must be done
-            if (gt >= 2 && !mbar_wait_fast(&bars->o_done[t][b], ((gt - 2) >> 1) & 1, abort_flag, 16, lim)) {
+            if (gt >= 2 && !issue_wait(&bars->o_done[t][b], ((gt - 2) >> 1) & 1)) {
               ok = false;
               break;
             }
@@ -505,32 +540,41 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             const uint32_t idesc_s = keys >= kKeys ? idesc_full : idesc_bf16_f32(128, (keys + 15) & ~15, 0);
             const uint64_t kd = kdesc0 + static_cast<uint64_t>((bk * 2 * NSL * kKVSlab) >> 4);
             const uint32_t dcol = s_tm + b * 64;
+            if (one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * kQSlab + (kk & 3) * 32) >> 4);
-              const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * kKVSlab + (kk & 3) * 32) >> 4);
-              mma_bf16_ss(dcol, qdesc + qo, kd + ko, idesc_s, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * kQSlab + (kk & 3) * 32) >> 4);
+                const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * kKVSlab + (kk & 3) * 32) >> 4);
+                mma_bf16_ss(dcol, qdesc + qo, kd + ko, idesc_s, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars->s_full[t][b]);
             }
-            mma_commit(&bars->s_full[t][b]);
+            join();
           }
-          mma_commit(&bars->k_empty[bk]);
-          if (kt == n_kt - 1) mma_commit(&bars->q_empty);
+          if (one()) {
+            mma_commit(&bars->k_empty[bk]);
+            if (kt == n_kt - 1) mma_commit(&bars->q_empty);
+          }
+          join();
           if (++bk == KVS) {
             bk = 0;
             kph ^= 1u;
           }
         }
         if (!ok) break;
-        mbar_arrive(&bars->item_empty[slot]);
+        join();
+        if (one()) mbar_arrive(&bars->item_empty[slot]);
       }
       if (!ok) *abort_flag = 1;
       // every MMA this thread issued must finish before TMEM is reused or released
-      mma_commit(&bars->mma_done[t]);
-      mbar_wait(&bars->mma_done[t], 0, nullptr, 200000000ull);
+      if (one()) {
+        mma_commit(&bars->mma_done[t]);
+        mbar_wait(&bars->mma_done[t], 0, nullptr, 200000000ull);
+      }
     }
   } else if (warp == 3 + kSoftmaxWarps) {
     // ---------------------------------------------------------------- PV issuer of both groups
-    if (lane == 0) {
+    if (Q4 || lane == 0) {
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
       // V is the MN-major B operand, one page per k-step of 16 keys: the page's
       // 64-column slabs 2048 B apart (LBO), its two 8-key row groups 1024 B apart
@@ -541,7 +585,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       bool ok = true;
       for (int n = 0; ok; ++n) {
         const int slot = n & 1;
-        if (!mbar_wait(&bars->item_full[slot], (n >> 1) & 1, abort_flag, lim)) {
+        if (!issue_wait_item(&bars->item_full[slot], (n >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -553,7 +597,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const int ke_[2] = {it.kv_end[0], it.kv_end[1]};
         const int kv_max = max(ke_[0], ke_[1]);
         for (int j = 0; j < n_kt && ok; ++j) {
-          if (!mbar_wait_fast(&bars->v_full[bv], vph, abort_flag, 16, lim)) {
+          if (!issue_wait(&bars->v_full[bv], vph)) {
             ok = false;
             break;
           }
@@ -561,20 +605,23 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           if (!Q4 && (keys & 15) != 0) {
             // rows past the context in the last page may hold stale (even non-finite)
             // data: zero them in V so that P = 0 times V stays 0
-            uint8_t* v0 = smem + v_off(bv);
-            for (int r = keys; r < ((keys + 15) & ~15); ++r)
-              for (int s = 0; s < NSL; ++s)
-                for (int q16 = 0; q16 < 8; ++q16)
-                  *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + s * 2048 + (r & 15) * 128 + q16 * 16) =
-                      make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
+            if (one()) {
+              uint8_t* v0 = smem + v_off(bv);
+              for (int r = keys; r < ((keys + 15) & ~15); ++r)
+                for (int s = 0; s < NSL; ++s)
+                  for (int q16 = 0; q16 < 8; ++q16)
+                    *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + s * 2048 + (r & 15) * 128 + q16 * 16) =
+                        make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            join();
           }
           const uint64_t vd = vdesc0 + static_cast<uint64_t>((bv * 2 * NSL * kKVSlab) >> 4);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (j < nkt_[t]) {
               const int gt = t0_[t] + j, b = gt & 1;
-              if (!mbar_wait_fast(&bars->p_full[t][b], (gt >> 1) & 1, abort_flag, 16, lim)) {
+              if (!issue_wait(&bars->p_full[t][b], (gt >> 1) & 1)) {
                 ok = false;
                 break;
               }
@@ -582,33 +629,40 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
               const uint32_t dcol = tmem + t * C::O_COL;
               const uint32_t acol = s_col(t, b);
               const int kr = ke_[t] - j * kKeys;  // keys this Q tile sees in the tile
-              if (kr >= kKeys) {
+              if (one()) {
+                if (kr >= kKeys) {
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                  mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
-                              (j > 0 || kk > 0) ? 1u : 0u);
-              } else {
-                const int nk_t = (kr + 15) >> 4;
-                for (int kk = 0; kk < nk_t; ++kk)
-                  mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
-                              (j > 0 || kk > 0) ? 1u : 0u);
+                  for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
+                                (j > 0 || kk > 0) ? 1u : 0u);
+                } else {
+                  const int nk_t = (kr + 15) >> 4;
+                  for (int kk = 0; kk < nk_t; ++kk)
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
+                                (j > 0 || kk > 0) ? 1u : 0u);
+                }
+                mma_commit(&bars->o_done[t][b]);
               }
-              mma_commit(&bars->o_done[t][b]);
+              join();
             }
           }
           if (!ok) break;
-          mma_commit(&bars->v_empty[bv]);
+          if (one()) mma_commit(&bars->v_empty[bv]);
+          join();
           if (++bv == KVS) {
             bv = 0;
             vph ^= 1u;
           }
         }
         if (!ok) break;
-        mbar_arrive(&bars->item_empty[slot]);
+        join();
+        if (one()) mbar_arrive(&bars->item_empty[slot]);
       }
       if (!ok) *abort_flag = 1;
-      mma_commit(&bars->mma_done[2]);
-      mbar_wait(&bars->mma_done[2], 0, nullptr, 200000000ull);
+      if (one()) {
+        mma_commit(&bars->mma_done[2]);
+        mbar_wait(&bars->mma_done[2], 0, nullptr, 200000000ull);
+      }
     }
   } else if (warp >= 2 && warp < 2 + kSoftmaxWarps) {
     // ---------------------------------------------------------------- softmax
@@ -625,7 +679,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int slot = n & 1;
-      if (!warp_wait(&bars->item_full[slot], (n >> 1) & 1, abort_flag, lim)) {
+      if (!softmax_wait(&bars->item_full[slot], (n >> 1) & 1)) {
         ok = false;
         break;
       }
@@ -640,7 +694,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         float m_use = -INFINITY, l = 0.f;
         for (int kt = 0; kt < nkt; ++kt) {
           const int gt = it.t0[t] + kt, b = gt & 1;
-          if (!warp_wait(&bars->s_full[t][b], (gt >> 1) & 1, abort_flag, lim)) {
+          if (!softmax_wait(&bars->s_full[t][b], (gt >> 1) & 1)) {
             ok = false;
             break;
           }
@@ -704,7 +758,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           tmem_st32u(ts, pw);
           if (kt > 0 && __any_sync(0xffffffffu, grow)) {  // rescale this row's O
             // the PV MMA of the previous tile must be done with O first
-            if (!warp_wait(&bars->o_done[t][(gt - 1) & 1], ((gt - 1) >> 1) & 1, abort_flag, lim)) {
+            if (!softmax_wait(&bars->o_done[t][(gt - 1) & 1], ((gt - 1) >> 1) & 1)) {
               ok = false;
               break;
             }
@@ -726,7 +780,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         }
         if (!ok) break;
         const int gl = it.t0[t] + nkt - 1;
-        if (!warp_wait(&bars->o_done[t][gl & 1], (gl >> 1) & 1, abort_flag, lim)) {
+        if (!softmax_wait(&bars->o_done[t][gl & 1], (gl >> 1) & 1)) {
           ok = false;
           break;
         }

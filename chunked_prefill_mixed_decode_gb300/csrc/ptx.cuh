@@ -133,6 +133,16 @@ __device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity, c
   return mbar_wait(bar, parity, abort, limit_ns);
 }
 
+// True in one lane of a converged warp, always the same one.  Issuing tcgen05
+// instructions under it, in a loop that the whole warp runs, keeps their operands
+// in uniform registers; under `lane == 0` the compiler has to assume several
+// lanes, and one product takes about 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // named barrier among `count` threads (a multiple of 32); id 0 is __syncthreads
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
