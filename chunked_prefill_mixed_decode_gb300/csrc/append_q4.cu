@@ -173,9 +173,8 @@ struct ReadQ4Args {
 
 // Eight nibbles in K order -> their bf16 values, elements in order.
 __device__ __forceinline__ uint4 dequantize8(uint32_t word, uint32_t s2) {
-  const uint32_t c2 = q4_minus_24(s2);
-  return make_uint4(q4_scaled_pair(word, 0, s2, c2), q4_scaled_pair(word, 1, s2, c2), q4_scaled_pair(word, 2, s2, c2),
-                    q4_scaled_pair(word, 3, s2, c2));
+  return make_uint4(q4_pair_times(word, 0, s2), q4_pair_times(word, 1, s2), q4_pair_times(word, 2, s2),
+                    q4_pair_times(word, 3, s2));
 }
 
 // One thread per quarter of one (slot, KV head) row of K and of V: 8 elements

@@ -103,8 +103,8 @@ __device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(dst[0]) : "r"(src) : "memory");
 }
 
-// Quarter t of one row (a word per group) as bf16 into a 128-byte-swizzled
-// tile: group g's eight elements are 16-byte chunk 4 g + t of the row, in slab
+// Quarter t of one row (a word per group) as bf16, a quarter of each value, into
+// a 128-byte-swizzled tile: group g's eight elements are 16-byte chunk 4 g + t of the row, in slab
 // g / 2.
 template <int D, int SLAB>
 __device__ __forceinline__ void store_row_part(uint32_t row_addr, int key, int t, const uint32_t* words,
@@ -113,10 +113,10 @@ __device__ __forceinline__ void store_row_part(uint32_t row_addr, int key, int t
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const uint32_t s2 = __byte_perm(scales[g >> 1], 0, (g & 1) ? 0x3232 : 0x1010);
-    const uint32_t c2 = q4_minus_24(s2);
+    const uint32_t c2 = q4_minus_6(s2);
     uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = q4_scaled_pair(words[g], i, s2, c2);
+    for (int i = 0; i < 4; ++i) x[i] = q4_quarter_pair(words[g], i, s2, c2);
     const uint32_t dst = row_addr + (g >> 1) * SLAB + ((((g & 1) * 4 + t) ^ (key & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
                  : "memory");
@@ -220,13 +220,14 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
 //
 // Over a 4-bit pool (Q4) warp 0 brings the pages of a tile as they are stored,
 // one bulk copy a page, into a ring of their own, and four more warps, 12-15,
-// write their values -- exactly bf16, so nothing else of the phase changes --
-// into the K and V stages: warp 12 + w page w of each tile.  Two chunks of 3968
-// tokens at 0 and 6000, 32 / 8 heads, D = 128: 501 us, 1.29 PFLOP/s, 0.69 of the
-// measured dense rate; the tensor pipe is 55 % and the issue slots 59 % busy.  A
-// tile pair takes about 1800 cycles, in which the softmax warps, the dequantizing
-// warps and the issuers are each busy nearly all the time: without any softmax
-// work it would take 482 us, without any dequantizing 487.
+// write a quarter of their values -- exactly bf16; the score scale and the last
+// division make up for the factor -- into the K and V stages: warp 12 + w page w
+// of each tile.  Two chunks of 3968 tokens at 0 and 6000, 32 / 8 heads, D = 128:
+// 501 us, 1.29 PFLOP/s, 0.69 of the measured dense rate; the tensor pipe is 55 %
+// and the issue slots 59 % busy.  A tile pair takes about 1800 cycles, in which
+// the softmax warps, the dequantizing warps and the issuers are each busy nearly
+// all the time: without any softmax work it would take 482 us, without any
+// dequantizing 487.
 // Measured and not kept, before the issue by elected lanes (605 us then): loads
 // from global memory into the dequantizing warps' registers a tile ahead, without
 // the ring (740 us); where items are few, one Q tile for both softmax groups, every
@@ -671,7 +672,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     const int r = quad * 32 + lane;             // query row of this thread
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tO = tmem + t * C::O_COL + lane_off;
-    const float sl2 = p.scale_log2;
+    const float sl2 = Q4 ? 4.f * p.scale_log2 : p.scale_log2;  // Q4: the tiles hold quarters
     // A row exponentiates against m_use, the largest scaled score seen when it
     // was last raised; it is raised (and O rescaled) only when a tile's max
     // exceeds it by more than 2^8, so P <= 256 and O, l stay exact in fp32.
@@ -785,7 +786,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           break;
         }
         tc_fence_after();
-        const float inv = 1.f / l;
+        const float inv = (Q4 ? 4.f : 1.f) / l;
         bf16* dst = p.out + (static_cast<int64_t>(it.tb + tl) * p.H_q + it.hk * G + r % G) * D;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {

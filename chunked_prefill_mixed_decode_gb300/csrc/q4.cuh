@@ -95,23 +95,31 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w, int i) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// A pair of values, scale * code, from s2 = (s, s) and c2 = -24 s2: with the
-// nibble n higher in the mantissa the operand is 16 + n, and
-//     (16 + n) s - 24 s = s (n - 8)
-// is one fused multiply-add.  24 s is exact (24 = 3 * 8 and s has five bits),
+// A pair of values, scale * code, from s2 = (s, s): any scale.
+__device__ __forceinline__ uint32_t q4_pair_times(uint32_t w, int i, uint32_t s2) {
+  const uint32_t r = q4_pair(w, i);
+  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&s2));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// A quarter of the same pair from s2 and c2 = -6 s2: with the nibble n higher in
+// the mantissa the operand is 4 + n / 4, and
+//     (4 + n / 4) s - 6 s = s (n - 8) / 4
+// is one fused multiply-add.  6 s is exact (6 = 3 * 2 and s has five bits) and
+// finite for every scale, which 24 s for whole values would not be from 2^123.4 on;
 // the result fits in eight bits, so the single rounding changes nothing.
-__device__ __forceinline__ uint32_t q4_scaled_pair(uint32_t w, int i, uint32_t s2, uint32_t c2) {
+__device__ __forceinline__ uint32_t q4_quarter_pair(uint32_t w, int i, uint32_t s2, uint32_t c2) {
   uint32_t r;
   const uint32_t m = i == 0 ? w << 3 : w >> (4 * i - 3);
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(m), "r"(0x00780078u), "r"(0x41804180u));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(m), "r"(0x00780078u), "r"(0x40804080u));
   const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&s2),
                                    *reinterpret_cast<const __nv_bfloat162*>(&c2));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-__device__ __forceinline__ uint32_t q4_minus_24(uint32_t s2) {
-  const uint32_t m24 = 0xc1c0c1c0u;
-  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&m24));
+__device__ __forceinline__ uint32_t q4_minus_6(uint32_t s2) {
+  const uint32_t m6 = 0xc0c0c0c0u;
+  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&s2), *reinterpret_cast<const __nv_bfloat162*>(&m6));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 

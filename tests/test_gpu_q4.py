@@ -499,6 +499,23 @@ def test_sharp_and_flat_scores(env, qscale, sigma, scale):
             a.check(scale=scale)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_largest_scales(env, D):
+    """Scales past 2^123, where 24 of them pass the largest bf16: read back exactly, and attended over."""
+    torch, ms, _ = env
+    rows = [(0, 2), (0, 3), (1, 2), (0, 1), (1, 1), (2, 1)]  # at most three keys: their sum stays below 2^128
+    a = Attn(env, rows, 8, 2, D, seed=31, sigma=2.0 ** 125, qscale=2.0 ** -110)
+    pages = a.pool.shape[0]
+    sc = a.pool[..., 16 * D:].contiguous().view(torch.bfloat16)
+    assert sc.max() > 2.0 ** 123.5 and sc.min() < 2.0 ** 123
+    k, v = (torch.empty(16 * pages, 2, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ms.kv_read_q4(a.pool, _i32(torch, np.arange(16 * pages)), k, v)
+    for got, want in zip((k, v), _values(torch, a.pool, D)):
+        assert torch.equal(got.double(), want.permute(0, 2, 1, 3).reshape(got.shape))
+    a.call(scale=2.0 ** -17)
+    a.check(scale=2.0 ** -17)
+
+
 def test_stale_bytes_past_the_context_are_not_read_as_values(env):
     """Every slot past a row's context holds code -8 and a NaN scale; so does every page of the pool that no row owns."""
     torch, ms, _ = env
