@@ -250,6 +250,9 @@ __global__ void __launch_bounds__(kMetaThreads) metadata_kernel(MetaArgs a) {
         if (i0 + j * kMetaThreads < n) a.block_tables[i0 + j * kMetaThreads] = page[j];
     }
   }
+  // An attention call directly after this one starts its prologue, which reads the rows, as soon as every
+  // CTA here has ended: what the CTA wrote is performed by then.
+  __threadfence();
   // 5. the new pages into the requests' tables, and the free count
   if (a.free_pages == nullptr) return;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMetaThreads + tid; i0 < tot_new;
@@ -267,6 +270,15 @@ __global__ void __launch_bounds__(kMetaThreads) metadata_kernel(MetaArgs a) {
     if (atomicInc(reinterpret_cast<unsigned*>(a.free_state + 1), gridDim.x - 1) == gridDim.x - 1)
       a.free_state[0] = fc - static_cast<int32_t>(tot_new);
   }
+}
+
+struct Span {
+  const int32_t* p;
+  int64_t n;
+};
+
+inline bool overlap(const Span& x, const Span& y) {
+  return x.p != nullptr && y.p != nullptr && x.n > 0 && y.n > 0 && x.p < y.p + y.n && y.p < x.p + x.n;
 }
 
 }  // namespace
@@ -287,6 +299,16 @@ extern "C" MS_API int ms_build_batch_metadata_device(
     return MS_ERR_ARG;
   const bool alloc = free_pages != nullptr;
   if (alloc != (free_count != nullptr) || alloc != (free_state != nullptr)) return MS_ERR_ARG;
+  // the kernel's CTAs read the inputs while others write the outputs
+  const int64_t R = num_rows, table_n = ragged ? cap_pages : R * bt_stride;
+  const Span in[] = {{cached_lens, R}, {new_tokens, R}, {page_tables, R * table_stride}, {free_pages, free_cap}};
+  const Span out[] = {{cu_seqlens_q, R + 1}, {q_start_pos, R}, {context_lens, R}, {positions, cap_tokens},
+                      {slot_mapping, cap_tokens}, {ragged ? bt_pages : block_tables, table_n}, {bt_offsets, R + 1},
+                      {info, 4}};
+  for (const Span& x : in)
+    for (const Span& y : out)
+      if (overlap(x, y)) return MS_ERR_ARG;
+  if (overlap(in[2], {free_state, 2}) || overlap(in[3], {free_state, 2}) || overlap(in[2], in[3])) return MS_ERR_ARG;
   MetaArgs a{cached_lens, new_tokens, page_tables, free_pages, free_count, free_state, cu_seqlens_q, q_start_pos,
              context_lens, positions, slot_mapping, block_tables, bt_offsets, bt_pages, info, dev_status,
              cap_pages, num_rows, table_stride, free_cap, num_pages, cap_tokens, bt_stride};
@@ -294,8 +316,7 @@ extern "C" MS_API int ms_build_batch_metadata_device(
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MS_ERR_CUDA;
-  const int64_t table = ragged ? cap_pages : static_cast<int64_t>(num_rows) * bt_stride;
-  const int64_t most = table > cap_tokens ? table : cap_tokens;
+  const int64_t most = table_n > cap_tokens ? table_n : cap_tokens;
   const int sms = ms_num_sms();
   if (sms <= 0) return MS_ERR_CUDA;
   int64_t blocks = (most + 4 * kMetaThreads - 1) / (4 * kMetaThreads);

@@ -164,13 +164,14 @@ class StepTables:
     ``page_tables`` [rows, stride] (device int32) are the requests' pages.  With ``free_pages`` (device int32, all of
     them free at the start) a request holds exactly the pages of its cached tokens and ``build`` takes those that it
     lacks from the end of the list; without, the tables already hold every page.  ``build`` enqueues one kernel and
-    returns a DeviceBatch over the buffers: ``max_tokens`` tokens (the ones past the step's own are pad tokens), and a
-    context bound of the whole pool.  Nothing in it depends on host data, so a step can be captured and replayed while
-    ``cached_lens`` and ``new_tokens`` change on the GPU.  ``info`` [4] and ``status`` [1] are those of
+    returns a DeviceBatch over the buffers: ``max_tokens`` tokens (the ones past the step's own are pad tokens), and
+    ``max_context`` for the sum of the contexts, by default the whole pool (requests that share pages may need more).
+    Nothing in it depends on host data, so a step can be captured and replayed while ``cached_lens`` and ``new_tokens``
+    change on the GPU.  ``info`` [4] and ``status`` [1] are those of
     build_batch_metadata_device.
     """
 
-    def __init__(self, page_tables, num_pages: int, max_tokens: int, free_pages=None):
+    def __init__(self, page_tables, num_pages: int, max_tokens: int, free_pages=None, max_context: int = None):
         import torch
         rows, stride = page_tables.shape
         dev = page_tables.device
@@ -185,7 +186,8 @@ class StepTables:
         if free_pages is not None:
             self.free_state = torch.tensor([free_pages.numel(), 0], dtype=torch.int32, device=dev)
         self.batch = DeviceBatch(self.cu_seqlens_q, self.q_start_pos, self.context_lens, self.positions,
-                                 self.slot_mapping, self.block_tables, rows, int(max_tokens), 0, 16 * self.num_pages, {})
+                                 self.slot_mapping, self.block_tables, rows, int(max_tokens), 0,
+                                 16 * self.num_pages if max_context is None else int(max_context), {})
 
     def build(self, cached_lens, new_tokens, stream=None) -> DeviceBatch:
         free = {}

@@ -442,7 +442,8 @@ MS_API int ms_kv_read_q4(const void* kv_cache, int32_t num_pages, const int32_t*
  * rows, workspace (ms_attention_workspace_size), status bits, limits and
  * errors, with K[j] and V[j] the values that the cache holds.  Scores and
  * softmax statistics in fp32; the weights of V are rounded to bf16 before
- * their products, as in the bf16 call.
+ * their products, as in the bf16 call.  A decode row's intermediate sums reach
+ * 20 times the score's terms: sum |q| max |K| has to stay below 2^123.
  *   kv_cache  device, the 4-bit pool of num_pages pages, 16-byte aligned
  * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
 MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
@@ -489,8 +490,10 @@ MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, i
  * outside 0..free_cap), MS_STATUS_NO_PAGES (a row longer than table_stride
  * pages, or the free list too short).  A page id outside the pool gets slot
  * -1 and records MS_STATUS_BAD_PAGE.  Calls that share free_state must not
- * overlap on the GPU.
- * Errors: MS_ERR_ARG (also cap_tokens above 2^21), MS_ERR_CUDA. */
+ * overlap on the GPU.  No output may overlap cached_lens, new_tokens,
+ * page_tables or free_pages (the GPU reads them while it writes).
+ * Errors: MS_ERR_ARG (also cap_tokens above 2^21, overlapping arrays),
+ * MS_ERR_CUDA. */
 MS_API int ms_build_batch_metadata_device(
     const int32_t* cached_lens, const int32_t* new_tokens, int32_t num_rows, int32_t* page_tables,
     int32_t table_stride, const int32_t* free_pages, int32_t free_cap, const int32_t* free_count,

@@ -724,6 +724,40 @@ def test_step_tables_and_run_step(env):
     assert int(tables.free_state[0]) == count
 
 
+def test_attention_straight_after_the_tables(env):
+    """No append between the metadata and the attention that reads it: requests that share all their pages but the last
+    (contexts that sum to more than the pool), lengths changing under one captured pair of calls."""
+    torch, ms, step = env
+    H_q, H_kv, D, R, pages, stride, cap = 8, 2, 64, 40, 90, 50, 96
+    pool = _pool(torch, pages, H_kv, D, 60)
+    host_tab = np.array([np.r_[np.arange(stride - 1), stride - 1 + s] for s in range(R)])
+    tables = step.StepTables(_i32(torch, host_tab), pages, cap, max_context=R * stride * 16)
+    c, d = _i32(torch, [0] * R), _i32(torch, [0] * R)
+    q = torch.randn(cap, H_q, D, device="cuda").to(torch.bfloat16)
+    out = torch.zeros_like(q)
+    ws = step.workspace_for(tables.batch, H_q, H_kv, D, "cuda")
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=st):
+        b = tables.build(c, d)
+        ms.mixed_step_attention_q4(q, pool, b.cu_seqlens_q, b.q_start_pos, b.context_lens, b.block_tables, b.context_total,
+                                   out, ws)
+    rng = np.random.default_rng(61)
+    for n in range(12):
+        new = np.where(rng.random(R) < 0.2, 0, 1)
+        new[int(rng.integers(R))] = int(rng.integers(2, cap - R))
+        cached = rng.integers(0, 16 * stride - cap, R)
+        c.copy_(_i32(torch, cached))
+        d.copy_(_i32(torch, new))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ms.read_status(ws) == 0 and ms.read_status(tables.status) == 0
+        a = Attn(env, [(int(x) if y else 0, int(y)) for x, y in zip(cached, new)], H_q, H_kv, D, pool=pool)
+        a.pages = [host_tab[s, :-(-int(x + y) // 16)] if y else [] for s, (x, y) in enumerate(zip(cached, new))]
+        a.q, a.ws, a.out = q, ws, out[:a.T].clone()
+        a.check()
+
+
 @pytest.mark.parametrize("H_q,H_kv,D,seed", [(4, 2, 64, 50), (8, 1, 128, 52)])
 def test_engine_rounds_over_a_4_bit_pool(env, H_q, H_kv, D, seed):
     """Random arrivals through the engine and the round driver, pages freed and handed out again: the pool's bytes are

@@ -151,6 +151,29 @@ def test_abi_refusals(ms):
         assert meta(**kw) == ms.MS_ERR_ARG, kw
 
 
+def test_metadata_refuses_overlapping_arrays(ms):
+    """Inputs that an output would overwrite while other CTAs read them."""
+    lib, R, ts, cap, fcap = ms.lib(), 5, 6, 40, 7
+    at = {n: (i + 1) << 20 for i, n in enumerate("c d tab free fc fs cu qs ctx pos slot bt off btp info".split())}
+    sizes = dict(c=R, d=R, tab=R * ts, free=fcap, fs=2, cu=R + 1, qs=R, ctx=R, pos=cap, slot=cap, bt=R * 8, off=R + 1, btp=30,
+                 info=4)
+
+    def meta(ragged, **kw):
+        a = {**at, **kw}
+        return lib.ms_build_batch_metadata_device(
+            a["c"], a["d"], R, a["tab"], ts, a["free"], fcap, a["fc"], a["fs"], 50, cap, a["cu"], a["qs"], a["ctx"], a["pos"],
+            a["slot"], None if ragged else a["bt"], 0 if ragged else 8, a["off"] if ragged else None,
+            a["btp"] if ragged else None, 30 if ragged else 0, a["info"], None, None)
+
+    for ragged in (False, True):
+        for src in ("c", "d", "tab", "free"):
+            for dst in ("cu", "qs", "ctx", "pos", "slot", "info") + (("off", "btp") if ragged else ("bt",)):
+                for to in (at[src], at[src] + 4 * (sizes[src] - 1), at[src] - 4 * (sizes[dst] - 1)):  # alike, last, first word
+                    assert meta(ragged, **{dst: to}) == ms.MS_ERR_ARG, (src, dst)
+        assert meta(ragged, free=at["tab"] + 4) == ms.MS_ERR_ARG
+        assert meta(ragged, fs=at["tab"]) == ms.MS_ERR_ARG and meta(ragged, fs=at["free"] - 4) == ms.MS_ERR_ARG
+
+
 def test_binding_refusals(ms):
     torch = pytest.importorskip("torch")
     bf, i32 = torch.bfloat16, torch.int32
