@@ -205,13 +205,9 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
     for (int pi = 0; pi < np; pi += 2, rem -= 2 * kPage) {
       __syncwarp();  // every lane is done with the stage before
       issue_pair(st == 0 ? NST - 1 : st - 1);
-      if (!mbar_wait(full + st, ph, nullptr)) {
-        failed = true;
-        break;
-      }
-      --in_flight;
+      // a lane whose wait gave up goes on within the stage's bounds to the vote below
+      const bool late = !mbar_wait(full + st, ph, nullptr);
       const uint32_t stage = ring + st * C::STAGE;
-      next_stage();
       const int n_half = pi + 1 < np ? 2 : 1;
       // S^T: lane holds (row ra, heads 2 tq, 2 tq + 1) and (row ra + 8, same heads) of each page
       float s[2][4];
@@ -256,7 +252,11 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
       // past it by more than 2^8 do they look for the heads' maxima
       float mh0 = fmaxf(fmax3(s[0][0], s[0][2], s[1][0]), s[1][2]) * sl2;
       float mh1 = fmaxf(fmax3(s[0][1], s[0][3], s[1][1]), s[1][3]) * sl2;
-      if (__any_sync(0xffffffffu, mh0 > mu0 + kRescaleLog2 || mh1 > mu1 + kRescaleLog2)) {
+      if (__any_sync(0xffffffffu, late || mh0 > mu0 + kRescaleLog2 || mh1 > mu1 + kRescaleLog2)) {
+        if (__any_sync(0xffffffffu, late)) {
+          failed = true;
+          break;
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           mh0 = fmaxf(mh0, __shfl_xor_sync(0xffffffffu, mh0, o));
@@ -286,6 +286,8 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
         l0 += s[h][0] + s[h][2];
         l1 += s[h][1] + s[h][3];
       }
+      --in_flight;
+      next_stage();
       // O^T += V^T (P s)^T, page by page and group by group
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
