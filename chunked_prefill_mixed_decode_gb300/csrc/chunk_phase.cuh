@@ -104,8 +104,8 @@ __device__ __forceinline__ void lds_words(uint32_t src, uint32_t* dst) {
 }
 
 // Quarter t of one row (a word per group) as bf16, a quarter of each value, into
-// a 128-byte-swizzled tile: group g's eight elements are 16-byte chunk 4 g + t of the row, in slab
-// g / 2.
+// a 128-byte-swizzled tile: group g's eight elements are 16-byte chunk 4 g + t of
+// the row, in slab g / 2.
 template <int D, int SLAB>
 __device__ __forceinline__ void store_row_part(uint32_t row_addr, int key, int t, const uint32_t* words,
                                                const uint32_t* scales) {
