@@ -47,6 +47,7 @@ enum {
   H_CHUNK_CTAS = 9,  // CTAs that start on chunk work (the rest start on decodes)
   H_CLOCK_MHZ = 10,  // SM clock the last call ran at (kept across calls; 0 in a fresh workspace)
   H_TEAM = 11,       // warps that share a decode item, where the kernel runs them in teams
+  H_CH_TILES = 12,   // KV tiles to a part of a chunk item (0: items are whole), where the kernel splits them
   H_WORDS = 64
 };
 
@@ -91,6 +92,26 @@ struct AttnParams {
   float* part_acc;
   uint64_t wait_limit_ns;  // bound of every chunk-phase wait
   int32_t test_stall;      // test hook: chunk-phase producers publish no work item (0 in every real call)
+  // chunk items in parts (4-bit pools), in what the workspace has behind its layout: room for ch_cap
+  // parts of ch_rec query rows (ChunkParts)
+  uint8_t* ch_parts;
+  int32_t ch_cap, ch_rec;
+};
+
+// Where the parts' records lie: sums of O first ([part][row][D]), (max, sum)
+// ([part][row]), the parts' table, then counters per item and Q tile.
+struct ChunkParts {
+  float* acc;
+  float2* ml;
+  int2* items;
+  int32_t* cnt;
+  __device__ __forceinline__ explicit ChunkParts(const AttnParams& p) {
+    const int64_t rows = static_cast<int64_t>(p.ch_cap) * p.ch_rec;
+    acc = reinterpret_cast<float*>(p.ch_parts);
+    ml = reinterpret_cast<float2*>(p.ch_parts + rows * p.D * 4);
+    items = reinterpret_cast<int2*>(p.ch_parts + rows * (p.D * 4 + 8));
+    cnt = reinterpret_cast<int32_t*>(items + p.ch_cap);
+  }
 };
 
 __host__ __device__ inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -147,6 +168,14 @@ __device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsi
   if (!chunk) return static_cast<int>((static_cast<unsigned>(c + kPage) / kPage + split - 1) / split);
   const int n_qt = (d + tpt - 1) / tpt;
   return (n_qt + 1) >> 1;
+}
+
+constexpr int kChunkTile = 64;  // keys per KV tile of a chunk item
+constexpr int kMinPartedTiles = 15;  // items of up to this many are not cut (chunk_part_tiles would not cut them)
+
+// Parts of a chunk row's items, of `tiles` KV tiles or fewer each.
+__device__ __forceinline__ int chunk_parts(int c, int d, int tiles) {
+  return static_cast<int>((static_cast<unsigned>(c + d + kChunkTile - 1) / kChunkTile + tiles - 1) / tiles);
 }
 
 // 128x128 tiles of a chunk row's Q tiles against their causal key ranges (the
@@ -317,6 +346,88 @@ __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_
   return dec_candidate(static_cast<int>(best & 31u));
 }
 
+// KV tiles to a part of a chunk item, or 0 for whole items.  Items are cut where
+// they are fewer than half the CTAs that chunk work gets beside the decodes (k,
+// the balance of chunk_cta_split): every part then starts at once.  Parts are
+// written out and the last one to finish joins them, which costs about 0.0125 us a
+// part and row where a tile takes about 1 us, hence the square root; 8 tiles and a
+// 32nd of the longest item at least, and only for a fifth of its time or more.
+// pairs, pair_tiles: of one KV head, over the rows (a Q tile alone takes about the
+// time of a pair).  32 / 8 heads, D = 128, whole and in parts: 20 tokens at 28000
+// 342 and 72 us, 4 at 100000 1192 and 95 us, 128 at 8000 beside 16 decodes 132 and
+// 71 us, four rows of 32 at 3000 to 6000 84 and 52 us.
+__device__ __forceinline__ int chunk_part_tiles(const AttnParams& p, float pairs, float pair_tiles, float longest,
+                                                float dec_pages) {
+  const float n0 = pairs * p.H_kv, work = pair_tiles * p.H_kv;
+  const float T = work * __fdividef(p.tile_cycles * 1000.f, p.sm_mhz), g = p.dec_bytes_cycle * p.sm_mhz * 1e-3f;
+  const float B = dec_pages * p.H_kv * kPage * p.key_bytes;
+  const float k = fminf(p.num_sms * __fdividef(T * g, B + T * g), static_cast<float>(p.ch_cap)) - 1.f;
+  if (!(n0 >= 1.f && 2.f * n0 <= k)) return 0;
+  const float row_us = 0.0125f * min(p.ch_rec, 128);
+  const float tiles = ceilf(fmaxf(fmaxf(8.f, longest * (1.f / 32)), fmaxf(__fdividef(work, k - n0), sqrtf(row_us * longest))));
+  const float cut = tiles + row_us * (__fdividef(longest, tiles) + 4.f) + 4.f;
+  return cut < 0.8f * longest ? static_cast<int>(tiles) : 0;
+}
+
+// chunk_part_tiles for a chunk row per lane (keys: its context, or 0; np: its pairs).
+__device__ __noinline__ int plan_parts_warp(const AttnParams& p, int keys, int np, int64_t dec_pages) {
+  const int n_kt = (keys + kChunkTile - 1) / kChunkTile, longest = __reduce_max_sync(0xffffffffu, n_kt);
+  if (longest <= kMinPartedTiles) return 0;
+  const int64_t pair_tiles = warp_sum31(static_cast<int>(min(static_cast<int64_t>(np) * n_kt, int64_t{0x7fffffff})));
+  return chunk_part_tiles(p, static_cast<float>(__reduce_add_sync(0xffffffffu, np)), static_cast<float>(pair_tiles),
+                          static_cast<float>(longest), static_cast<float>(dec_pages));
+}
+
+// chunk_part_tiles for the rows of a block, from their values in shared memory.  Called by every
+// thread.  Both forms are out of line: the prologue runs from a cold instruction cache, and most
+// steps need neither.
+__device__ __noinline__ int plan_parts_block(const AttnParams& p, const int* rd, const int* rc, int64_t dec_pages) {
+  __shared__ long long s_tiles[32];
+  __shared__ int s_pairs[32], s_longest[32];
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+  int64_t tiles = 0;
+  int pairs = 0, longest = 0;
+  for (int s = tid; s < p.num_rows; s += nt) {
+    const int c = rc[s], d = rd[s];
+    if (d <= 1) continue;
+    const int np = row_items(true, c, d, 128 / p.G, 1u), n_kt = chunk_parts(c, d, 1);
+    pairs += np;
+    tiles += static_cast<int64_t>(np) * n_kt;
+    longest = max(longest, n_kt);
+  }
+  tiles = warp_sum64(tiles);
+  pairs = __reduce_add_sync(0xffffffffu, pairs);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    s_tiles[warp] = tiles;
+    s_pairs[warp] = pairs;
+    s_longest[warp] = longest;
+  }
+  __syncthreads();
+  tiles = pairs = longest = 0;
+  for (int j = 0; j < nw; ++j) {
+    tiles += s_tiles[j];
+    pairs += s_pairs[j];
+    longest = max(longest, s_longest[j]);
+  }
+  if (longest <= kMinPartedTiles) return 0;
+  return chunk_part_tiles(p, static_cast<float>(pairs), static_cast<float>(tiles), static_cast<float>(longest),
+                          static_cast<float>(dec_pages));
+}
+
+// Table entries and counters of a chunk row in parts, from place `first`: `items` of
+// them per KV head, the parts of a pair neighbours.  The first word is the row's
+// position k in the list and, above it, the part.  By one warp.
+__device__ __noinline__ void chunk_part_table(const AttnParams& p, int first, int k, int items, int parts, bool head_major,
+                                              int lane) {
+  const ChunkParts cp(p);
+  for (int i = lane; i < items * p.H_kv; i += 32) {
+    const int j = i / parts;
+    cp.items[first + i] = make_int2(k | ((i - j * parts) << 16), chunk_entry(j, items / parts, p.H_kv, head_major));
+    reinterpret_cast<int2*>(cp.cnt)[first + i] = make_int2(0, 0);
+  }
+}
+
 // First word of a decode row's table entries: its position k in the list, and for
 // teams, which look every word of a split up at once, its row above that.
 template <bool Teams>
@@ -398,7 +509,13 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const uint4 v = k4[m];
     rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
   }
-  const int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
+  int part_tiles = 0, parts = 1;
+  int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
+  if (Teams && 2 * n_ch * p.H_kv < p.num_sms &&  // the least that chunk_part_tiles needs
+      __reduce_max_sync(0xffffffffu, is_ch ? ctx : 0) > kMinPartedTiles * kChunkTile) {
+    part_tiles = plan_parts_warp(p, is_ch ? ctx : 0, is_ch ? items : 0, dec_pages);
+    if (part_tiles > 0 && is_ch) items *= parts = chunk_parts(c, d, part_tiles);
+  }
   const int q = (is_ch ? n_dec : 0) + rank;  // queue position
   if (listed) s_items[q] = items;
   __syncwarp();
@@ -419,7 +536,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int64_t n_dec_items = static_cast<int64_t>(dec_tot) * p.H_kv;
   const int64_t n_ch_items = static_cast<int64_t>(ch_tot) * p.H_kv;
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
-  const bool ch_over = n_ch_items > p.max_ch_items;
+  const bool ch_over = n_ch_items > (part_tiles > 0 ? p.ch_cap : p.max_ch_items);
   const int64_t tiles =
       warp_sum31(is_ch ? static_cast<int>(min(static_cast<int64_t>(chunk_tiles(c, d, tpt)) * p.H_kv,
                                                 int64_t{0x7fffffff}))
@@ -443,6 +560,11 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const int src = __ffs(pend) - 1;
     const int r_rank = __shfl_sync(0xffffffffu, rank, src), r_items = __shfl_sync(0xffffffffu, items, src);
     const int r_before = __shfl_sync(0xffffffffu, before, src);
+    if (Teams && part_tiles > 0) {
+      chunk_part_table(p, (r_before - dec_tot) * p.H_kv, r_rank, r_items, __shfl_sync(0xffffffffu, parts, src), sp.head_major,
+                       lane);
+      continue;
+    }
     int2* out = p.ch_items + static_cast<int64_t>(r_before - dec_tot) * p.H_kv;
     for (int i = lane; i < r_items * p.H_kv; i += 32)
       out[i] = make_int2(r_rank, chunk_entry(i, r_items, p.H_kv, sp.head_major));
@@ -462,7 +584,10 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_DEC_CTR] = 0;
     hdr[H_CH_CTR] = 0;
     hdr[H_SPLIT] = split;
-    if (Teams) hdr[H_TEAM] = plan.team;
+    if (Teams) {
+      hdr[H_TEAM] = plan.team;
+      hdr[H_CH_TILES] = part_tiles;
+    }
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -566,6 +691,9 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   // 2. decode split size
   const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
   const int split = plan.split;
+  const int part_tiles = Teams && 2 * n_ch * p.H_kv < p.num_sms && chunk_keys > kMinPartedTiles * kChunkTile &&
+                                 (p.cu[S] - n_dec) / 128 * p.G * p.H_kv < p.num_sms  // the least that it needs
+                             ? plan_parts_block(p, rd, rc, dec_pages) : 0;
   const int tpt = 128 / p.G;
   const unsigned split32 = static_cast<unsigned>(split);
   // 3. the two lists in input order: decode rows at lst[0, n_dec), chunk rows after them
@@ -616,7 +744,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     }
     const int row = lst[j], c = rc[row], d = rd[row];
     (ch ? p.ch_rows : p.dec_rows)[rank] = row;
-    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32);
+    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32) * (Teams && ch && part_tiles > 0 ? chunk_parts(c, d, part_tiles) : 1);
     if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(chunk_tiles(c, d, tpt)) * p.H_kv);
   }
   __syncthreads();
@@ -642,7 +770,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   const int64_t n_dec_items = static_cast<int64_t>(dec_tot) * p.H_kv;
   const int64_t n_ch_items = static_cast<int64_t>(ch_tot) * p.H_kv;
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
-  const bool ch_over = n_ch_items > p.max_ch_items;
+  const bool ch_over = n_ch_items > (part_tiles > 0 ? p.ch_cap : p.max_ch_items);
   // 7. item tables.  Decode rows, a thread per row: entry pref[q] + i -> (row
   // k, split i), one entry per split (a work item is an entry and a KV head).
   // Then the SM split, which also orders the chunk items; chunk rows, a warp
@@ -664,6 +792,12 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   __syncthreads();
   for (int q = n_dec + warp; q < n_tot && !ch_over; q += nw) {
     const int np = pref[q + 1] - pref[q];
+    if (Teams && part_tiles > 0) {
+      const int row = p.ch_rows[q - n_dec];
+      chunk_part_table(p, (pref[q] - dec_tot) * p.H_kv, q - n_dec, np, chunk_parts(rc[row], rd[row], part_tiles),
+                       s_split.head_major, lane);
+      continue;
+    }
     int2* out = p.ch_items + static_cast<int64_t>(pref[q] - dec_tot) * p.H_kv;
     for (int i = lane; i < np * p.H_kv; i += 32)
       out[i] = make_int2(q - n_dec, chunk_entry(i, np, p.H_kv, s_split.head_major));
@@ -685,7 +819,10 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_DEC_CTR] = 0;
       hdr[H_CH_CTR] = 0;
       hdr[H_SPLIT] = static_cast<int32_t>(split);
-      if (Teams) hdr[H_TEAM] = plan.team;
+      if (Teams) {
+        hdr[H_TEAM] = plan.team;
+        hdr[H_CH_TILES] = part_tiles;
+      }
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }
@@ -828,6 +965,20 @@ inline bool encode_bf16(EncodeTiledFn fn, CUtensorMap* map, const void* base, in
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides_bytes, box, elem,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What a workspace holds behind its layout for chunk items in parts: bytes of one
+// part of `rec` query rows (table entry, two counters, then (max, sum) and D sums a row),
+// and of kPartItems of them, about one for every SM (of steps of at most max_tokens tokens).
+constexpr int kPartItems = 152;
+
+inline int part_rows(int64_t tokens, int64_t G) { return static_cast<int>(tokens * G < 256 ? tokens * G : 256); }
+
+inline size_t part_bytes(int rec, int64_t D) { return 16 + static_cast<size_t>(rec) * (8 + 4 * static_cast<size_t>(D)); }
+
+inline size_t parts_total(int64_t max_tokens, int64_t H_q, int64_t H_kv, int64_t D) {
+  if (max_tokens < 2) return 0;
+  return align_up(kPartItems * part_bytes(part_rows(max_tokens, H_q / H_kv), D), 256);
 }
 
 // Per-device host state (devices 0 .. kMaxDevices - 1): the SM count and which
@@ -994,6 +1145,7 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
 
   p.kv_q4 = nullptr;
   p.force_chunk_ctas = -1;
+  p.ch_cap = 0;
   if (device_rates(&p.sm_mhz, &p.hbm_gbs, &p.l2_bytes) != MS_OK) return MS_ERR_CUDA;
   return MS_OK;
 }

@@ -2,6 +2,8 @@
 // new token on the tcgen05 tensor cores.
 #pragma once
 
+#include <cfloat>
+
 #include "attention_step.cuh"
 #include "q4.cuh"
 
@@ -9,7 +11,7 @@ namespace {
 
 constexpr int kQSlab = 128 * 128;  // one 128-row x 64-column bf16 slab of a Q tile (128-byte rows)
 constexpr int kKVSlab = 64 * 128;  // one 64-key x 64-column bf16 slab of a K or V tile
-constexpr int kKeys = 64;          // keys per KV tile
+constexpr int kKeys = kChunkTile;  // keys per KV tile
 constexpr int kTilePages = kKeys / kPage;
 
 template <int D>
@@ -34,6 +36,10 @@ struct ChItem {
   int kv0;      // CTA-global index of the item's first KV tile (stage and parity)
   int tok0[2], ntok[2], kv_end[2], nkt[2];  // per Q tile; ntok[1] == 0: no second tile
   int t0[2];    // per Q tile: index of its first KV tile among all tiles its softmax group ran
+  // Parts (4-bit pools): of how many this is which, and the place of the first.  c and kv_end then
+  // count from the part's first key, and n_kt and nkt are its own; ns == 1: the whole item.
+  int ns, part, item0;
+  int part_par[2];  // parity of this part among the group's
 };
 
 constexpr int kRawStages = 3;  // tiles of 4-bit pages on their way to the dequantizing warps
@@ -45,9 +51,11 @@ struct ChBars {
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [Q tile][S/P buffer]
   uint64_t item_full[2], item_empty[2];
   uint64_t mma_done[3];
+  uint64_t part_done[2], part_last[2];  // parts: group t's records are written; whether its part is the last is known
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // 4-bit pools: pages as they are stored
   uint32_t tmem;
   int abort;
+  int last[2];
   ChItem items[2];
 };
 
@@ -205,6 +213,112 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
   }
 }
 
+// ---- parts of a chunk item
+
+// The join of a Q tile's parts, at most 32, by the four warps of the group whose
+// part was the last.  A warp takes eight rows and two parts at a time, four lanes
+// to a row and a quarter of its 16-byte columns to a lane, so that 8 KB (D = 128)
+// are asked for at once; a row to a warp waits for each row's records in turn (40 us instead of 7
+// for two parts of 128 rows).
+template <int D, int G>
+__device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& it, int t, int w, int lane) {
+  constexpr int E = D / 16;  // 16-byte columns to a lane
+  const int rows = it.ntok[t] * G, ns = it.ns, q = lane & 3;
+  const ChunkParts cp(p);
+  for (int row0 = 8 * w; row0 < rows; row0 += 32) {
+    const int row = row0 + (lane >> 2);
+    const bool valid = row < rows;
+    const int64_t first = static_cast<int64_t>(it.item0) * p.ch_rec + t * 128 + (valid ? row : row0);
+    float M = -FLT_MAX;
+#pragma unroll 8
+    for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(cp.ml + first + static_cast<int64_t>(i) * p.ch_rec).x);
+    float L = 0.f, o[4 * E];
+#pragma unroll
+    for (int j = 0; j < 4 * E; ++j) o[j] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < ns; i += 2) {  // two parts at a time (the last may be alone, and then weighs nothing)
+      float2 x[2];
+      float4 a[2][E];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t rec = first + static_cast<int64_t>(min(i + h, ns - 1)) * p.ch_rec;
+        x[h] = __ldcg(cp.ml + rec);
+        const float4* src = reinterpret_cast<const float4*>(cp.acc + rec * D) + q;
+#pragma unroll
+        for (int j = 0; j < E; ++j) a[h][j] = __ldcg(src + 4 * j);
+      }
+      if (i + 1 == ns) x[1].y = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (x[h].y == 0.f) continue;  // no key of the row in this part, and no record of sums
+        const float wt = ex2(x[h].x - M);
+        L += wt * x[h].y;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          o[4 * j] = fmaf(wt, a[h][j].x, o[4 * j]);
+          o[4 * j + 1] = fmaf(wt, a[h][j].y, o[4 * j + 1]);
+          o[4 * j + 2] = fmaf(wt, a[h][j].z, o[4 * j + 2]);
+          o[4 * j + 3] = fmaf(wt, a[h][j].w, o[4 * j + 3]);
+        }
+      }
+    }
+    if (valid) {
+      const float inv = 4.f / L;  // the records hold quarters
+      bf16* dst = p.out + (static_cast<int64_t>(it.tb + it.tok0[t] + row / G) * p.H_q + it.hk * G + row % G) * D;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o[4 * j] * inv, o[4 * j + 1] * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+        *reinterpret_cast<uint2*>(dst + 16 * j + 4 * q) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+  }
+}
+
+// The end of a part for the four warps of group t: each row's reference maximum
+// (log2 units), sum and O as it is in TMEM into the part's records; the last part
+// of the item to get here joins them all.  False when a wait gave up.
+template <int D, int G>
+__device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, const ChItem& it, int t, float m, float l, uint32_t tO,
+                                      const volatile int* abort_flag, uint64_t lim) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = quad * 32 + lane;
+  const bool valid = r / G < it.ntok[t];
+  const int64_t rec = static_cast<int64_t>(it.item0 + it.part) * p.ch_rec + t * 128 + r;
+  const ChunkParts cp(p);
+  if (valid) cp.ml[rec] = make_float2(m, l);
+  if (it.nkt[t] > 0) {
+#pragma unroll 1
+    for (int cc = 0; cc < D / 32; ++cc) {
+      uint32_t rr[32];
+      tmem_ld32(tO + cc * 32, rr);
+      tmem_wait_ld();
+      reg_fence32(rr);
+      if (valid) {
+        uint4* dst = reinterpret_cast<uint4*>(cp.acc + rec * D + cc * 32);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(rr[4 * j], rr[4 * j + 1], rr[4 * j + 2], rr[4 * j + 3]);
+      }
+      __syncwarp();
+    }
+  }
+  __threadfence();  // this part's records are visible before it is counted
+  mbar_arrive(&bars->part_done[t]);
+  if (quad == 0) {
+    if (!warp_wait_fast(&bars->part_done[t], it.part_par[t], abort_flag, lim)) return false;
+    if (lane == 0) {
+      bars->last[t] = atomicAdd(cp.cnt + 2 * it.item0 + t, 1) == it.ns - 1;
+      mbar_arrive(&bars->part_last[t]);
+    }
+  }
+  if (!warp_wait_fast(&bars->part_last[t], it.part_par[t], abort_flag, lim)) return false;
+  if (bars->last[t]) {
+    __threadfence();
+    merge_parts<D, G>(p, it, t, quad, lane);
+  }
+  return true;
+}
+
 // Chunk phase.  Warp 0 owns the work queue and streams Q and K/V with TMA (K
 // one tile ahead of V); warps 2-5 and 6-9 are two softmax groups, group t
 // owning Q tile t of the current pair, one query row per thread over 64-key
@@ -284,6 +398,11 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         mbar_init(&bars->raw_full[i], 1);
         mbar_init(&bars->raw_empty[i], kDequantWarps);
       }
+    if constexpr (Q4)
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&bars->part_done[t], 128);
+        mbar_init(&bars->part_last[t], 1);
+      }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -357,6 +476,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
       return true;
     };
+    const int part_tiles = Q4 ? p.hdr[H_CH_TILES] : 0;
+    int kt0 = 0;                // the part's first KV tile
+    int parts_run[2] = {0, 0};  // parts run by each softmax group so far
     while (ok) {
       int item = 0;
       if (lane == 0) item = atomicAdd(p.hdr + H_CH_CTR, 1);
@@ -369,8 +491,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       ChItem it;
       it.row = -1;
       if (item < n_items) {
-        const int2 kl = __ldg(p.ch_items + item);  // (chunk row index, KV head << 16 | pair from the last)
-        const int k = kl.x;
+        // (chunk row index and, above it, the part; KV head << 16 | pair from the last)
+        const int2 kl = __ldg((Q4 && part_tiles > 0 ? ChunkParts(p).items : p.ch_items) + item);
+        const int k = Q4 ? kl.x & 0xffff : kl.x;
         it.row = __ldg(p.ch_rows + k);
         it.tb = __ldg(p.cu + it.row);
         const int d = __ldg(p.cu + it.row + 1) - it.tb;
@@ -389,9 +512,32 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           it.ntok[t] = has ? min(TPT, d - qt * TPT) : 0;
           it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
           it.nkt[t] = (it.kv_end[t] + kKeys - 1) / kKeys;
+          it.n_kt = max(it.n_kt, it.nkt[t]);
+        }
+        if constexpr (Q4) {
+          it.ns = 1;
+          kt0 = 0;
+          if (part_tiles > 0) {
+            const int ns_row = chunk_parts(it.c, d, part_tiles), per = (it.n_kt + ns_row - 1) / ns_row;
+            it.ns = (it.n_kt + per - 1) / per;
+            it.part = kl.x >> 16;
+            it.item0 = item - it.part;
+            kt0 = it.part * per;
+            if (it.part >= it.ns) continue;  // an earlier pair of the row, with fewer tiles
+            it.c -= kt0 * kKeys;
+            it.n_kt = 0;
+            for (int t = 0; t < 2; ++t) {
+              it.kv_end[t] -= kt0 * kKeys;
+              it.nkt[t] = it.kv_end[t] > 0 ? min(per, (it.kv_end[t] + kKeys - 1) / kKeys) : 0;
+              it.n_kt = max(it.n_kt, it.nkt[t]);
+              it.part_par[t] = parts_run[t] & 1;
+              parts_run[t] += it.ns > 1 && it.ntok[t] > 0;
+            }
+          }
+        }
+        for (int t = 0; t < 2; ++t) {
           it.t0[t] = t_run[t];
           t_run[t] += it.nkt[t];
-          it.n_kt = max(it.n_kt, it.nkt[t]);
         }
         it.kv0 = g;
       }
@@ -415,7 +561,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
                     &bars->q_full);
       }
       const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-      const int32_t* btrow = row_table(p, it.row);
+      const int32_t* btrow = row_table(p, it.row) + (Q4 ? kt0 * kTilePages : 0);
       const int n_pages = (kv_max + kPage - 1) / kPage;
       // lane L < 4 holds the page id of page L of the current tile; the next tile's is in flight
       int pg_cur = lane < kTilePages && lane < n_pages ? __ldg(btrow + lane) : 0;
@@ -520,7 +666,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         if (row < 0) break;
         const int nkt = it.nkt[t], t0 = it.t0[t], n_kt = it.n_kt;
         const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-        if (nkt > 0 && !issue_wait_item(&bars->q_full, n & 1)) {
+        if ((Q4 || nkt > 0) && !issue_wait_item(&bars->q_full, n & 1)) {
           ok = false;
           break;
         }
@@ -692,7 +838,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const bool valid = (r / G) < it.ntok[t];
         const int pos = it.c + (valid ? tl : it.tok0[t] + it.ntok[t] - 1);
         const int warp_min_pos = it.c + it.tok0[t] + (quad * 32) / G;  // smallest position of this warp's rows
-        float m_use = -INFINITY, l = 0.f;
+        // (a row may see no key of its part: from the lowest finite number its masked
+        // scores have weight 0)
+        float m_use = Q4 ? -FLT_MAX : -INFINITY, l = 0.f;
         for (int kt = 0; kt < nkt; ++kt) {
           const int gt = it.t0[t] + kt, b = gt & 1;
           if (!softmax_wait(&bars->s_full[t][b], (gt >> 1) & 1)) {
@@ -786,35 +934,43 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           break;
         }
         tc_fence_after();
-        const float inv = (Q4 ? 4.f : 1.f) / l;
-        bf16* dst = p.out + (static_cast<int64_t>(it.tb + tl) * p.H_q + it.hk * G + r % G) * D;
+        if (Q4 && it.ns > 1) {
+          ok = end_part<D, G>(p, bars, it, t, m_use, l, tO, abort_flag, lim);
+        } else {
+          const float inv = (Q4 ? 4.f : 1.f) / l;
+          const bool valid_row = Q4 ? r / G < it.ntok[t] : valid;  // read again: a register less in the loop
+          bf16* dst = p.out + (static_cast<int64_t>(it.tb + (Q4 ? it.tok0[t] + r / G : tl)) * p.H_q + it.hk * G + r % G) * D;
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t rr[32];
-          tmem_ld32(tO + cc * 32, rr);
-          tmem_wait_ld();
-          reg_fence32(rr);
-          if (valid) {
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t rr[32];
+            tmem_ld32(tO + cc * 32, rr);
+            tmem_wait_ld();
+            reg_fence32(rr);
+            if (valid_row) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 u;
-              __nv_bfloat162 h0 =
-                  __floats2bfloat162_rn(__uint_as_float(rr[j]) * inv, __uint_as_float(rr[j + 1]) * inv);
-              __nv_bfloat162 h1 =
-                  __floats2bfloat162_rn(__uint_as_float(rr[j + 2]) * inv, __uint_as_float(rr[j + 3]) * inv);
-              __nv_bfloat162 h2 =
-                  __floats2bfloat162_rn(__uint_as_float(rr[j + 4]) * inv, __uint_as_float(rr[j + 5]) * inv);
-              __nv_bfloat162 h3 =
-                  __floats2bfloat162_rn(__uint_as_float(rr[j + 6]) * inv, __uint_as_float(rr[j + 7]) * inv);
-              u.x = *reinterpret_cast<uint32_t*>(&h0);
-              u.y = *reinterpret_cast<uint32_t*>(&h1);
-              u.z = *reinterpret_cast<uint32_t*>(&h2);
-              u.w = *reinterpret_cast<uint32_t*>(&h3);
-              *reinterpret_cast<uint4*>(dst + cc * 32 + j) = u;
+              for (int j = 0; j < 32; j += 8) {
+                uint4 u;
+                __nv_bfloat162 h0 =
+                    __floats2bfloat162_rn(__uint_as_float(rr[j]) * inv, __uint_as_float(rr[j + 1]) * inv);
+                __nv_bfloat162 h1 =
+                    __floats2bfloat162_rn(__uint_as_float(rr[j + 2]) * inv, __uint_as_float(rr[j + 3]) * inv);
+                __nv_bfloat162 h2 =
+                    __floats2bfloat162_rn(__uint_as_float(rr[j + 4]) * inv, __uint_as_float(rr[j + 5]) * inv);
+                __nv_bfloat162 h3 =
+                    __floats2bfloat162_rn(__uint_as_float(rr[j + 6]) * inv, __uint_as_float(rr[j + 7]) * inv);
+                u.x = *reinterpret_cast<uint32_t*>(&h0);
+                u.y = *reinterpret_cast<uint32_t*>(&h1);
+                u.z = *reinterpret_cast<uint32_t*>(&h2);
+                u.w = *reinterpret_cast<uint32_t*>(&h3);
+                *reinterpret_cast<uint4*>(dst + cc * 32 + j) = u;
+              }
             }
           }
         }
+      } else if (Q4 && it.ns > 1 && it.ntok[t] > 0) {  // the part's keys come after all of the tile's tokens
+        ok = end_part<D, G>(p, bars, it, t, -FLT_MAX, 0.f, tO, abort_flag, lim);
       }
+      if (Q4 && !ok) break;
       // O has been read: the next item's first PV may overwrite it
       tc_fence_before();
       mbar_arrive(&bars->item_empty[slot]);

@@ -227,7 +227,9 @@ MS_API int ms_kv_append_rope(const void* q, const void* k, const void* v,
  * the status word, then queue counters and the step's plan (word 9: how many
  * CTAs started on chunk work) and, kept across calls, word 10: the SM clock
  * in MHz the last call measured, which the next call's SM-split cost model
- * uses.  Zero the whole workspace once before its first use. */
+ * uses.  For steps of more than one token the last part, up to 20 MB, is room
+ * for ms_mixed_step_attention_q4 to cut few long chunk items into parts; no
+ * other call uses it.  Zero the whole workspace once before its first use. */
 MS_API size_t ms_attention_workspace_size(int32_t max_rows, int32_t max_tokens, int64_t max_context_total,
                                           int32_t H_q, int32_t H_kv, int32_t D);
 
@@ -314,10 +316,10 @@ MS_API int ms_mixed_step(const void* q, const void* k, const void* v, const int3
  * code on a per-step path should not call cudaMalloc (it may synchronise the
  * device and stall other streams).  This call allocates nothing: no
  * cudaMalloc, cudaFree or allocating library routine.  It works out of a
- * scratch array the library owns, 64 MiB per device (the step's workspace
- * size, ms_attention_workspace_size(num_rows, num_tokens, context_total, H_q,
- * H_kv, D), must not exceed it -- else MS_ERR_SCRATCH and nothing is
- * enqueued).  The array is device memory that every GPU which loads this
+ * scratch array the library owns, 64 MiB per device (the step's workspace,
+ * ms_attention_workspace_size(num_rows, num_tokens, context_total, H_q, H_kv,
+ * D) without the last part, must not exceed it -- else MS_ERR_SCRATCH and
+ * nothing is enqueued).  The array is device memory that every GPU which loads this
  * library holds until the process exits.
  *
  * The first call on a device looks up the array's device address (once per

@@ -454,6 +454,27 @@ def test_chunk_rows(env, H_q, H_kv, D):
     a.check()
 
 
+@pytest.mark.parametrize("H_q,H_kv,D", SHAPES)
+@pytest.mark.parametrize("rows", [[(5000, 2)], [(9001, 40)], [(0, 700), (6000, 3)], [(3000, 200), (3100, 130), (20, 5), (1100, 64)],
+                                  [(511, 2), (512, 2), (575, 65), (576, 129)], [(7990, 17), (4000, 1), (900, 1), (0, 0)],
+                                  [(200 * i, 1) for i in range(40)] + [(12000, 33), (64, 64)]])
+def test_few_chunk_rows(env, H_q, H_kv, D, rows):
+    """Few items over long contexts: their keys are cut into parts, joined by the part that ends last.  Rows whose last
+    part starts past their earlier tokens, rows too short to cut beside long ones, decodes beside them."""
+    torch = env[0]
+    a = Attn(env, rows, H_q, H_kv, D, seed=H_q + D + len(rows))
+    a.call()
+    a.check()
+    first = a.out.clone()
+    for cut in (0, 4096, 70000):  # less room for parts (80 KB at least with all of it); the same call again gives the same bits
+        b = a.ws[:a.ws.numel() - cut]
+        b.zero_()
+        a.call(ws=b)
+        if cut == 0:
+            assert torch.equal(a.out, first)
+        a.check()
+
+
 @pytest.mark.parametrize("H_q,H_kv,D,seed", [(8, 2, 128, 1), (4, 4, 64, 2), (8, 1, 64, 3), (32, 8, 128, 4)])
 def test_mixed_rows_with_pads(env, H_q, H_kv, D, seed):
     """Decodes, chunks and rows without tokens, in any order; tokens that no row covers stay as they were."""
