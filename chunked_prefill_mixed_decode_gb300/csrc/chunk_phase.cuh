@@ -36,10 +36,14 @@ struct ChItem {
   int kv0;      // CTA-global index of the item's first KV tile (stage and parity)
   int tok0[2], ntok[2], kv_end[2], nkt[2];  // per Q tile; ntok[1] == 0: no second tile
   int t0[2];    // per Q tile: index of its first KV tile among all tiles its softmax group ran
-  // Parts (4-bit pools): of how many this is which, and the place of the first.  c and kv_end then
-  // count from the part's first key, and n_kt and nkt are its own; ns == 1: the whole item.
-  int ns, part, item0;
-  int part_par[2];  // parity of this part among the group's
+};
+
+// Part of an item (4-bit pools): of how many it is which, the place of the first,
+// and the parity of this one among the parts of each softmax group.  The item's c
+// and kv_end then count from the part's first key, and n_kt and nkt are the part's
+// own; ns == 1: the whole item.
+struct ChPart {
+  int ns, part, item0, parity[2];
 };
 
 constexpr int kRawStages = 3;  // tiles of 4-bit pages on their way to the dequantizing warps
@@ -55,8 +59,9 @@ struct ChBars {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // 4-bit pools: pages as they are stored
   uint32_t tmem;
   int abort;
-  int last[2];
   ChItem items[2];
+  ChPart parts[2];
+  int last[2];
 };
 
 static_assert(sizeof(ChBars) <= 1024, "chunk-phase barrier block exceeds its reserved space");
@@ -221,14 +226,14 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
 // are asked for at once; a row to a warp waits for each row's records in turn (40 us instead of 7
 // for two parts of 128 rows).
 template <int D, int G>
-__device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& it, int t, int w, int lane) {
+__device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& it, const ChPart& pt, int t, int w, int lane) {
   constexpr int E = D / 16;  // 16-byte columns to a lane
-  const int rows = it.ntok[t] * G, ns = it.ns, q = lane & 3;
+  const int rows = it.ntok[t] * G, ns = pt.ns, q = lane & 3;
   const ChunkParts cp(p);
   for (int row0 = 8 * w; row0 < rows; row0 += 32) {
     const int row = row0 + (lane >> 2);
     const bool valid = row < rows;
-    const int64_t first = static_cast<int64_t>(it.item0) * p.ch_rec + t * 128 + (valid ? row : row0);
+    const int64_t first = static_cast<int64_t>(pt.item0) * p.ch_rec + t * 128 + (valid ? row : row0);
     float M = -FLT_MAX;
 #pragma unroll 8
     for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(cp.ml + first + static_cast<int64_t>(i) * p.ch_rec).x);
@@ -280,11 +285,13 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& i
 // (log2 units), sum and O as it is in TMEM into the part's records; the last part
 // of the item to get here joins them all.  False when a wait gave up.
 template <int D, int G>
-__device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, const ChItem& it, int t, float m, float l, uint32_t tO,
+__device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slot, int t, float m, float l, uint32_t tO,
                                       const volatile int* abort_flag, uint64_t lim) {
+  const ChItem& it = bars->items[slot];
+  const ChPart& pt = bars->parts[slot];
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, r = quad * 32 + lane;
   const bool valid = r / G < it.ntok[t];
-  const int64_t rec = static_cast<int64_t>(it.item0 + it.part) * p.ch_rec + t * 128 + r;
+  const int64_t rec = static_cast<int64_t>(pt.item0 + pt.part) * p.ch_rec + t * 128 + r;
   const ChunkParts cp(p);
   if (valid) cp.ml[rec] = make_float2(m, l);
   if (it.nkt[t] > 0) {
@@ -305,16 +312,16 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, const C
   __threadfence();  // this part's records are visible before it is counted
   mbar_arrive(&bars->part_done[t]);
   if (quad == 0) {
-    if (!warp_wait_fast(&bars->part_done[t], it.part_par[t], abort_flag, lim)) return false;
+    if (!warp_wait_fast(&bars->part_done[t], pt.parity[t], abort_flag, lim)) return false;
     if (lane == 0) {
-      bars->last[t] = atomicAdd(cp.cnt + 2 * it.item0 + t, 1) == it.ns - 1;
+      bars->last[t] = atomicAdd(cp.cnt + 2 * pt.item0 + t, 1) == pt.ns - 1;
       mbar_arrive(&bars->part_last[t]);
     }
   }
-  if (!warp_wait_fast(&bars->part_last[t], it.part_par[t], abort_flag, lim)) return false;
+  if (!warp_wait_fast(&bars->part_last[t], pt.parity[t], abort_flag, lim)) return false;
   if (bars->last[t]) {
     __threadfence();
-    merge_parts<D, G>(p, it, t, quad, lane);
+    merge_parts<D, G>(p, it, pt, t, quad, lane);
   }
   return true;
 }
@@ -489,6 +496,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         break;
       }
       ChItem it;
+      ChPart pt{};
       it.row = -1;
       if (item < n_items) {
         // (chunk row index and, above it, the part; KV head << 16 | pair from the last)
@@ -512,37 +520,42 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           it.ntok[t] = has ? min(TPT, d - qt * TPT) : 0;
           it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
           it.nkt[t] = (it.kv_end[t] + kKeys - 1) / kKeys;
+          if constexpr (!Q4) {
+            it.t0[t] = t_run[t];
+            t_run[t] += it.nkt[t];
+          }
           it.n_kt = max(it.n_kt, it.nkt[t]);
         }
         if constexpr (Q4) {
-          it.ns = 1;
+          pt.ns = 1;
           kt0 = 0;
           if (part_tiles > 0) {
             const int ns_row = chunk_parts(it.c, d, part_tiles), per = (it.n_kt + ns_row - 1) / ns_row;
-            it.ns = (it.n_kt + per - 1) / per;
-            it.part = kl.x >> 16;
-            it.item0 = item - it.part;
-            kt0 = it.part * per;
-            if (it.part >= it.ns) continue;  // an earlier pair of the row, with fewer tiles
+            pt.ns = (it.n_kt + per - 1) / per;
+            pt.part = kl.x >> 16;
+            pt.item0 = item - pt.part;
+            if (pt.part >= pt.ns) continue;  // an earlier pair of the row, with fewer tiles
+            kt0 = pt.part * per;
             it.c -= kt0 * kKeys;
             it.n_kt = 0;
             for (int t = 0; t < 2; ++t) {
               it.kv_end[t] -= kt0 * kKeys;
               it.nkt[t] = it.kv_end[t] > 0 ? min(per, (it.kv_end[t] + kKeys - 1) / kKeys) : 0;
               it.n_kt = max(it.n_kt, it.nkt[t]);
-              it.part_par[t] = parts_run[t] & 1;
-              parts_run[t] += it.ns > 1 && it.ntok[t] > 0;
+              pt.parity[t] = parts_run[t] & 1;
+              parts_run[t] += pt.ns > 1 && it.ntok[t] > 0;
             }
           }
-        }
-        for (int t = 0; t < 2; ++t) {
-          it.t0[t] = t_run[t];
-          t_run[t] += it.nkt[t];
+          for (int t = 0; t < 2; ++t) {
+            it.t0[t] = t_run[t];
+            t_run[t] += it.nkt[t];
+          }
         }
         it.kv0 = g;
       }
       if (lane == 0) {
         bars->items[slot] = it;
+        if constexpr (Q4) bars->parts[slot] = pt;
         mbar_arrive(&bars->item_full[slot]);
       }
       ++n_done;
@@ -934,8 +947,8 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           break;
         }
         tc_fence_after();
-        if (Q4 && it.ns > 1) {
-          ok = end_part<D, G>(p, bars, it, t, m_use, l, tO, abort_flag, lim);
+        if (Q4 && bars->parts[slot].ns > 1) {
+          ok = end_part<D, G>(p, bars, slot, t, m_use, l, tO, abort_flag, lim);
         } else {
           const float inv = (Q4 ? 4.f : 1.f) / l;
           const bool valid_row = Q4 ? r / G < it.ntok[t] : valid;  // read again: a register less in the loop
@@ -967,8 +980,8 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             }
           }
         }
-      } else if (Q4 && it.ns > 1 && it.ntok[t] > 0) {  // the part's keys come after all of the tile's tokens
-        ok = end_part<D, G>(p, bars, it, t, -FLT_MAX, 0.f, tO, abort_flag, lim);
+      } else if (Q4 && bars->parts[slot].ns > 1 && it.ntok[t] > 0) {  // the part's keys come after all of the tile's tokens
+        ok = end_part<D, G>(p, bars, slot, t, -FLT_MAX, 0.f, tO, abort_flag, lim);
       }
       if (Q4 && !ok) break;
       // O has been read: the next item's first PV may overwrite it
