@@ -475,6 +475,35 @@ def test_few_chunk_rows(env, H_q, H_kv, D, rows):
         a.check()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_chunk_rows_ragged_and_replayed(env, D):
+    """Parts over a ragged table, captured once and replayed as the rows' lengths change under it: cut, whole, cut."""
+    torch, ms, _ = env
+    H_q, H_kv = 8, 2
+    big = Attn(env, [(9000, 30), (5000, 100), (700, 1)], H_q, H_kv, D, seed=70 + D, ragged=True, slack_tokens=2)
+    big.call()
+    big.check()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        big.call()
+    first = big.out.clone()
+    for rows in ([(9000, 30), (5000, 100), (700, 1)], [(40, 30), (60, 70), (0, 0)], [(8000, 129), (0, 1), (0, 2)]):
+        rows_now = [(c, d) for c, d in rows]
+        cu = np.concatenate([[0], np.cumsum([d for _, d in rows_now])])
+        big.cu.copy_(_i32(torch, cu))
+        big.start.copy_(_i32(torch, [c for c, _ in rows_now]))
+        big.ctx.copy_(_i32(torch, [c + d for c, d in rows_now]))
+        big.out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert rows_now != [(9000, 30), (5000, 100), (700, 1)] or torch.equal(big.out, first)
+        a = Attn(env, rows_now, H_q, H_kv, D, pool=big.pool)
+        a.pages = [pg[:-(-(c + d) // 16)] for pg, (c, d) in zip(big.pages, rows_now)]
+        a.q, a.ws, a.out = big.q, big.ws, big.out
+        a.check()
+
+
 @pytest.mark.parametrize("H_q,H_kv,D,seed", [(8, 2, 128, 1), (4, 4, 64, 2), (8, 1, 64, 3), (32, 8, 128, 4)])
 def test_mixed_rows_with_pads(env, H_q, H_kv, D, seed):
     """Decodes, chunks and rows without tokens, in any order; tokens that no row covers stay as they were."""
