@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "device_state.cuh"
 #include "mixed_step.h"
 #include "ptx.cuh"
 
@@ -981,19 +982,7 @@ inline size_t parts_total(int64_t max_tokens, int64_t H_q, int64_t H_kv, int64_t
   return align_up(kPartItems * part_bytes(part_rows(max_tokens, H_q / H_kv), D), 256);
 }
 
-// Per-device host state (devices 0 .. kMaxDevices - 1): the SM count and which
-// kernels have had their shared-memory limit raised.  Safe to use from
-// several host threads: every entry is computed the same way by whoever gets
-// there first.
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_num_sms[kMaxDevices];
-std::atomic<uint32_t> g_smem_attr_set[kMaxDevices];
-
-inline int current_device() {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
-  return dev;
-}
 
 inline int num_sms() {
   const int dev = current_device();
@@ -1034,19 +1023,6 @@ inline int device_rates(float* sm_mhz, float* hbm_gbs, float* l2_bytes) {
   *sm_mhz = mhz;
   *hbm_gbs = gbs;
   *l2_bytes = l2;
-  return MS_OK;
-}
-
-// Raise `kernel`'s dynamic shared-memory limit on the current device once
-// (bit `slot` of the device's mask).
-template <typename Kernel>
-int ensure_smem_limit(Kernel kernel, int slot, int bytes) {
-  const int dev = current_device();
-  if (dev < 0) return MS_ERR_CUDA;
-  if (g_smem_attr_set[dev].load(std::memory_order_acquire) & (1u << slot)) return MS_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return MS_ERR_CUDA;
-  g_smem_attr_set[dev].fetch_or(1u << slot, std::memory_order_release);
   return MS_OK;
 }
 

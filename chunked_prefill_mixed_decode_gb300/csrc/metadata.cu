@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "device_state.cuh"
 #include "mixed_step.h"
 
 namespace {
@@ -24,6 +25,9 @@ constexpr int kPage = 16;
 constexpr int kMetaThreads = 512;
 constexpr int kMetaMaxRows = 8192;
 constexpr int kMetaMaxTokens = 1 << 21;
+
+// 32-bit words of dynamic shared memory for R rows
+constexpr int metadata_words(int R) { return 4 * (R + 1); }
 
 struct MetaArgs {
   const int32_t* cached;
@@ -312,10 +316,9 @@ extern "C" MS_API int ms_build_batch_metadata_device(
   MetaArgs a{cached_lens, new_tokens, page_tables, free_pages, free_count, free_state, cu_seqlens_q, q_start_pos,
              context_lens, positions, slot_mapping, block_tables, bt_offsets, bt_pages, info, dev_status,
              cap_pages, num_rows, table_stride, free_cap, num_pages, cap_tokens, bt_stride};
-  const int smem = 4 * (num_rows + 1) * 4;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(metadata_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MS_ERR_CUDA;
+  // 48 KB without a raised limit cover the kernel's static arrays too, so it is raised for every call
+  if (ensure_smem_limit(metadata_kernel, 0, metadata_words(kMetaMaxRows) * 4) != MS_OK) return MS_ERR_CUDA;
+  const int smem = metadata_words(num_rows) * 4;
   const int64_t most = table_n > cap_tokens ? table_n : cap_tokens;
   const int sms = ms_num_sms();
   if (sms <= 0) return MS_ERR_CUDA;

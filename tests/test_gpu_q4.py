@@ -843,3 +843,51 @@ def test_engine_rounds_over_a_4_bit_pool(env, H_q, H_kv, D, seed):
         a.check()
         finished += len(rec["finished"])
     assert finished >= 4
+
+
+# ---------------------------------------------------------------------------- the metadata call's shared memory
+
+_FRESH = """
+import sys, threading
+import torch
+import chunked_prefill_mixed_decode_gb300 as ms
+
+def one(R, rounds=1):
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    c, d, tab = i32(R) + 5, i32(R) + 1, torch.arange(R, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    cu, start, ctx, pos, slot, bt = i32(R + 1), i32(R), i32(R), i32(R), i32(R), i32(R, 1)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for _ in range(rounds):
+        ms.build_batch_metadata_device(c, d, tab, R, cu, start, ctx, pos, slot, block_tables=bt, stream=stream)
+    stream.synchronize()
+    assert torch.equal(cu, torch.arange(R + 1, dtype=torch.int32, device="cuda")), R
+    assert torch.equal(slot, 16 * tab[:, 0] + 5) and torch.equal(bt, tab), R
+
+def threads(counts, rounds):
+    failed = []
+    def work(R):
+        try:
+            one(R, rounds)
+        except BaseException as e:
+            failed.append((R, repr(e)))
+    ts = [threading.Thread(target=work, args=(R,)) for R in counts]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not failed, failed
+
+torch.zeros(1, device="cuda")
+"""
+
+
+@pytest.mark.parametrize("code", ["[one(R) for R in (3045, 3046, 3047, 3060, 3071, 3073, 8192)]", "one(3047)", "one(3071)",
+                                  "threads((3100, 8192, 4000, 5000), 400)"])
+def test_metadata_row_counts_in_a_fresh_process(env, code):
+    """Row counts around the 48 KB of shared memory that a kernel has without asking, static arrays included, before any
+    larger call of the process; and calls of different counts by several host threads at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FRESH + code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
