@@ -309,10 +309,19 @@ extern "C" MS_API int ms_build_batch_metadata_device(
   const Span out[] = {{cu_seqlens_q, R + 1}, {q_start_pos, R}, {context_lens, R}, {positions, cap_tokens},
                       {slot_mapping, cap_tokens}, {ragged ? bt_pages : block_tables, table_n}, {bt_offsets, R + 1},
                       {info, 4}};
-  for (const Span& x : in)
+  const Span status{dev_status, 1}, state{free_state, 2}, count{free_count, 1};
+  for (const Span& x : in) {
+    if (overlap(x, status) || overlap(x, state)) return MS_ERR_ARG;
     for (const Span& y : out)
       if (overlap(x, y)) return MS_ERR_ARG;
-  if (overlap(in[2], {free_state, 2}) || overlap(in[3], {free_state, 2}) || overlap(in[2], in[3])) return MS_ERR_ARG;
+  }
+  // the free count is an input (written, with free_state's first word, only after every CTA has read it),
+  // and the counter beside it lasts from call to call
+  for (const Span& y : out)
+    if (overlap(count, y) || overlap(state, y)) return MS_ERR_ARG;
+  if (overlap(in[2], in[3]) || overlap(in[2], count) || overlap(status, count) || overlap(status, state) ||
+      (alloc && free_count == free_state + 1))
+    return MS_ERR_ARG;
   MetaArgs a{cached_lens, new_tokens, page_tables, free_pages, free_count, free_state, cu_seqlens_q, q_start_pos,
              context_lens, positions, slot_mapping, block_tables, bt_offsets, bt_pages, info, dev_status,
              cap_pages, num_rows, table_stride, free_cap, num_pages, cap_tokens, bt_stride};

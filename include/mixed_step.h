@@ -493,7 +493,9 @@ MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, i
  * pages, or the free list too short).  A page id outside the pool gets slot
  * -1 and records MS_STATUS_BAD_PAGE.  Calls that share free_state must not
  * overlap on the GPU.  No output may overlap cached_lens, new_tokens,
- * page_tables or free_pages (the GPU reads them while it writes).
+ * page_tables or free_pages (the GPU reads them while it writes), nor
+ * free_count or free_state: free_count is an array of its own or free_state's
+ * word 0.
  * Errors: MS_ERR_ARG (also cap_tokens above 2^21, overlapping arrays),
  * MS_ERR_CUDA. */
 MS_API int ms_build_batch_metadata_device(

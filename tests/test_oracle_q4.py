@@ -224,3 +224,30 @@ def test_round_driver_refuses_graph_buckets_over_a_4_bit_pool(ms):
     pool = torch.zeros(4, 2, 1152, dtype=torch.uint8)
     with pytest.raises(ValueError, match="graph_buckets"):
         RoundDriver(ms.Engine(4, 8), pool, None, torch.zeros(8, 32), torch.zeros(8, 32), 4, 2, 64, graph_buckets=[8])
+
+
+def test_metadata_refuses_overlapping_counts_and_status(ms):
+    """The words of the free count and the status: written by one CTA while others read what lies under them."""
+    lib, R, ts, cap, fcap = ms.lib(), 5, 6, 40, 7
+    at = {n: (i + 1) << 20 for i, n in enumerate("c d tab free fc fs cu qs ctx pos slot bt off btp info st".split())}
+    sizes = dict(c=R, d=R, tab=R * ts, free=fcap, fs=2, cu=R + 1, qs=R, ctx=R, pos=cap, slot=cap, bt=R * 8, off=R + 1, btp=30,
+                 info=4, st=1)
+
+    def meta(ragged, **kw):
+        a = {**at, **kw}
+        return lib.ms_build_batch_metadata_device(
+            a["c"], a["d"], R, a["tab"], ts, a["free"], fcap, a["fc"], a["fs"], 50, cap, a["cu"], a["qs"], a["ctx"], a["pos"],
+            a["slot"], None if ragged else a["bt"], 0 if ragged else 8, a["off"] if ragged else None,
+            a["btp"] if ragged else None, 30 if ragged else 0, a["info"], a["st"], None)
+
+    for ragged in (False, True):
+        outs = ("cu", "qs", "ctx", "pos", "slot", "info") + (("off", "btp") if ragged else ("bt",))
+        for src in ("c", "d", "tab", "free"):  # an input under the free state or the status word
+            for to in (at[src], at[src] + 4 * (sizes[src] - 1)):
+                assert meta(ragged, fs=to) == ms.MS_ERR_ARG and meta(ragged, st=to) == ms.MS_ERR_ARG, src
+            assert meta(ragged, fs=at[src] - 4) == ms.MS_ERR_ARG, src
+        for dst in outs + ("tab",):  # the free count, and the library's word, in an array that the call writes
+            for to in (at[dst], at[dst] + 4 * (sizes[dst] - 1)):
+                assert meta(ragged, fc=to) == ms.MS_ERR_ARG and meta(ragged, fs=to) == ms.MS_ERR_ARG, dst
+        assert meta(ragged, fc=at["fs"] + 4) == ms.MS_ERR_ARG and meta(ragged, fc=at["st"]) == ms.MS_ERR_ARG
+        assert meta(ragged, fs=at["st"]) == ms.MS_ERR_ARG and meta(ragged, fs=at["st"] - 4) == ms.MS_ERR_ARG
