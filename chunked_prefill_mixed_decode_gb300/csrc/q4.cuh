@@ -95,10 +95,12 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w, int i) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// A pair of values, scale * code, from s2 = (s, s): any scale.
+// A pair of values, scale * code, from s2 = (s, s): any scale.  The product plus
+// zero: a scale of zero gives +0 whatever the codes (-8 in a row never written).
 __device__ __forceinline__ uint32_t q4_pair_times(uint32_t w, int i, uint32_t s2) {
-  const uint32_t r = q4_pair(w, i);
-  const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&s2));
+  const uint32_t r = q4_pair(w, i), zero = 0u;
+  const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&s2),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&zero));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 

@@ -891,3 +891,20 @@ def test_metadata_row_counts_in_a_fresh_process(env, code):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _FRESH + code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_read_of_no_row_is_bitwise_zero(env):
+    """Slot -1 and slots outside the pool read as +0, whatever the outputs held."""
+    torch, ms, _ = env
+    for D in (64, 128):
+        pool = _pool(torch, 2, 3, D, 80 + D)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        ko, vo = (torch.ones(5, 3, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ms.kv_read_q4(pool, _i32(torch, [-1, 7, 32, -9, 31]), ko, vo, dev_status=status)
+        assert ms.read_status(status) == ms.STATUS_BAD_SLOT
+        for x in (ko, vo):
+            bits = workloads.bf16_bits(x)
+            assert not bits[[0, 2, 3]].any() and bits[[1, 4]].any()
+        # and so do the rows of a pool of zeros
+        ms.kv_read_q4(torch.zeros_like(pool), _i32(torch, [0, 7, 31, 16, -1]), ko, vo)
+        assert not workloads.bf16_bits(ko).any() and not workloads.bf16_bits(vo).any()
