@@ -255,7 +255,8 @@ def measure_config(name, args, ms, world, rank, device, dist) -> dict:
         subs.append(dict(wl=wl, states=states, tables=tables, meta=meta, batch=batch, q=q, k=k, v=v,
                          q_rot=torch.empty_like(q), out=torch.empty_like(q), counts=counts))
     ws_bytes = max(ms.attention_workspace_size(max(s["meta"]["num_rows"], 1), max(s["meta"]["num_tokens"], 1),
-                                               s["batch"].context_total, wl0.H_q, wl0.H_kv, wl0.D) for s in subs)
+                                               s["batch"].context_total, wl0.H_q, wl0.H_kv, wl0.D, q4=False)
+                   for s in subs)
     ws = torch.zeros(ws_bytes, dtype=torch.uint8, device=device)
     status = torch.zeros(1, dtype=torch.int32, device=device)
     stream = torch.cuda.current_stream(device)

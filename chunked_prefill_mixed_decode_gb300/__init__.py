@@ -101,9 +101,9 @@ def lib() -> ctypes.CDLL:
     h.ms_kv_append_rope.argtypes = [_VP, _VP, _VP, _VP, _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int32, _VP, _VP,
                                     ctypes.c_int32, _VP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                     ctypes.c_int32, _VP, _VP]
-    h.ms_attention_workspace_size.restype = ctypes.c_size_t
-    h.ms_attention_workspace_size.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
-                                              ctypes.c_int32, ctypes.c_int32]
+    for size in (h.ms_attention_workspace_size, h.ms_attention_workspace_size_q4):
+        size.restype = ctypes.c_size_t
+        size.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
     h.ms_mixed_step_attention.restype = ctypes.c_int
     h.ms_mixed_step_attention.argtypes = [_VP, _VP, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP, ctypes.c_int32,
                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
@@ -484,9 +484,12 @@ def rope_table(max_pos: int, D: int, base: float = 10000.0):
 
 
 def attention_workspace_size(max_rows: int, max_tokens: int, max_context_total: int, H_q: int, H_kv: int,
-                             D: int) -> int:
-    return int(lib().ms_attention_workspace_size(int(max_rows), int(max_tokens), int(max_context_total), int(H_q),
-                                                 int(H_kv), int(D)))
+                             D: int, q4: bool = True) -> int:
+    """Workspace bytes for steps of these sizes, over a pool of either kind (ms_attention_workspace_size_q4).  With
+    ``q4=False`` for bf16 pools alone (ms_attention_workspace_size), up to 20 MB less; the 4-bit call takes such a
+    workspace too, and then leaves few long chunk items whole."""
+    size = lib().ms_attention_workspace_size_q4 if q4 else lib().ms_attention_workspace_size
+    return int(size(int(max_rows), int(max_tokens), int(max_context_total), int(H_q), int(H_kv), int(D)))
 
 
 def num_sms() -> int:

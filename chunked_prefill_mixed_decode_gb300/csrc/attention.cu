@@ -531,8 +531,7 @@ extern "C" MS_API size_t ms_attention_workspace_size(int32_t max_rows, int32_t m
   if (max_rows < 0 || max_tokens < 0 || max_context_total < 0 || H_q < 1 || H_kv < 1 || H_q % H_kv != 0 ||
       (D != 64 && D != 128))
     return 0;
-  return align_up(ws_layout(max_rows, max_tokens, max_context_total, H_q, H_kv, D).total, 256) +
-         parts_total(max_tokens, H_q, H_kv, D);
+  return ws_layout(max_rows, max_tokens, max_context_total, H_q, H_kv, D).total;
 }
 
 extern "C" MS_API int ms_cost_model_rates(float* sm_mhz, float* hbm_gbs) {

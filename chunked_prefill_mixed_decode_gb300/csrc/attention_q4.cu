@@ -535,6 +535,12 @@ int launch_q4(const AttnParams& p, const CUtensorMap& tq, cudaStream_t st) {
 
 }  // namespace
 
+extern "C" MS_API size_t ms_attention_workspace_size_q4(int32_t max_rows, int32_t max_tokens, int64_t max_context_total,
+                                                        int32_t H_q, int32_t H_kv, int32_t D) {
+  const size_t n = ms_attention_workspace_size(max_rows, max_tokens, max_context_total, H_q, H_kv, D);
+  return n == 0 ? 0 : align_up(n, 256) + parts_total(max_tokens, H_q, H_kv, D);
+}
+
 extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
                                                  const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
                                                  const int32_t* context_lens, const int32_t* block_tables,

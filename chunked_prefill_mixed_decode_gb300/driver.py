@@ -60,7 +60,7 @@ class RoundDriver:
             self.q_rot, self.out = self.graph.q_rot, self.graph.out
             return
         self.stager = MetaStager(max_rows, max(budget, 1), 64 * max_rows, self.device)  # grows on demand
-        ws = attention_workspace_size(max_rows, max(budget, 1), num_pages * 16, H_q, H_kv, D)
+        ws = attention_workspace_size(max_rows, max(budget, 1), num_pages * 16, H_q, H_kv, D, q4=self.q4)
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.q_rot = torch.empty((max(budget, 1), H_q, D), dtype=torch.bfloat16, device=self.device)

@@ -145,10 +145,12 @@ def rope_tables_device(max_pos: int, D: int, device, base: float = 10000.0):
     return torch.from_numpy(cos).to(device), torch.from_numpy(sin).to(device)
 
 
-def workspace_for(batch: DeviceBatch, H_q: int, H_kv: int, D: int, device):
+def workspace_for(batch: DeviceBatch, H_q: int, H_kv: int, D: int, device, q4: bool = False):
+    """A zeroed workspace for the attention of this batch; ``q4``: with the room that a step over a 4-bit pool uses to
+    cut few long chunk items into parts (it runs without, on whole items)."""
     import torch
     n = attention_workspace_size(max(batch.num_rows, 1), max(batch.num_tokens, 1), batch.context_total, H_q, H_kv,
-                                 D)
+                                 D, q4=q4)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 

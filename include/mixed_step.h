@@ -227,9 +227,7 @@ MS_API int ms_kv_append_rope(const void* q, const void* k, const void* v,
  * the status word, then queue counters and the step's plan (word 9: how many
  * CTAs started on chunk work) and, kept across calls, word 10: the SM clock
  * in MHz the last call measured, which the next call's SM-split cost model
- * uses.  For steps of more than one token the last part, up to 20 MB, is room
- * for ms_mixed_step_attention_q4 to cut few long chunk items into parts; no
- * other call uses it.  Zero the whole workspace once before its first use. */
+ * uses.  Zero the whole workspace once before its first use. */
 MS_API size_t ms_attention_workspace_size(int32_t max_rows, int32_t max_tokens, int64_t max_context_total,
                                           int32_t H_q, int32_t H_kv, int32_t D);
 
@@ -316,10 +314,10 @@ MS_API int ms_mixed_step(const void* q, const void* k, const void* v, const int3
  * code on a per-step path should not call cudaMalloc (it may synchronise the
  * device and stall other streams).  This call allocates nothing: no
  * cudaMalloc, cudaFree or allocating library routine.  It works out of a
- * scratch array the library owns, 64 MiB per device (the step's workspace,
- * ms_attention_workspace_size(num_rows, num_tokens, context_total, H_q, H_kv,
- * D) without the last part, must not exceed it -- else MS_ERR_SCRATCH and
- * nothing is enqueued).  The array is device memory that every GPU which loads this
+ * scratch array the library owns, 64 MiB per device (the step's workspace
+ * size, ms_attention_workspace_size(num_rows, num_tokens, context_total, H_q,
+ * H_kv, D), must not exceed it -- else MS_ERR_SCRATCH and nothing is
+ * enqueued).  The array is device memory that every GPU which loads this
  * library holds until the process exits.
  *
  * The first call on a device looks up the array's device address (once per
@@ -437,12 +435,21 @@ MS_API int ms_kv_read_q4(const void* kv_cache, int32_t num_pages, const int32_t*
                          void* k_out, void* v_out, int32_t H_kv, int32_t D, int32_t page_size,
                          int32_t* dev_status, ms_stream_t stream);
 
+/* ms_attention_workspace_size_q4 -- ms_attention_workspace_size plus, for
+ * steps of more than one token, up to 20 MB (D = 128) in which
+ * ms_mixed_step_attention_q4 cuts few long chunk items into parts that run at
+ * once. */
+MS_API size_t ms_attention_workspace_size_q4(int32_t max_rows, int32_t max_tokens, int64_t max_context_total,
+                                             int32_t H_q, int32_t H_kv, int32_t D);
+
 /* ms_mixed_step_attention_q4 -- the attention of ms_mixed_step_attention
  * (block_tables padded with bt_stride, bt_offsets == NULL) or of
  * ms_mixed_step_attention_ragged (block_tables = bt_pages with bt_len entries,
  * bt_offsets given) over a 4-bit cache: the same rows, causal bounds, pad
- * rows, workspace (ms_attention_workspace_size), status bits, limits and
- * errors, with K[j] and V[j] the values that the cache holds.  Scores and
+ * rows, status bits, limits and errors, with K[j] and V[j] the values that the
+ * cache holds.  A workspace of ms_attention_workspace_size bytes will do; with
+ * one of ms_attention_workspace_size_q4 bytes chunk rows that make few work
+ * items over long contexts take a fraction of the time.  Scores and
  * softmax statistics in fp32; the weights of V are rounded to bf16 before
  * their products, as in the bf16 call.  A decode row's intermediate sums reach
  * 20 times the score's terms: sum |q| max |K| has to stay below 2^123.

@@ -251,3 +251,26 @@ def test_metadata_refuses_overlapping_counts_and_status(ms):
                 assert meta(ragged, fc=to) == ms.MS_ERR_ARG and meta(ragged, fs=to) == ms.MS_ERR_ARG, dst
         assert meta(ragged, fc=at["fs"] + 4) == ms.MS_ERR_ARG and meta(ragged, fc=at["st"]) == ms.MS_ERR_ARG
         assert meta(ragged, fs=at["st"]) == ms.MS_ERR_ARG and meta(ragged, fs=at["st"] - 4) == ms.MS_ERR_ARG
+
+
+def test_workspace_sizes(ms):
+    """Only the 4-bit query has the room for chunk items in parts: at D = 64 and G = 1 (256 rows of 264 bytes and 16 a
+    part, 152 parts) 10.3 MB, at 128 20.2 MB, less for steps of few tokens and none for one token; the bf16 steps'
+    own size is that of their layout."""
+    def extra(*a):
+        return ms.attention_workspace_size(*a) - ms.attention_workspace_size(*a, q4=False)
+    assert 0 <= extra(7, 5000, 90000, 8, 8, 64) - 152 * (16 + 256 * 264) < 512
+    assert 0 <= extra(7, 5000, 90000, 32, 8, 128) - 152 * (16 + 256 * 520) < 512
+    assert 0 <= extra(7, 3, 90000, 32, 8, 128) - 152 * (16 + 12 * 520) < 512
+    assert extra(7, 1, 90000, 32, 8, 128) < 256 and extra(0, 0, 0, 4, 4, 64) < 256
+    assert ms.attention_workspace_size(1, 1, 0, 4, 2, 96) == 0 and ms.attention_workspace_size(1, 2, 0, 4, 3, 64) == 0
+    # the layout of a 65-row step of 512 tokens over 262144 keys, 32 heads of 128: header, tables, items, and for each
+    # of the 512 + 130 splits and heads a record of (max, sum) and 128 sums
+    n = ms.attention_workspace_size(65, 512, 262144, 32, 32, 128, q4=False)
+    records = 32 * (512 + 130) * (8 + 128 * 4)
+    assert records < n < records + (1 << 20)
+    # a replayed graph is one over bf16 pools
+    import ctypes
+    arr = (ctypes.c_int32 * 2)(8, 512)
+    cfg = ms.GraphConfig(32, 32, 128, 16384, 65, 300, 4096, 0.1, 2, arr)
+    assert n <= ms.lib().ms_graph_workspace_size(ctypes.byref(cfg)) < n + (1 << 20)
