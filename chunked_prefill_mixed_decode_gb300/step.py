@@ -34,7 +34,7 @@ class DeviceBatch:
     num_tokens: int
     num_decodes: int
     context_total: int
-    host: dict
+    host: dict  # the metadata's host arrays (empty for a batch built on the GPU)
     bt_offsets: object = None  # ragged block table (then block_tables holds the pages back to back)
 
     @property
@@ -43,7 +43,7 @@ class DeviceBatch:
 
     @property
     def h2d_bytes(self) -> int:
-        return sum(int(np.asarray(self.host[k]).nbytes) for k in _keys(self.host))
+        return sum(int(np.asarray(self.host[k]).nbytes) for k in _keys(self.host) if k in self.host)
 
 
 def to_device(meta: dict, device, non_blocking: bool = False) -> DeviceBatch:

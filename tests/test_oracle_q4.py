@@ -274,3 +274,13 @@ def test_workspace_sizes(ms):
     arr = (ctypes.c_int32 * 2)(8, 512)
     cfg = ms.GraphConfig(32, 32, 128, 16384, 65, 300, 4096, 0.1, 2, arr)
     assert n <= ms.lib().ms_graph_workspace_size(ctypes.byref(cfg)) < n + (1 << 20)
+
+
+def test_batch_from_tables_has_no_host_copy(ms):
+    """A batch built on the GPU copies no metadata: 0 bytes from the host; one from the host counts its arrays."""
+    torch = pytest.importorskip("torch")
+    from chunked_prefill_mixed_decode_gb300 import step
+    tables = step.StepTables(torch.zeros(3, 4, dtype=torch.int32), 12, 8)
+    assert tables.batch.h2d_bytes == 0 and not tables.batch.ragged
+    meta = ms.build_batch_metadata([(5, 0), (0, 3)], [np.array([0]), np.array([1])], 8)
+    assert step.to_device(meta, "cpu").h2d_bytes == 4 * (3 + 2 + 2 + 4 + 4 + 2)
