@@ -288,7 +288,9 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
       }
       --in_flight;
       next_stage();
-      // O^T += V^T (P s)^T, page by page and group by group
+      // O^T += V^T (P s)^T, page by page and group by group.  The weights p s are rounded to bf16, the operands'
+      // type (2^-9 of each, independent from key to key); the sum l is of the unrounded p.  They stay finite while
+      // V's scales are below 2^119, as they are wherever keys * max |V| < 2^120 keeps the sums finite (p <= 2^8).
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h >= n_half) break;

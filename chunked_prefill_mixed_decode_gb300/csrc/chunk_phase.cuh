@@ -908,7 +908,8 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           }
           l = l * alpha + ((rsa[0].x + rsa[0].y) + (rsa[1].x + rsa[1].y));
           m_use = m_new;
-          // P (bf16 pairs) over the first 32 columns of the S values it came from.
+          // P (bf16 pairs, the operands' type: 2^-9 of each; l is the sum from before) over
+          // the first 32 columns of the S values it came from.
           // Packing before the rescale keeps 32 registers live through it instead of
           // 64, and the store runs while O is rescaled.
           uint32_t pw[32];

@@ -450,9 +450,14 @@ MS_API size_t ms_attention_workspace_size_q4(int32_t max_rows, int32_t max_token
  * cache holds.  A workspace of ms_attention_workspace_size bytes will do; with
  * one of ms_attention_workspace_size_q4 bytes chunk rows that make few work
  * items over long contexts take a fraction of the time.  Scores and
- * softmax statistics in fp32; the weights of V are rounded to bf16 before
- * their products, as in the bf16 call.  A decode row's intermediate sums reach
- * 20 times the score's terms: sum |q| max |K| has to stay below 2^123.
+ * softmax statistics in fp32; the weights of V (in decode rows, times V's
+ * scales) are rounded to bf16 before their products, as in the bf16 call, the
+ * softmax's sum is taken before that rounding.  A weight reaches 2^8 before its
+ * row's reference maximum is raised, so a row's keys times max |V| have to stay
+ * below 2^120.  A decode row's products carry code + 128 in place of the code:
+ * its scores round as sums about 20 times as large, to about
+ * 2^-22 * 136 * scale * sum |q| s (s: the scale of the element's group), and
+ * sum |q| max |K| has to stay below 2^123.
  *   kv_cache  device, the 4-bit pool of num_pages pages, 16-byte aligned
  * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
 MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,

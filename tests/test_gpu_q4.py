@@ -908,3 +908,107 @@ def test_read_of_no_row_is_bitwise_zero(env):
         # and so do the rows of a pool of zeros
         ms.kv_read_q4(torch.zeros_like(pool), _i32(torch, [0, 7, 31, 16, -1]), ko, vo)
         assert not workloads.bf16_bits(ko).any() and not workloads.bf16_bits(vo).any()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64), (8, 1, 64)])
+def test_largest_sums_of_values(env, H_q, H_kv, D):
+    """Values just below the documented bound, keys * max |V| < 2^120, with weights that rise by 2^7.9 over the row, as
+    far as they may before the reference maximum follows: every sum stays finite, whatever keys a warp or tile starts
+    with.  4096 keys of |V| = 7 * 2^105: 2^119.8."""
+    torch, ms, _ = env
+    NG = D // 32
+    for rows in ([(4095, 1)], [(4000, 96)], [(4095, 1), (3990, 100), (64, 1), (1000, 40)]):
+        a = Attn(env, rows, H_q, H_kv, D, seed=90, pool=_pool(torch, 2 + sum(-(-(c + d) // 16) for c, d in rows), H_kv, D, 90))
+        for pages in a.pages:
+            for j, pg in enumerate(pages):
+                blk = a.pool[int(pg)]
+                blk[:, :8 * D] = 0x88 if j % 16 < 4 else 0xCC  # K: code 0 in the first 64 keys of every 256, else 4
+                blk[:, 8 * D:16 * D] = 0xFF  # V: code 7, in every other head -7
+                blk[1::2, 8 * D:16 * D] = 0x11
+                sc = torch.tensor([0.125] * 16 * NG + [2.0 ** 105] * 16 * NG, device="cuda").to(torch.bfloat16)
+                blk[:, 16 * D:] = sc.view(torch.uint8)
+        a.q.fill_(1.0)
+        scale = 7.9 * float(np.log(2)) / (0.5 * D)
+        a.call(scale=scale)
+        a.check(scale=scale)
+
+
+def _score_slack(a, s, scale):
+    """Bounds e[h, g, t, n] on the error of row s's scores, from each one's own products.
+
+    A tensor-core product adds 16 exact terms to its fp32 accumulator, all 17 cut to 24 bits of the largest: 17 steps of
+    2^-23 of the largest magnitude M among them.  Chunk rows: D / 16 such products of q with K (quarters of it, a factor
+    that changes nothing).  Decode rows: two products a group, of q with 128 + nibble, one over the scales times -136
+    sum q (in three bf16 parts, exact), a multiply-add a group.  Either kind: the factor scale * log2 e and the
+    exponent's multiply-add, 2^-22 of the score.
+    """
+    torch, D, H_kv = a.torch, a.D, a.H_kv
+    G, NG = a.H_q // H_kv, D // 32
+    c, d = a.rows[s]
+    n = c + d
+    pool = a.pool[torch.tensor(np.asarray(a.pages[s]), device="cuda")]
+    K = _values(torch, pool, D)[0].permute(1, 0, 2, 3).reshape(H_kv, -1, D)[:, :n]
+    q = a.q[a.cun[s]:a.cun[s + 1]].double().view(d, H_kv, G, D).permute(1, 2, 0, 3)
+    z = torch.einsum("hgtd,hnd->hgtn", q, K)
+    unit = 17 * 2.0 ** -23
+
+    def step_error(q_, k_):  # q [h, g, t, 16 m], k [h, n, 16 m]: m products in a row onto one accumulator
+        e = acc = 0.0
+        top = torch.maximum(q_.abs().amax(-1)[..., None] * k_.abs().amax(-1)[:, None, None], torch.zeros_like(z))
+        for i in range(q_.shape[-1] // 16):
+            acc = acc + torch.einsum("hgtd,hnd->hgtn", q_[..., 16 * i:16 * i + 16], k_[..., 16 * i:16 * i + 16])
+            e = e + unit * torch.maximum(acc.abs(), top)
+        return e
+
+    if d > 1:
+        e = step_error(q, K)
+    else:
+        sc = pool[..., 16 * D:16 * D + 32 * NG].contiguous().view(torch.bfloat16).double()
+        sc = sc.view(*pool.shape[:2], 16, NG).permute(1, 0, 2, 3).reshape(H_kv, -1, NG)[:, :n]  # [h, n, group]
+        # elements 0 to 3 of each quarter of a group go into its first product, 4 to 7 into its second
+        order = [8 * t + i + 4 * half for half in (0, 1) for t in range(4) for i in range(4)]
+        off = [-136.0 * q[..., 32 * g:32 * g + 32].sum(-1) for g in range(NG)]
+        run = sum(off[g][..., None] * sc[:, None, None, :, g] for g in range(NG))
+        biggest = torch.stack([off[g].abs()[..., None] * sc[:, None, None, :, g] for g in range(NG)]).amax(0)
+        e = unit * torch.maximum(run.abs(), biggest)
+        for g in range(NG):
+            cols = [32 * g + i for i in order]
+            nib = K[..., cols] / sc[..., g:g + 1] + 136.0
+            s_g = sc[:, None, None, :, g]
+            term = s_g * torch.einsum("hgtd,hnd->hgtn", q[..., cols], nib)
+            run = run + term
+            e = e + s_g * step_error(q[..., cols], nib) + 2.0 ** -24 * run.abs()
+        assert (run - z).abs().max() <= 1e-9 * biggest.max()  # the same score
+    return scale * (e + 2.0 ** -22 * z.abs())
+
+
+@pytest.mark.parametrize("qscale", [4.0, 30.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_sharp_scores_row_by_row(env, D, qscale):
+    """Scores up to the hundreds, each row within the bound that its own scores' errors e give: with eta = e^e - 1 a
+    weight is off by a factor 1 +- eta, the output by (sum p eta |v| + |o| sum p eta) / (1 - sum p eta), and by the
+    roundings of every test here."""
+    torch, ms, _ = env
+    rows = [(900, 1), (5, 1), (300, 140), (0, 20), (37, 1), (2000, 1), (1500, 3)]
+    a = Attn(env, rows, 8, 2, D, seed=95 + D, qscale=qscale)
+    a.call()
+    assert ms.read_status(a.ws) == 0
+    ref, A = a.reference()
+    scale, G = D ** -0.5, 4
+    for s, (c, d) in enumerate(rows):
+        pg = torch.tensor(np.asarray(a.pages[s]), device="cuda")
+        K, V = (x.permute(1, 0, 2, 3).reshape(2, -1, D)[:, :c + d] for x in _values(torch, a.pool[pg], D))
+        q = a.q[a.cun[s]:a.cun[s + 1]].double().view(d, 2, G, D).permute(1, 2, 0, 3)
+        z = torch.einsum("hgtd,hnd->hgtn", q, K) * scale
+        seen = torch.arange(c + d, device="cuda")[None] <= c + torch.arange(d, device="cuda")[:, None]
+        p = torch.softmax(z.masked_fill(~seen, -float("inf")), -1)
+        w = p * torch.expm1(_score_slack(a, s, scale))
+        X = w.sum(-1).permute(2, 0, 1).reshape(d, 8, 1)
+        assert X.max() < (0.003 if d > 1 else 0.04)  # what the scores' errors can add is a few parts in a thousand, or hundred
+        cut = slice(int(a.cun[s]), int(a.cun[s + 1]))
+        o, sums = ref[cut].abs(), A[cut]
+        e = (torch.einsum("hgtn,hnd->thgd", w, V.abs()).reshape(d, 8, D) + o * X) / (1 - X)
+        # weights below 2^-126 of the largest are lost: 2001 of them at most, times |v| <= 8 * 0.45 * 2^-126, under 1e-30
+        bound = 2.0 ** -8 * o + (2.0 ** -8 + 2.0 ** -10) * sums + 1.01 * e + 1e-30
+        err = (a.out[cut].double() - ref[cut]).abs()
+        assert (err <= bound).all(), (s, (err / bound).max())
