@@ -1012,3 +1012,62 @@ def test_sharp_scores_row_by_row(env, D, qscale):
         bound = 2.0 ** -8 * o + (2.0 ** -8 + 2.0 ** -10) * sums + 1.01 * e + 1e-30
         err = (a.out[cut].double() - ref[cut]).abs()
         assert (err <= bound).all(), (s, (err / bound).max())
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(4, 2, 64), (8, 1, 64), (2, 2, 128), (8, 2, 128), (8, 1, 128)])
+def test_which_chunk_items_are_cut(env, H_q, H_kv, D):
+    """Items of one pair of query tiles over 142 tiles of keys and more, alone and beside 40 decodes, run in parts
+    (workspace header: word 12 the tiles to a part, word 6 the items); rows of 10 tiles and of many items run whole, and
+    so does everything on a workspace without the room, with the same result within the bounds."""
+    torch, ms, _ = env
+
+    def plan(ws):
+        return ws[:256].view(torch.int32)[[12, 6]].tolist()
+
+    for rows, cut in (([(9001, 40 // (H_q // H_kv))], True), ([(200 * i, 1) for i in range(40)] + [(12000, 32 // (H_q // H_kv))], True),
+                      ([(511, 2), (512, 2), (575, 65)], False), ([(5000, 1500)] * 12, False)):
+        a = Attn(env, rows, H_q, H_kv, D, seed=100 + len(rows))
+        a.call()
+        tiles, items = plan(a.ws)
+        a.check()
+        if cut:
+            n_kt = -(-(rows[-1][0] + rows[-1][1]) // 64)
+            assert 8 <= tiles < n_kt and items == H_kv * -(-n_kt // tiles) and items > H_kv
+        else:
+            assert tiles == 0
+        bare = torch.zeros(ms.attention_workspace_size(len(rows), a.T, a.total, H_q, H_kv, D, q4=False), dtype=torch.uint8,
+                           device="cuda")
+        a.out.fill_(5.0)
+        a.call(ws=bare)
+        assert plan(bare)[0] == 0 and ms.read_status(bare) == 0
+        a.check()
+        # 256 bytes more are less than one part needs
+        a.call(ws=torch.cat([bare.zero_(), torch.zeros(256, dtype=torch.uint8, device="cuda")]))
+        a.check()
+
+
+def test_rotation_in_place(env):
+    """The append and a whole step with q_rot left out: q holds the rotated values afterwards, bit for bit the others."""
+    torch, ms, step = env
+    for H_q, H_kv, D, T in ((8, 2, 128, 37), (4, 4, 64, 300), (3, 1, 64, 5)):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        q, k, v = (torch.randn(T, H, D, generator=g, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+        pages = -(-T // 16)
+        slots, positions = _i32(torch, np.arange(T)), _i32(torch, np.arange(T))
+        cos, sin = step.rope_tables_device(T, D, "cuda")
+        pools = [step.kv_pool_q4(pages, H_kv, D, "cuda") for _ in range(3)]
+        q_rot = torch.empty_like(q)
+        ms.kv_append_rope_q4(q, k, v, positions, slots, cos, sin, pools[0], q_rot=q_rot)
+        mine = q.clone()
+        ms.kv_append_rope_q4(mine, k, v, positions, slots, cos, sin, pools[1])
+        assert torch.equal(mine, q_rot) and torch.equal(pools[1], pools[0])
+        cu, start, ctx = _i32(torch, [0, T]), _i32(torch, [0]), _i32(torch, [T])
+        b = step.DeviceBatch(cu, start, ctx, positions, slots, _i32(torch, [list(range(pages))]), 1, T, 0, T, {})
+        ws = step.workspace_for(b, H_q, H_kv, D, "cuda", q4=True)
+        out, want = torch.zeros_like(q), torch.zeros_like(q)
+        if H_q // H_kv in (1, 2, 4, 8):
+            mine = q.clone()
+            assert step.run_step_q4(mine, k, v, b, cos, sin, pools[2], out, ws) is mine
+            ms.mixed_step_attention_q4(q_rot, pools[0], cu, start, ctx, b.block_tables, T, want, ws)
+            assert torch.equal(mine, q_rot) and torch.equal(pools[2], pools[0]) and torch.equal(out, want)
+            assert ms.read_status(ws) == 0
