@@ -558,10 +558,11 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         if constexpr (Q4) bars->parts[slot] = pt;
         mbar_arrive(&bars->item_full[slot]);
       }
-      ++n_done;
       if (it.row < 0) break;
+      ++n_done;
       // Q tiles: the previous item's S MMAs must be done with them
       if (n_done >= 2 && !lane0_wait(&bars->q_empty, (n_done - 2) & 1)) {
+        --n_done;  // its Q tiles have not been asked for
         ok = false;
         break;
       }
@@ -638,6 +639,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     if (lane == 0) {
       if (!ok && !stalled) *abort_flag = 1;
       // copies still in flight must land before the CTA moves on
+      if (n_done > 0) mbar_wait(&bars->q_full, (n_done - 1) & 1, nullptr, 200000000ull);
       if constexpr (Q4) {
         for (int t = (g > kRawStages ? g - kRawStages : 0); t < g; ++t)
           mbar_wait(&bars->raw_full[t % kRawStages], (t / kRawStages) & 1, nullptr, 200000000ull);
