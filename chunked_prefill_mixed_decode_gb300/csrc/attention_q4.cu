@@ -507,8 +507,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __gri
       __syncthreads();
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
       const bool aborted = bars->abort != 0;
-      if (threadIdx.x == 0)
-        for (uint64_t* b = &bars->q_full; b <= &bars->raw_empty[kRawStages - 1]; ++b) mbar_inval(b);
+      if (threadIdx.x == 0) close_chunk_barriers(bars, &bars->raw_empty[kRawStages - 1]);
       __syncthreads();
       if (aborted) break;
     }

@@ -59,6 +59,7 @@ struct ChBars {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // 4-bit pools: pages as they are stored
   uint32_t tmem;
   int abort;
+  int q_asked;  // items whose Q tiles have been asked for
   ChItem items[2];
   ChPart parts[2];
   int last[2];
@@ -68,6 +69,16 @@ static_assert(sizeof(ChBars) <= 1024, "chunk-phase barrier block exceeds its res
 static_assert(ChCfg<128>::SMEM <= 232448 && ChCfg<64>::SMEM <= 232448,
               "chunk phase exceeds the per-CTA shared-memory limit");
 static_assert(ChCfg<128>::KVS <= 8 && ChCfg<64>::KVS <= 8, "more K/V stages than barriers");
+
+// By one thread once every warp has left the phase: Q tiles that a phase given up
+// early still has in flight land, and its barriers, up to `last`, are invalidated.
+// (Here and not at the producer's end, where the loops of the phase pay for it in
+// registers: 516 -> 519.6 us, two chunks of 3968 tokens over 4-bit pages.)
+__device__ __forceinline__ void close_chunk_barriers(ChBars* bars, uint64_t* last) {
+  const int n_q = bars->q_asked;
+  if (n_q > 0) mbar_wait(&bars->q_full, (n_q - 1) & 1, nullptr, 200000000ull);
+  for (uint64_t* b = &bars->q_full; b <= last; ++b) mbar_inval(b);
+}
 
 // wait by lane 0, result and ordering shared with the whole warp
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
@@ -411,6 +422,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         mbar_init(&bars->part_last[t], 1);
       }
     bars->abort = 0;
+    bars->q_asked = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -558,16 +570,18 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         if constexpr (Q4) bars->parts[slot] = pt;
         mbar_arrive(&bars->item_full[slot]);
       }
-      if (it.row < 0) break;
       ++n_done;
+      if (it.row < 0) break;
       // Q tiles: the previous item's S MMAs must be done with them
       if (n_done >= 2 && !lane0_wait(&bars->q_empty, (n_done - 2) & 1)) {
-        --n_done;  // its Q tiles have not been asked for
         ok = false;
         break;
       }
       const int nq = it.ntok[1] > 0 ? 2 : 1;
-      if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
+        bars->q_asked = n_done;
+      }
       __syncwarp();
       if (lane < nq * NSL) {
         const int t = lane / NSL, s = lane % NSL;
@@ -638,8 +652,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     }
     if (lane == 0) {
       if (!ok && !stalled) *abort_flag = 1;
-      // copies still in flight must land before the CTA moves on
-      if (n_done > 0) mbar_wait(&bars->q_full, (n_done - 1) & 1, nullptr, 200000000ull);
+      // copies still in flight must land before the CTA moves on (Q's: close_chunk_barriers)
       if constexpr (Q4) {
         for (int t = (g > kRawStages ? g - kRawStages : 0); t < g; ++t)
           mbar_wait(&bars->raw_full[t % kRawStages], (t / kRawStages) & 1, nullptr, 200000000ull);
