@@ -174,6 +174,10 @@ def lib() -> ctypes.CDLL:
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                             ctypes.c_float, _VP, _VP, ctypes.c_size_t, _VP]),
+            ("ms_test_attention_stall_q4", [_VP, _VP, ctypes.c_int32, _VP, _VP, _VP, _VP, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _VP, _VP,
+                                            ctypes.c_size_t, ctypes.c_int64, _VP]),
             ("ms_build_batch_metadata_device", [_VP, _VP, ctypes.c_int32, _VP, ctypes.c_int32, _VP, ctypes.c_int32,
                                                 _VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP,
                                                 _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int64, _VP, _VP, _VP])):
@@ -837,6 +841,22 @@ def mixed_step_attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_
                             stream=None) -> None:
     """Causal attention of every packed row over its pages of a 4-bit pool (ms_mixed_step_attention_q4).
     ``block_tables`` is the padded [rows, stride] table, or, with ``bt_offsets`` given, the ragged page list."""
+    _attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, context_total, out, workspace,
+                  bt_offsets, scale, stream)
+
+
+def test_attention_stall_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables,
+                            context_total: int, out, workspace, wait_limit_ns: int, scale: float = None,
+                            stream=None) -> None:
+    """test_attention_stall over a 4-bit pool (ms_test_attention_stall_q4): no work item is published and no copy
+    issued; the chunk phase's waits give up after ``wait_limit_ns``, the decode rows' after 2 s.  Not for production
+    use."""
+    _attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, context_total, out, workspace,
+                  None, scale, stream, int(wait_limit_ns))
+
+
+def _attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, context_total, out, workspace,
+                  bt_offsets, scale, stream, stall_limit_ns=None) -> None:
     import torch
     if q_rot.dim() != 3:
         raise ValueError(f"q_rot must be [T, H_q, D], got {tuple(q_rot.shape)}")
@@ -863,6 +883,14 @@ def mixed_step_attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_
                     q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out, workspace)
     if scale is None:
         scale = float(D) ** -0.5
+    if stall_limit_ns is not None:
+        rc = lib().ms_test_attention_stall_q4(q_rot.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+                                              cu_seqlens_q.data_ptr(), q_start_pos.data_ptr(), context_lens.data_ptr(),
+                                              block_tables.data_ptr(), stride, S, T, int(context_total), H_q, H_kv, D,
+                                              PAGE_SIZE, float(scale), out.data_ptr(), workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size(), stall_limit_ns, st)
+        _check(rc, "ms_test_attention_stall_q4")
+        return
     rc = lib().ms_mixed_step_attention_q4(q_rot.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
                                           cu_seqlens_q.data_ptr(), q_start_pos.data_ptr(), context_lens.data_ptr(),
                                           block_tables.data_ptr(), _ptr(bt_offsets), bt_len, stride, S, T,

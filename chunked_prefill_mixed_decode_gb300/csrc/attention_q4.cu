@@ -206,7 +206,7 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
       __syncwarp();  // every lane is done with the stage before
       issue_pair(st == 0 ? NST - 1 : st - 1);
       // a lane whose wait gave up goes on within the stage's bounds to the vote below
-      const bool late = !mbar_wait(full + st, ph, nullptr);
+      const bool late = !mbar_wait(full + st, ph, nullptr);  // 2 s: a limit from the parameters costs registers
       const uint32_t stage = ring + st * C::STAGE;
       const int n_half = pi + 1 < np ? 2 : 1;
       // S^T: lane holds (row ra, heads 2 tq, 2 tq + 1) and (row ra + 8, same heads) of each page
@@ -387,7 +387,7 @@ __device__ __forceinline__ void decode_phase_q4(const AttnParams& p, uint8_t* ds
       const int np = split->np, hk = split->hk;
       const int share = 2 * ((np + 2 * T - 1) / (2 * T));  // pages to a warp, in pairs
       const int w0 = tw * share, mine = max(0, min(share, np - w0));
-      iss.left = mine;
+      iss.left = p.test_stall != 0 ? 0 : mine;  // test hook: no copy is issued, and the wait for it gives up
       iss.next = 0;
       iss.base = p.kv_q4 + hk * Q::BYTES;
       iss.btr = row_table(p, split->row) + split->p0 + w0;
@@ -542,19 +542,20 @@ extern "C" MS_API size_t ms_attention_workspace_size_q4(int32_t max_rows, int32_
   return n == 0 ? 0 : align_up(n, 256) + parts_total(max_tokens, H_q, H_kv, D);
 }
 
-extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
-                                                 const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
-                                                 const int32_t* context_lens, const int32_t* block_tables,
-                                                 const int32_t* bt_offsets, int64_t bt_len, int32_t bt_stride,
-                                                 int32_t num_rows, int32_t num_tokens, int64_t context_total, int32_t H_q,
-                                                 int32_t H_kv, int32_t D, int32_t page_size, float scale, void* out,
-                                                 void* workspace, size_t ws_bytes, ms_stream_t stream) {
+namespace {
+
+// The attention call over a 4-bit pool; stall_limit_ns as in step_setup (its decode phase issues no copy either).
+int attention_q4_call(const void* q_rot, const void* kv_cache, int32_t num_pages, const int32_t* cu_seqlens_q,
+                      const int32_t* q_start_pos, const int32_t* context_lens, const int32_t* block_tables,
+                      const int32_t* bt_offsets, int64_t bt_len, int32_t bt_stride, int32_t num_rows, int32_t num_tokens,
+                      int64_t context_total, int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, float scale, void* out,
+                      void* workspace, size_t ws_bytes, int64_t stall_limit_ns, ms_stream_t stream) {
   AttnParams p;
   bool empty = true;
   int rc = step_setup(q_rot, kv_cache, kv_cache, num_pages, cu_seqlens_q, q_start_pos, context_lens, block_tables,
                       bt_offsets, bt_offsets != nullptr ? bt_len : 0, bt_offsets != nullptr ? 0 : bt_stride, num_rows,
-                      num_tokens, context_total, H_q, H_kv, D, page_size, scale, out, workspace, ws_bytes, false, 0, &p,
-                      &empty);
+                      num_tokens, context_total, H_q, H_kv, D, page_size, scale, out, workspace, ws_bytes, false,
+                      stall_limit_ns, &p, &empty);
   if (rc != MS_OK || empty) return rc;
   p.kv_q4 = static_cast<const uint8_t*>(kv_cache);
   p.dec_workers = p.num_sms * (kQ4Threads / 32);
@@ -588,4 +589,31 @@ extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* 
     case 12804: return launch_q4<128, 4>(p, tq, st);
     default: return launch_q4<128, 8>(p, tq, st);
   }
+}
+
+}  // namespace
+
+extern "C" MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
+                                                 const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                                 const int32_t* context_lens, const int32_t* block_tables,
+                                                 const int32_t* bt_offsets, int64_t bt_len, int32_t bt_stride,
+                                                 int32_t num_rows, int32_t num_tokens, int64_t context_total, int32_t H_q,
+                                                 int32_t H_kv, int32_t D, int32_t page_size, float scale, void* out,
+                                                 void* workspace, size_t ws_bytes, ms_stream_t stream) {
+  return attention_q4_call(q_rot, kv_cache, num_pages, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets,
+                           bt_len, bt_stride, num_rows, num_tokens, context_total, H_q, H_kv, D, page_size, scale, out,
+                           workspace, ws_bytes, 0, stream);
+}
+
+extern "C" MS_API int ms_test_attention_stall_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
+                                                 const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                                 const int32_t* context_lens, const int32_t* block_tables,
+                                                 int32_t bt_stride, int32_t num_rows, int32_t num_tokens,
+                                                 int64_t context_total, int32_t H_q, int32_t H_kv, int32_t D,
+                                                 int32_t page_size, float scale, void* out, void* workspace,
+                                                 size_t ws_bytes, int64_t wait_limit_ns, ms_stream_t stream) {
+  if (wait_limit_ns < 100000 || wait_limit_ns > 2000000000ll) return MS_ERR_ARG;  // 0.1 ms .. 2 s
+  return attention_q4_call(q_rot, kv_cache, num_pages, cu_seqlens_q, q_start_pos, context_lens, block_tables, nullptr, 0,
+                           bt_stride, num_rows, num_tokens, context_total, H_q, H_kv, D, page_size, scale, out, workspace,
+                           ws_bytes, wait_limit_ns, stream);
 }

@@ -92,7 +92,8 @@ struct AttnParams {
   float* part_ml;
   float* part_acc;
   uint64_t wait_limit_ns;  // bound of every chunk-phase wait
-  int32_t test_stall;      // test hook: chunk-phase producers publish no work item (0 in every real call)
+  int32_t test_stall;      // test hook: chunk-phase producers publish no work item, decode warps over a
+                           // 4-bit pool issue no copy (0 in every real call)
   // chunk items in parts (4-bit pools), in what the workspace has behind its layout: room for ch_cap
   // parts of ch_rec query rows (ChunkParts)
   uint8_t* ch_parts;

@@ -468,6 +468,20 @@ MS_API int ms_mixed_step_attention_q4(const void* q_rot, const void* kv_cache, i
                                       int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, float scale,
                                       void* out, void* workspace, size_t ws_bytes, ms_stream_t stream);
 
+/* ms_test_attention_stall_q4 -- ms_test_attention_stall over a 4-bit pool
+ * (padded table): chunk-phase producers publish nothing, decode warps issue no
+ * copy, and the waits give up, the chunk phase's after wait_limit_ns, a decode
+ * warp's after 2 s.  No output is written, MS_STATUS_TIMEOUT is set, nothing is
+ * in flight when the kernel ends, and the next call on the workspace computes
+ * its step normally.  Not for production use.
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_test_attention_stall_q4(const void* q_rot, const void* kv_cache, int32_t num_pages,
+                                      const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                      const int32_t* context_lens, const int32_t* block_tables, int32_t bt_stride,
+                                      int32_t num_rows, int32_t num_tokens, int64_t context_total, int32_t H_q,
+                                      int32_t H_kv, int32_t D, int32_t page_size, float scale, void* out,
+                                      void* workspace, size_t ws_bytes, int64_t wait_limit_ns, ms_stream_t stream);
+
 /* ---- Step metadata on the GPU ----------------------------------------------
  * ms_build_batch_metadata_device -- the metadata of a step (what
  * ms_build_batch_metadata writes on the host) from the requests' lengths, on

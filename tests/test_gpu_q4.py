@@ -1071,3 +1071,29 @@ def test_rotation_in_place(env):
             ms.mixed_step_attention_q4(q_rot, pools[0], cu, start, ctx, b.block_tables, T, want, ws)
             assert torch.equal(mine, q_rot) and torch.equal(pools[2], pools[0]) and torch.equal(out, want)
             assert ms.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64), (8, 1, 64)])
+def test_stalled_copies_time_out_and_the_workspace_recovers(env, H_q, H_kv, D):
+    """The kernel's waits made to run out (no work item published, no copy issued): the chunk phase's after 1 ms, the
+    decode teams' after their 2 s; chunk rows whole and in parts, decode rows, both together.  The call ends, reports
+    it, writes no output, and the next call on the workspace, with the tensor memory that the stalled one held, is
+    right."""
+    import time
+    torch, ms, _ = env
+    for rows in ([(5, 1), (600, 1), (9000, 1)], [(0, 300), (777, 129)], [(9001, 20)],
+                 [(7 * i, 1) for i in range(100)] + [(100, 70), (64, 5)]):
+        a = Attn(env, rows, H_q, H_kv, D, seed=110 + len(rows))
+        for _ in range(1 if any(d == 1 for _, d in rows) else 2):
+            a.out.fill_(5.0)
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            ms.test_attention_stall_q4(a.q, a.pool, a.cu, a.start, a.ctx, a.bt, a.total, a.out, a.ws, 1_000_000)
+            torch.cuda.synchronize()
+            assert time.perf_counter() - t0 < 10.0
+            assert ms.read_status(a.ws) == ms.STATUS_TIMEOUT and (a.out == 5.0).all()
+            a.call()
+            a.check()
+    for limit in (0, 99_999, 2_000_000_001):
+        with pytest.raises(ms.MixedStepError):
+            ms.test_attention_stall_q4(a.q, a.pool, a.cu, a.start, a.ctx, a.bt, a.total, a.out, a.ws, limit)
