@@ -271,7 +271,9 @@ extern "C" MS_API int ms_kv_read_q4(const void* kv_cache, int32_t num_pages, con
   a.n = n;
   a.H_kv = H_kv;
   const int64_t units = static_cast<int64_t>(n) * H_kv * 4;
-  const unsigned blocks = static_cast<unsigned>(append_blocks(units, 152));
+  const int sms = ms_num_sms();
+  if (sms <= 0) return MS_ERR_CUDA;
+  const unsigned blocks = static_cast<unsigned>(append_blocks(units, sms));
   const bool small = units + static_cast<int64_t>(blocks) * 256 < (int64_t{1} << 31);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const auto kernel = D == 128 ? (small ? read_q4_kernel<128, uint32_t> : read_q4_kernel<128, int64_t>)
