@@ -171,6 +171,10 @@ class StepTables:
     Nothing in it depends on host data, so a step can be captured and replayed while ``cached_lens`` and ``new_tokens``
     change on the GPU.  ``info`` [4] and ``status`` [1] are those of
     build_batch_metadata_device.
+
+    The first ``free_state[0]`` entries of ``free_pages`` are the free ones.  Pages that a finished request held go back
+    between two builds by writing them behind those and adding to the count, on the GPU too: ``free_pages[n:n + k] =
+    pages; free_state[0] += k``.
     """
 
     def __init__(self, page_tables, num_pages: int, max_tokens: int, free_pages=None, max_context: int = None):

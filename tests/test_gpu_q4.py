@@ -1097,3 +1097,60 @@ def test_stalled_copies_time_out_and_the_workspace_recovers(env, H_q, H_kv, D):
     for limit in (0, 99_999, 2_000_000_001):
         with pytest.raises(ms.MixedStepError):
             ms.test_attention_stall_q4(a.q, a.pool, a.cu, a.start, a.ctx, a.bt, a.total, a.out, a.ws, limit)
+
+
+def test_pages_given_back_between_steps(env):
+    """A pool of 12 pages serves six requests of 5 pages each in turn: a finished one's pages go behind the free ones, by
+    operations on the GPU, and the next build hands them out again."""
+    torch, ms, step = env
+    R, pages, stride, cap = 2, 12, 6, 96
+    tables = step.StepTables(torch.full((R, stride), -1, dtype=torch.int32, device="cuda"), pages, cap,
+                             free_pages=torch.arange(pages, dtype=torch.int32, device="cuda"))
+    c, d = _i32(torch, [0, 0]), _i32(torch, [0, 0])
+    tab, free, count = np.full((R, stride), -1), list(range(pages)), pages
+    hc = np.zeros(R, dtype=np.int64)
+    for n in range(12):
+        new = [72 if hc[s] == 0 else 1 for s in range(R)] if n else [72, 0]  # the second request starts a step later
+        if n and sum(new) > cap:
+            new[1] = 0
+        d.copy_(_i32(torch, new))
+        tables.build(c, d)
+        m = oracle.metadata_from_lengths(hc, new, tab, cap, free=free, count=count)
+        tab, count = m["tables"], m["free_count"]
+        assert ms.read_status(tables.status) == 0
+        np.testing.assert_array_equal(tables.slot_mapping.tolist(), m["slot_mapping"])
+        np.testing.assert_array_equal(tables.page_tables.cpu().numpy(), tab)
+        c += d
+        hc = hc + new
+        for s in range(R):
+            if hc[s] >= 74:  # finished: its five pages back, and the row to the next request
+                at = tables.free_state[0].long() + torch.arange(5, device="cuda")
+                tables.free_pages.index_copy_(0, at, tables.page_tables[s, :5])
+                tables.free_state[0] += 5
+                tables.page_tables[s] = -1
+                c[s] = 0
+                free[count:count + 5], count, hc[s] = [int(x) for x in tab[s, :5]], count + 5, 0
+                tab[s] = -1
+    assert tables.free_state.tolist() == [count, 0] and tables.free_pages[:count].tolist() == free[:count]
+
+
+def test_two_steps_at_once(env):
+    """Two attention calls in flight on two streams, each with its workspace: the bits of each one alone."""
+    torch, ms, _ = env
+    a = Attn(env, [(3000, 1), (500, 200), (8000, 1)], 8, 2, 128, seed=120)
+    b = Attn(env, [(9001, 20), (77, 1), (64, 300)], 4, 4, 64, seed=121)
+    want = []
+    for x in (a, b):
+        x.call()
+        x.check()
+        want.append(x.out.clone())
+        x.outs = [torch.empty_like(x.out) for _ in range(20)]
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for i in range(20):
+        for x, st in zip((a, b), streams):
+            x.call(stream=st, out=x.outs[i])
+    torch.cuda.synchronize()
+    for x, w in zip((a, b), want):
+        assert all(torch.equal(o, w) for o in x.outs) and ms.read_status(x.ws) == 0
