@@ -35,8 +35,9 @@
 namespace {
 
 constexpr int kQ4Threads = 32 * (kDequantWarp0 + kDequantWarps);
-// The cost model's rates (attention_step.cuh).  The split that they choose is
-// within 1 % of the best of 13 forced ones on six mixed steps (124 to 2140 us).
+// The cost model's rates (attention_step.cuh), measured at D = 128 and used for both
+// head dims.  In a build that forced the split for the purpose, the one that they
+// choose was within 1 % of the best of 13 on six mixed steps (124 to 2140 us).
 constexpr float kQ4TileCycles = 4900.f;
 constexpr float kQ4DecodeBytesPerCycle = 24.f;
 
@@ -99,10 +100,12 @@ struct IssueCursor {
 // 16384 keys: 372 us with a warp to a split of 64 pages, 310 us with four to 512;
 // 61 rows of 1 to 5003 keys, 2 KV heads, D = 64: 55 us, and 20 us with eight to 32.
 //
-// What bounds it is instructions: about 360 a page and warp (2.25 KB of K and V
+// Instructions are nearest to a limit: about 355 a page and warp (2.25 KB of K and V
 // at D = 128), half of them on the logic pipe, which is 65 % busy, as are the
 // issue slots; DRAM delivers 4.8 TB/s, 0.70 of the measured copy rate (256 rows,
-// above).  Measured and not kept: shifts as multiplications (310 -> 362 to 388 us);
+// above).  Neither is full: with four warps to a scheduler, dependent steps and
+// the pipe's turns leave the rest.  64 rows of 32 heads of their own and 512 to 4096
+// keys: 122 us, 4.2 TB/s, issue slots 60 % busy.  Measured and not kept: shifts as multiplications (310 -> 362 to 388 us);
 // V's offset taken off by a product with -136 instead of before it (330 us);
 // one page at a time; 16-byte asynchronous copies by all lanes instead of a bulk
 // copy a page (346 us before the teams, 378 us).

@@ -309,10 +309,11 @@ __device__ __forceinline__ int decode_split(const AttnParams& p, int64_t dec_pag
 // P / W: pages per warp; L = min(split, longest row) / team: pages of a warp's
 // share; n: splits of the longest row, which one team joins; o = 16, 11, 9, 9.4 by
 // team size: the cost of a split around its pages; c = 1.15: a page's with the
-// SM full (D = 128).  Fitted to sweeps of 27 pairs over 28 steps (1 to 512 rows
-// of 1 to 32 KV heads, 1 to 131072 keys, 19 to 420 us): its choice is 2.3 % slower
-// than the best pair on average, 11 % but for one step (4 rows of 64K to 128K
-// keys: 20 %).  Called by whole warps.
+// SM full at D = 128 (used at 64 too, where a page is half the work).  Fitted to
+// sweeps of 27 pairs over 28 steps (1 to 512 rows of 1 to 32 KV heads, 1 to 131072
+// keys, 19 to 420 us) in a build that forced the pair for the purpose: its choice was
+// 2.3 % slower than the best pair on average, 11 % but for one step (4 rows of 64K to
+// 128K keys: 20 %).  Called by whole warps.
 struct DecPlan {
   int split, team;
 };
@@ -352,12 +353,13 @@ __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_
 // they are fewer than half the CTAs that chunk work gets beside the decodes (k,
 // the balance of chunk_cta_split): every part then starts at once.  Parts are
 // written out and the last one to finish joins them, which costs about 0.0125 us a
-// part and row where a tile takes about 1 us, hence the square root; 8 tiles and a
+// part and row where a tile takes about 1 us (D = 128), hence the square root; 8 tiles and a
 // 32nd of the longest item at least, and only for a fifth of its time or more.
 // pairs, pair_tiles: of one KV head, over the rows (a Q tile alone takes about the
-// time of a pair).  32 / 8 heads, D = 128, whole and in parts: 20 tokens at 28000
-// 342 and 72 us, 4 at 100000 1192 and 95 us, 128 at 8000 beside 16 decodes 132 and
-// 71 us, four rows of 32 at 3000 to 6000 84 and 52 us.
+// time of a pair).  32 / 8 heads, D = 128, whole (on a workspace without the room) and
+// in parts: 20 tokens at 28000 347 and 71 us, 4 at 100000 1217 and 97 us, 128 at 8000
+// beside 16 decodes of 512 to 8012 keys 131 and 81 us, four rows of 32 at 3000 to 6000
+// 85 and 53 us.
 __device__ __forceinline__ int chunk_part_tiles(const AttnParams& p, float pairs, float pair_tiles, float longest,
                                                 float dec_pages) {
   const float n0 = pairs * p.H_kv, work = pair_tiles * p.H_kv;

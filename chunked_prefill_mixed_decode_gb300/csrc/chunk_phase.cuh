@@ -355,11 +355,13 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
 // write a quarter of their values -- exactly bf16; the score scale and the last
 // division make up for the factor -- into the K and V stages: warp 12 + w page w
 // of each tile.  Two chunks of 3968 tokens at 0 and 6000, 32 / 8 heads, D = 128:
-// 501 us, 1.29 PFLOP/s, 0.69 of the measured dense rate; the tensor pipe is 55 %
-// and the issue slots 59 % busy.  A tile pair takes about 1800 cycles, in which
-// the softmax warps, the dequantizing warps and the issuers are each busy nearly
-// all the time: without any softmax work it would take 482 us, without any
-// dequantizing 487.
+// 508 us over the same inputs again, 516 to 520 with the inputs changing from call
+// to call, 1.25 PFLOP/s, 0.67 of the measured dense rate; the tensor pipe is 55 % and
+// the issue slots 59 % busy, so neither is a limit reached.  A tile pair takes about
+// 1800 cycles, in which the softmax warps (which spill: 128 registers a thread), the
+// dequantizing warps and the issuers are each busy nearly all the time; copies of the
+// kernel without any softmax work, or without any dequantizing, took 482 and 487 us
+// where the whole took 507.
 // Measured and not kept, before the issue by elected lanes (605 us then): loads
 // from global memory into the dequantizing warps' registers a tile ahead, without
 // the ring (740 us); where items are few, one Q tile for both softmax groups, every
@@ -429,7 +431,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   volatile int* abort_flag = &bars->abort;
   const uint64_t lim = p.wait_limit_ns;
   // The MMA issuers.  Over a 4-bit pool a whole warp runs the loop and one elected lane
-  // issues, which takes the issue off the critical path: 605 -> 507 us for chunks of
+  // issues, which takes the issue off the critical path: 605 -> 507 us then for chunks of
   // 3968 tokens at 0 and 6000, 32 / 8 heads.  Over a bf16 pool, where the same change
   // measures 522 -> 527 us there and 2060 -> 2110 us beside long decodes (and 69 -> 61 us
   // for D = 64), lane 0 runs it alone.

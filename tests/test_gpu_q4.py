@@ -1154,3 +1154,30 @@ def test_two_steps_at_once(env):
     torch.cuda.synchronize()
     for x, w in zip((a, b), want):
         assert all(torch.equal(o, w) for o in x.outs) and ms.read_status(x.ws) == 0
+
+
+def test_a_step_that_the_tables_refuse_computes_nothing(env):
+    """The free list runs short: the step becomes one of pad rows, the append and the attention after it leave cache and
+    output as they were, and the next step, with pages enough, is served."""
+    torch, ms, step = env
+    H_q, H_kv, D, pages, cap = 8, 2, 128, 3, 64
+    pool = _pool(torch, pages, H_kv, D, 130)
+    before = pool.clone()
+    tables = step.StepTables(torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), pages, cap,
+                             free_pages=torch.arange(pages, dtype=torch.int32, device="cuda"))
+    cos, sin = step.rope_tables_device(64, D, "cuda")
+    q, k, v = (torch.randn(cap, H, D, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+    q_rot, out = torch.empty_like(q), torch.full_like(q, 5.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = step.workspace_for(tables.batch, H_q, H_kv, D, "cuda", q4=True)
+    c = _i32(torch, [0, 0])
+    step.run_step_q4(q, k, v, tables.build(c, _i32(torch, [20, 17])), cos, sin, pool, out, ws, q_rot=q_rot, dev_status=status)
+    assert ms.read_status(tables.status) == ms.STATUS_NO_PAGES and ms.read_status(status) == 0 and ms.read_status(ws) == 0
+    assert torch.equal(pool, before) and (out == 5.0).all()
+    assert tables.free_state.tolist() == [pages, 0] and (tables.page_tables == -1).all()
+    step.run_step_q4(q, k, v, tables.build(c, _i32(torch, [20, 16])), cos, sin, pool, out, ws, q_rot=q_rot, dev_status=status)
+    assert ms.read_status(tables.status) == 0 and ms.read_status(status) == 0 and ms.read_status(ws) == 0
+    a = Attn(env, [(0, 20), (0, 16)], H_q, H_kv, D, pool=pool)
+    a.pages = [[2, 1], [0]]
+    a.q, a.ws, a.out = q_rot, ws, out
+    a.check()
