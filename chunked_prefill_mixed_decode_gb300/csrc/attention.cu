@@ -400,7 +400,9 @@ __device__ __forceinline__ void invalidate_phase_barriers(uint8_t* smem, bool ch
   if (chunk) {
     if (threadIdx.x == 0) {
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
-      close_chunk_barriers(bars, &bars->mma_done[2]);
+      uint64_t* b0 = &bars->q_full;
+      uint64_t* b1 = &bars->mma_done[2];
+      for (uint64_t* b = b0; b <= b1; ++b) mbar_inval(b);
     }
   } else if ((threadIdx.x & 31) == 0 && (threadIdx.x >> 5) < DecCfg<D, G>::WARPS) {
     using C = DecCfg<D, G>;

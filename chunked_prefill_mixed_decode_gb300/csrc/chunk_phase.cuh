@@ -59,10 +59,12 @@ struct ChBars {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // 4-bit pools: pages as they are stored
   uint32_t tmem;
   int abort;
-  int q_asked;  // items whose Q tiles have been asked for
   ChItem items[2];
   ChPart parts[2];
   int last[2];
+  // 4-bit pools: items whose Q tiles have been asked for.  Behind the rest: ahead of
+  // `items` it costs a GQA 8B step over bf16 pools 0.6 %.
+  int q_asked;
 };
 
 static_assert(sizeof(ChBars) <= 1024, "chunk-phase barrier block exceeds its reserved space");
@@ -70,10 +72,12 @@ static_assert(ChCfg<128>::SMEM <= 232448 && ChCfg<64>::SMEM <= 232448,
               "chunk phase exceeds the per-CTA shared-memory limit");
 static_assert(ChCfg<128>::KVS <= 8 && ChCfg<64>::KVS <= 8, "more K/V stages than barriers");
 
-// By one thread once every warp has left the phase: Q tiles that a phase given up
-// early still has in flight land, and its barriers, up to `last`, are invalidated.
-// (Here and not at the producer's end, where the loops of the phase pay for it in
-// registers: 516 -> 519.6 us, two chunks of 3968 tokens over 4-bit pages.)
+// Over a 4-bit pool, by one thread once every warp has left the phase: Q tiles that
+// a phase given up early still has in flight land, and its barriers, up to `last`,
+// are invalidated.  (Here and not at the producer's end, where the loops of the phase
+// pay for it in registers: 516 -> 519.6 us, two chunks of 3968 tokens.  The bf16 phase
+// keeps no count of its Q tiles: with it a GQA 8B step takes 0.9 % longer, 0.720 ->
+// 0.728 ms.  Its waits run for 2 s, a Q tile's copy for a few microseconds.)
 __device__ __forceinline__ void close_chunk_barriers(ChBars* bars, uint64_t* last) {
   const int n_q = bars->q_asked;
   if (n_q > 0) mbar_wait(&bars->q_full, (n_q - 1) & 1, nullptr, 200000000ull);
@@ -424,7 +428,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         mbar_init(&bars->part_last[t], 1);
       }
     bars->abort = 0;
-    bars->q_asked = 0;
+    if constexpr (Q4) bars->q_asked = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -582,7 +586,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       const int nq = it.ntok[1] > 0 ? 2 : 1;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
-        bars->q_asked = n_done;
+        if constexpr (Q4) bars->q_asked = n_done;
       }
       __syncwarp();
       if (lane < nq * NSL) {
