@@ -74,6 +74,16 @@ class GraphBuffers(ctypes.Structure):
                [("ws_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
 
 
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_BANDS, ROTARY_RAMP = 0, 1, 2, 3, 4
+_ROTARY_KINDS = {"plain": ROTARY_PLAIN, "linear": ROTARY_LINEAR, "base": ROTARY_BASE, "bands": ROTARY_BANDS,
+                 "ramp": ROTARY_RAMP}
+
+
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_len", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
 _lib_handle = None
 # ms_mixed_step runs the attention's prologue inside the append's launch on steps of at most
 # this many rows (mixed_step.h)
@@ -181,6 +191,20 @@ def lib() -> ctypes.CDLL:
             ("ms_build_batch_metadata_device", [_VP, _VP, ctypes.c_int32, _VP, ctypes.c_int32, _VP, ctypes.c_int32,
                                                 _VP, _VP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP,
                                                 _VP, ctypes.c_int32, _VP, _VP, ctypes.c_int64, _VP, _VP, _VP])):
+        getattr(h, name).restype = ctypes.c_int
+        getattr(h, name).argtypes = args
+    i32, i64, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    for name, args in (
+            ("ms_rotary_frequencies", [i32, f64, ctypes.POINTER(RotaryScaling), _VP, _VP]),
+            ("ms_rotary_table_device", [_VP, i32, f64, i32, i32, _VP, _VP, _VP]),
+            ("ms_kv_append_rotary", [_VP, i64, _VP, i64, _VP, i64, _VP, _VP, i32, _VP, _VP, i32, i32, i32, _VP, _VP, i32,
+                                     _VP, i32, i32, i32, i32, _VP, _VP]),
+            ("ms_mixed_step_attention_window", [_VP, _VP, _VP, i32, _VP, _VP, _VP, _VP, _VP, i64, i32, i32, i32, i64, i32,
+                                                i32, i32, i32, ctypes.c_float, i32, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            ("ms_test_attention_stall_window", [_VP, _VP, _VP, i32, _VP, _VP, _VP, _VP, i32, i32, i32, i64, i32, i32, i32,
+                                                i32, ctypes.c_float, i32, _VP, _VP, ctypes.c_size_t, i64, _VP]),
+            ("ms_mixed_step_cross_attention", [_VP, _VP, _VP, i32, _VP, _VP, _VP, _VP, i64, i32, i32, i32, i64, i32, i32,
+                                               i32, i32, ctypes.c_float, _VP, _VP, ctypes.c_size_t, _VP])):
         getattr(h, name).restype = ctypes.c_int
         getattr(h, name).argtypes = args
     h.ms_graph_workspace_size.restype = ctypes.c_size_t
@@ -487,11 +511,35 @@ def rope_table(max_pos: int, D: int, base: float = 10000.0):
     return cos, sin
 
 
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict = None) -> tuple:
+    """The rotary frequencies (fp64 [rotary_dim / 2], radians a position) and the factor of their cosines and sines
+    (ms_rotary_frequencies).  ``scaling``: None, or a dict of ``kind`` ("plain", "linear", "base", "bands" or "ramp"),
+    ``factor`` and, for bands and ramp, ``original_len``, ``low`` and ``high`` (turns over the original length); for
+    ramp also ``amplitude``, by default 0.1 ln(factor) + 1."""
+    freq = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.float64)
+    amplitude = ctypes.c_double(1.0)
+    sc = None
+    if scaling is not None:
+        d = dict(scaling)
+        kind = d.pop("kind", None)
+        if kind not in _ROTARY_KINDS:
+            raise ValueError(f"scaling kind must be one of {sorted(_ROTARY_KINDS)}, got {kind!r}")
+        names = {"factor"} if kind in ("linear", "base") else set() if kind == "plain" else {"factor", "original_len", "low", "high"}
+        given = set(d) - ({"amplitude"} if kind == "ramp" else set())
+        if given != names:
+            raise ValueError(f"scaling {kind!r} takes {sorted(names)}, got {sorted(given)}")
+        sc = RotaryScaling(_ROTARY_KINDS[kind], int(d.get("original_len", 0)), float(d.get("factor", 1.0)),
+                           float(d.get("low", 0.0)), float(d.get("high", 0.0)), float(d.get("amplitude") or 0.0))
+    _check(lib().ms_rotary_frequencies(int(rotary_dim), float(base), None if sc is None else ctypes.byref(sc),
+                                       freq.ctypes.data, ctypes.addressof(amplitude)), "ms_rotary_frequencies")
+    return freq, amplitude.value
+
+
 def attention_workspace_size(max_rows: int, max_tokens: int, max_context_total: int, H_q: int, H_kv: int,
                              D: int, q4: bool = True) -> int:
     """Workspace bytes for steps of these sizes, over a pool of either kind (ms_attention_workspace_size_q4).  With
-    ``q4=False`` for bf16 pools alone (ms_attention_workspace_size), up to 20 MB less; the 4-bit call takes such a
-    workspace too, and then leaves few long chunk items whole."""
+    ``q4=False`` for bf16 pools alone (ms_attention_workspace_size), up to 20 MB less; the calls over a 4-bit pool, a
+    window or an encoder's states take such a workspace too, and then leave few long chunk items whole."""
     size = lib().ms_attention_workspace_size_q4 if q4 else lib().ms_attention_workspace_size
     return int(size(int(max_rows), int(max_tokens), int(max_context_total), int(H_q), int(H_kv), int(D)))
 
@@ -897,6 +945,179 @@ def _attention_q4(q_rot, kv_cache, cu_seqlens_q, q_start_pos, context_lens, bloc
                                           int(context_total), H_q, H_kv, D, PAGE_SIZE, float(scale), out.data_ptr(),
                                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
     _check(rc, "ms_mixed_step_attention_q4")
+
+
+# ---------------------------------------------------------------------------- other rotations, windows, cross attention
+
+def rotary_table_device(freq, cos_tab, sin_tab, amplitude: float = 1.0, first_pos: int = 0, stream=None) -> None:
+    """Cosines and sines of ``freq`` (host fp64 [pairs], rotary_frequencies) at the positions ``first_pos`` on, into the
+    device tables [n, pairs] (ms_rotary_table_device)."""
+    import torch
+    freq = np.ascontiguousarray(freq, dtype=np.float64)
+    if freq.ndim != 1 or cos_tab.dim() != 2:
+        raise ValueError("freq must be 1-D and cos_tab [n, pairs]")
+    _dev(cos_tab, "cos_tab", torch.float32, (cos_tab.shape[0], freq.shape[0]))
+    _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
+    st = _stream_of(stream, "cos_tab sin_tab", cos_tab, sin_tab)
+    _check(lib().ms_rotary_table_device(freq.ctypes.data, freq.shape[0], float(amplitude), int(first_pos), cos_tab.shape[0],
+                                        cos_tab.data_ptr(), sin_tab.data_ptr(), st), "ms_rotary_table_device")
+
+
+def _token_rows(t, name: str, T: int, H: int, D: int) -> int:
+    """Check a tensor [T, H, D] whose tokens' rows may lie apart (a slice of a fused projection); returns the elements
+    from one token to the next."""
+    import torch
+    if t is None or t.dim() != 3 or t.shape != (T, H, D):
+        raise ValueError(f"{name} must be [{T}, {H}, {D}], got {None if t is None else tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != D and H > 1):
+        raise ValueError(f"{name}: a token's heads must lie back to back, got strides {s}")
+    return s[0] if T > 1 else H * D
+
+
+def kv_append_rotary(q, k, v, positions, slot_mapping, cos_tab, sin_tab, k_cache, v_cache, q_rot=None,
+                     interleaved: bool = False, dev_status=None, stream=None) -> None:
+    """Rotate q and k over the first ``2 * cos_tab.shape[1]`` elements of a head, in pairs (i, i + R/2) or, with
+    ``interleaved``, (2i, 2i + 1), and append k, v into the paged pools (ms_kv_append_rotary).
+
+    q, k and v are [T, heads, D]; their tokens' rows may lie apart, as in slices of a fused projection.  ``q`` None: only
+    k and v.  ``cos_tab`` and ``sin_tab`` None: nothing turns, and ``positions`` is not looked at.  ``q_rot``
+    [T, H_q, D] is contiguous; by default q is rotated in place, which needs a contiguous q."""
+    import torch
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, H_kv, {PAGE_SIZE}, D]")
+    if k is None or k.dim() != 3:
+        raise ValueError("k must be [T, H_kv, D]")
+    H_kv, D = k_cache.shape[1], k_cache.shape[3]
+    T = k.shape[0]
+    _pools(k_cache, v_cache, H_kv, D)
+    ks, vs = _token_rows(k, "k", T, H_kv, D), _token_rows(v, "v", T, H_kv, D)
+    H_q = qs = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [T, H_q, D], got {tuple(q.shape)}")
+        H_q = q.shape[1]
+        qs = _token_rows(q, "q", T, H_q, D)
+        if q_rot is None:
+            q_rot = q
+        _dev(q_rot, "q_rot", torch.bfloat16, (T, H_q, D))
+    elif q_rot is not None:
+        raise ValueError("q_rot without q")
+    _dev(slot_mapping, "slot_mapping", torch.int32, min_numel=T)
+    R = max_pos = 0
+    if (cos_tab is None) != (sin_tab is None):
+        raise ValueError("cos_tab and sin_tab come together")
+    if cos_tab is not None:
+        if cos_tab.dim() != 2:
+            raise ValueError("cos_tab must be [max_pos, R/2]")
+        max_pos, R = cos_tab.shape[0], 2 * cos_tab.shape[1]
+        _dev(cos_tab, "cos_tab", torch.float32)
+        _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
+        _dev(positions, "positions", torch.int32, min_numel=T)
+    else:
+        positions = None
+    if dev_status is not None:
+        _dev(dev_status, "dev_status", torch.int32, min_numel=1)
+    st = _stream_of(stream, "k v q q_rot positions slot_mapping cos_tab sin_tab k_cache v_cache dev_status", k, v, q, q_rot,
+                    positions, slot_mapping, cos_tab, sin_tab, k_cache, v_cache, dev_status)
+    rc = lib().ms_kv_append_rotary(_ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(positions), slot_mapping.data_ptr(),
+                                   T, _ptr(cos_tab), _ptr(sin_tab), max_pos, R, 1 if interleaved else 0, k_cache.data_ptr(),
+                                   v_cache.data_ptr(), k_cache.shape[0], _ptr(q_rot), H_q, H_kv, D, PAGE_SIZE,
+                                   _ptr(dev_status), st)
+    _check(rc, "ms_kv_append_rotary")
+
+
+def _span_args(q, k_cache, v_cache, cu_seqlens_q, block_tables, bt_offsets, out, workspace):
+    """The checks that the windowed and the cross attention share; returns (T, H_q, D, H_kv, rows, stride, bt_len)."""
+    import torch
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H_q, D], got {tuple(q.shape)}")
+    T, H_q, D = q.shape
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, H_kv, {PAGE_SIZE}, D]")
+    H_kv = k_cache.shape[1]
+    _dev(q, "q", torch.bfloat16)
+    _pools(k_cache, v_cache, H_kv, D)
+    if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must be 1-D with rows + 1 entries")
+    S = cu_seqlens_q.shape[0] - 1
+    _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32)
+    if bt_offsets is None:
+        stride = block_tables.shape[1] if block_tables.dim() == 2 else block_tables.shape[0] // max(S, 1)
+        _dev(block_tables, "block_tables", torch.int32, min_numel=S * stride)
+        bt_len = 0
+    else:
+        _dev(bt_offsets, "bt_offsets", torch.int32, min_numel=S + 1)
+        _dev(block_tables, "block_tables", torch.int32, min_numel=1)
+        stride, bt_len = 0, block_tables.numel()
+    _dev(out, "out", torch.bfloat16, (T, H_q, D))
+    _dev(workspace, "workspace", None)
+    return T, H_q, D, H_kv, S, stride, bt_len
+
+
+def mixed_step_attention_window(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables,
+                                context_total: int, out, workspace, window: int, sinks=None, bt_offsets=None,
+                                scale: float = None, stream=None) -> None:
+    """Causal attention of every packed row over the last ``window`` keys up to each token's own, with an optional sink
+    per query head (fp32 [H_q]): a logit that joins the softmax's sum without a value (ms_mixed_step_attention_window).
+    ``block_tables`` is the padded [rows, stride] table, or, with ``bt_offsets`` given, the ragged page list; entries
+    of pages that lie wholly in front of a row's first window are not read."""
+    import torch
+    T, H_q, D, H_kv, S, stride, bt_len = _span_args(q_rot, k_cache, v_cache, cu_seqlens_q, block_tables, bt_offsets, out,
+                                                    workspace)
+    _dev(q_start_pos, "q_start_pos", torch.int32, min_numel=S)
+    _dev(context_lens, "context_lens", torch.int32, min_numel=S)
+    if sinks is not None:
+        _dev(sinks, "sinks", torch.float32, (H_q,))
+    st = _stream_of(stream, "q_rot k_cache v_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace "
+                    "sinks", q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out,
+                    workspace, sinks)
+    rc = lib().ms_mixed_step_attention_window(
+        q_rot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], cu_seqlens_q.data_ptr(),
+        q_start_pos.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), _ptr(bt_offsets), bt_len, stride, S, T,
+        int(context_total), H_q, H_kv, D, PAGE_SIZE, float(D) ** -0.5 if scale is None else float(scale),
+        min(int(window), 2 ** 31 - 1), _ptr(sinks), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st)
+    _check(rc, "ms_mixed_step_attention_window")
+
+
+def test_attention_stall_window(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables,
+                                context_total: int, out, workspace, window: int, wait_limit_ns: int,
+                                scale: float = None, stream=None) -> None:
+    """test_attention_stall over a window (ms_test_attention_stall_window).  Not for production use."""
+    import torch
+    T, H_q, D, H_kv, S, stride, _ = _span_args(q_rot, k_cache, v_cache, cu_seqlens_q, block_tables, None, out, workspace)
+    _dev(q_start_pos, "q_start_pos", torch.int32, min_numel=S)
+    _dev(context_lens, "context_lens", torch.int32, min_numel=S)
+    st = _stream_of(stream, "q_rot k_cache v_cache cu_seqlens_q q_start_pos context_lens block_tables out workspace", q_rot,
+                    k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, out, workspace)
+    rc = lib().ms_test_attention_stall_window(
+        q_rot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], cu_seqlens_q.data_ptr(),
+        q_start_pos.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), stride, S, T, int(context_total), H_q,
+        H_kv, D, PAGE_SIZE, float(D) ** -0.5 if scale is None else float(scale), int(window), out.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(wait_limit_ns), st)
+    _check(rc, "ms_test_attention_stall_window")
+
+
+def mixed_step_cross_attention(q, k_cache, v_cache, cu_seqlens_q, key_lens, block_tables, key_total: int, out, workspace,
+                               bt_offsets=None, scale: float = None, stream=None) -> None:
+    """Attention of every token of row s to all ``key_lens[s]`` keys in the row's pages, the states of an encoder
+    (ms_mixed_step_cross_attention); zeros for the tokens of a row without keys.  ``key_total``: the sum of key_lens, or
+    more."""
+    import torch
+    T, H_q, D, H_kv, S, stride, bt_len = _span_args(q, k_cache, v_cache, cu_seqlens_q, block_tables, bt_offsets, out,
+                                                    workspace)
+    _dev(key_lens, "key_lens", torch.int32, min_numel=S)
+    st = _stream_of(stream, "q k_cache v_cache cu_seqlens_q key_lens block_tables bt_offsets out workspace", q, k_cache,
+                    v_cache, cu_seqlens_q, key_lens, block_tables, bt_offsets, out, workspace)
+    rc = lib().ms_mixed_step_cross_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], cu_seqlens_q.data_ptr(), key_lens.data_ptr(),
+        block_tables.data_ptr(), _ptr(bt_offsets), bt_len, stride, S, T, int(key_total), H_q, H_kv, D, PAGE_SIZE,
+        float(D) ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), st)
+    _check(rc, "ms_mixed_step_cross_attention")
 
 
 def build_batch_metadata_device(cached_lens, new_tokens, page_tables, num_pages: int, cu_seqlens_q, q_start_pos,

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libmixed_step.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["sched.cpp", "engine.cpp", "graph.cpp", "append_rope.cu", "attention.cu",
-           "append_q4.cu", "attention_q4.cu", "metadata.cu"]
+           "append_q4.cu", "attention_q4.cu", "metadata.cu", "attention_span.cu", "rotary.cu"]
 
 
 def _nvcc() -> str:

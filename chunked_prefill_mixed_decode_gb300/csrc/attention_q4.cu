@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) attention_q4_kernel(const __gri
       decode_phase_q4<D, G>(p, smem);
       __syncthreads();
     } else if (chunk && n_ch_items > 0) {
-      chunk_phase<D, G, true>(&tm_q, &tm_q, &tm_q, &tm_q, p, smem, tmem);
+      chunk_phase<D, G, kQ4>(&tm_q, &tm_q, &tm_q, &tm_q, p, smem, tmem);
       tc_fence_before();
       __syncthreads();
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
@@ -565,13 +565,7 @@ int attention_q4_call(const void* q_rot, const void* kv_cache, int32_t num_pages
   p.tile_cycles = kQ4TileCycles;
   p.dec_bytes_cycle = kQ4DecodeBytesPerCycle;
   p.key_bytes = q4_block_bytes(D) / 16.f;
-  {  // room for chunk items in parts, in what the workspace has behind the layout
-    const size_t used = align_up(ws_layout(num_rows, num_tokens, context_total, H_q, H_kv, D).total, 256);
-    p.ch_parts = static_cast<uint8_t*>(workspace) + used;
-    p.ch_rec = part_rows(num_tokens, p.G);
-    const int64_t cap = ws_bytes > used ? static_cast<int64_t>((ws_bytes - used) / part_bytes(p.ch_rec, D)) : 0;
-    p.ch_cap = num_tokens < 2 ? 0 : cap > p.num_sms ? p.num_sms : static_cast<int32_t>(cap);
-  }
+  set_parts_room(&p, workspace, ws_bytes, context_total);
   EncodeTiledFn enc = get_encode_fn();
   if (enc == nullptr) return MS_ERR_CUDA;
   CUtensorMap tq;

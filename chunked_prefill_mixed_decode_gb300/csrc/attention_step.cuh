@@ -94,10 +94,16 @@ struct AttnParams {
   uint64_t wait_limit_ns;  // bound of every chunk-phase wait
   int32_t test_stall;      // test hook: chunk-phase producers publish no work item, decode warps over a
                            // 4-bit pool issue no copy (0 in every real call)
-  // chunk items in parts (4-bit pools), in what the workspace has behind its layout: room for ch_cap
+  // chunk items in parts (4-bit pools, spans), in what the workspace has behind its layout: room for ch_cap
   // parts of ch_rec query rows (ChunkParts)
   uint8_t* ch_parts;
   int32_t ch_cap, ch_rec;
+  // Spans (the kernels' Span instances).  The query at position p sees the keys p - window + 1 .. p of its
+  // row; with fixed_span every query of a row sees all of the row's ctx_lens keys, as the query at position
+  // ctx_lens - 1 would without a window, and q_start is not read.  sinks: per query head a logit that
+  // joins the softmax's sum without a value, or nullptr.
+  const float* sinks;
+  int32_t window, fixed_span;
 };
 
 // Where the parts' records lie: sums of O first ([part][row][D]), (max, sum)
@@ -165,6 +171,32 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
   return v;
 }
 
+// Spans: position of a row's first query, the first key that the query at position
+// pos sees, the pages that a decode row reads, and the keys that any pair of Q tiles
+// of a chunk row walks at most (from a page boundary).
+__device__ __forceinline__ int span_start(const AttnParams& p, int row) {
+  return p.fixed_span ? __ldg(p.ctx_lens + row) - 1 : __ldg(p.q_start + row);
+}
+
+__device__ __forceinline__ int span_first(const AttnParams& p, int pos) {
+  return pos >= p.window ? pos - p.window + 1 : 0;
+}
+
+__device__ __forceinline__ int span_pages(const AttnParams& p, int ctx) {
+  return static_cast<int>(static_cast<unsigned>(ctx + kPage - 1) / kPage) - span_first(p, ctx - 1) / kPage;
+}
+
+__device__ __forceinline__ int span_keys(const AttnParams& p, int c, int d, int tpt) {
+  if (p.fixed_span) return c + 1;
+  const int64_t most = static_cast<int64_t>(p.window) + min(d, 2 * tpt) + kPage - 2;
+  return most < c + d ? static_cast<int>(most) : c + d;
+}
+
+// log2 units, as the scores are
+__device__ __forceinline__ float sink_log2(const AttnParams& p, int head) {
+  return __ldg(p.sinks + head) * 1.4426950408889634f;
+}
+
 // Work items of one row: decode splits of `split` pages, or pairs of 128-row Q tiles.
 __device__ __forceinline__ int row_items(bool chunk, int c, int d, int tpt, unsigned split) {
   if (!chunk) return static_cast<int>((static_cast<unsigned>(c + kPage) / kPage + split - 1) / split);
@@ -180,12 +212,55 @@ __device__ __forceinline__ int chunk_parts(int c, int d, int tiles) {
   return static_cast<int>((static_cast<unsigned>(c + d + kChunkTile - 1) / kChunkTile + tiles - 1) / tiles);
 }
 
+__device__ __forceinline__ int span_parts(const AttnParams& p, int c, int d, int tpt, int tiles) {
+  const unsigned n = (static_cast<unsigned>(span_keys(p, c, d, tpt)) + kChunkTile - 1) / kChunkTile;
+  return max(1, static_cast<int>((n + tiles - 1) / tiles));
+}
+
 // 128x128 tiles of a chunk row's Q tiles against their causal key ranges (the
 // cost model's unit of chunk work)
 __device__ __forceinline__ unsigned chunk_tiles(int c, int d, int tpt) {
   unsigned tiles = 0;
   for (int end = tpt; end - tpt < d; end += tpt) tiles += static_cast<unsigned>(c + min(d, end) + 127) >> 7;
   return tiles;
+}
+
+// The same, with what a row sees given by its span: pages of a decode row, work items,
+// 128x128 tiles and the cost that orders the rows.
+template <bool Span>
+__device__ __forceinline__ int dec_pages_of(const AttnParams& p, int ctx) {
+  return Span ? span_pages(p, ctx) : (ctx + kPage - 1) / kPage;
+}
+
+template <bool Span>
+__device__ __forceinline__ int items_of(const AttnParams& p, bool chunk, int c, int d, int tpt, unsigned split) {
+  if (!Span || chunk) return row_items(chunk, c, d, tpt, split);
+  return max(1, static_cast<int>((span_pages(p, c + 1) + split - 1) / split));  // a row without keys: its zeros
+}
+
+template <bool Span>
+__device__ __forceinline__ int parts_of(const AttnParams& p, int c, int d, int tpt, int tiles) {
+  return Span ? span_parts(p, c, d, tpt, tiles) : chunk_parts(c, d, tiles);
+}
+
+template <bool Span>
+__device__ __forceinline__ unsigned tiles_of(const AttnParams& p, int c, int d, int tpt) {
+  if (!Span) return chunk_tiles(c, d, tpt);
+  if (p.fixed_span) return static_cast<unsigned>(d + tpt - 1) / tpt * ((static_cast<unsigned>(c) + 128u) >> 7);
+  unsigned tiles = 0;
+  for (int tok = 0; tok < d; tok += tpt) {
+    const int end = c + min(d, tok + tpt);
+    tiles += static_cast<unsigned>(end - span_first(p, c + tok) + 127) >> 7;
+  }
+  return tiles;
+}
+
+template <bool Span>
+__device__ __forceinline__ float cost_of(const AttnParams& p, bool chunk, float c, float d) {
+  if (!Span) return chunk ? 0.5f * d * (2.f * c + d + 1.f) : c + 1.f;
+  const float w = static_cast<float>(p.window);
+  const float keys = p.fixed_span || !chunk ? fminf(c + 1.f, w) : fminf(c + 0.5f * (d + 1.f), w);
+  return fmaxf(1.f, chunk ? d * keys : keys);
 }
 
 // Sort key of the row at position `pos` of its list: the top 19 bits of the
@@ -385,6 +460,7 @@ __device__ __noinline__ int plan_parts_warp(const AttnParams& p, int keys, int n
 // chunk_part_tiles for the rows of a block, from their values in shared memory.  Called by every
 // thread.  Both forms are out of line: the prologue runs from a cold instruction cache, and most
 // steps need neither.
+template <bool Span>
 __device__ __noinline__ int plan_parts_block(const AttnParams& p, const int* rd, const int* rc, int64_t dec_pages) {
   __shared__ long long s_tiles[32];
   __shared__ int s_pairs[32], s_longest[32];
@@ -394,7 +470,7 @@ __device__ __noinline__ int plan_parts_block(const AttnParams& p, const int* rd,
   for (int s = tid; s < p.num_rows; s += nt) {
     const int c = rc[s], d = rd[s];
     if (d <= 1) continue;
-    const int np = row_items(true, c, d, 128 / p.G, 1u), n_kt = chunk_parts(c, d, 1);
+    const int np = row_items(true, c, d, 128 / p.G, 1u), n_kt = parts_of<Span>(p, c, d, 128 / p.G, 1);
     pairs += np;
     tiles += static_cast<int64_t>(np) * n_kt;
     longest = max(longest, n_kt);
@@ -457,8 +533,9 @@ __device__ __forceinline__ void header_bad_meta(int32_t* hdr) {
 // The prologue of a step of at most 32 rows: one warp, a row per lane, with
 // ballots and shuffles in place of shared memory and barriers.  Same outputs
 // as the block version below.
-template <bool Teams>
+template <bool Teams, bool Span>
 __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
+  constexpr bool Parts = Teams || Span;
   const int lane = threadIdx.x, S = p.num_rows;
   int32_t* hdr = p.hdr;
   const int measured_mhz = hdr[H_CLOCK_MHZ];  // loaded beside the row metadata
@@ -467,9 +544,11 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   if (lane < S) {
     const int32_t a = p.cu[lane], b = p.cu[lane + 1];
     d = static_cast<int32_t>(static_cast<uint32_t>(b) - static_cast<uint32_t>(a));  // checked below
-    c = p.q_start[lane];
     ctx = p.ctx_lens[lane];
-    ok = a >= 0 && b >= a && b <= p.num_tokens && c >= 0 && static_cast<int64_t>(ctx) == static_cast<int64_t>(c) + d;
+    const bool fixed = Span && p.fixed_span;
+    c = fixed ? ctx - 1 : p.q_start[lane];
+    ok = a >= 0 && b >= a && b <= p.num_tokens &&
+         (fixed ? ctx >= 0 : c >= 0 && static_cast<int64_t>(ctx) == static_cast<int64_t>(c) + d);
     if (p.bt_off != nullptr) {
       const int64_t o0 = p.bt_off[lane], o1 = p.bt_off[lane + 1];
       ok = ok && o0 >= 0 && o1 <= p.bt_len && cdiv64(ctx, kPage) <= o1 - o0;
@@ -485,7 +564,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     return;
   }
   const bool is_dec = d == 1, is_ch = d > 1;
-  const int64_t dec_pages = warp_sum31(is_dec ? (ctx + kPage - 1) / kPage : 0);
+  const int64_t dec_pages = warp_sum31(is_dec ? dec_pages_of<Span>(p, ctx) : 0);
   const int tpt = 128 / p.G;
   const unsigned bd = __ballot_sync(0xffffffffu, is_dec), bc = __ballot_sync(0xffffffffu, is_ch);
   const int n_dec = __popc(bd), n_ch = __popc(bc);
@@ -499,7 +578,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const bool listed = is_dec || is_ch;
   const unsigned list = is_ch ? bc : bd;
   const int pos = __popc(list & ((1u << lane) - 1u));
-  const uint32_t key = order_key(is_ch ? 0.5f * d * (2.f * c + d + 1.f) : c + 1.f, pos);
+  const uint32_t key = order_key(cost_of<Span>(p, is_ch, static_cast<float>(c), static_cast<float>(d)), pos);
   s_key[0][lane] = 0;
   s_key[1][lane] = 0;
   s_items[lane] = 0;
@@ -514,11 +593,12 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
   }
   int part_tiles = 0, parts = 1;
-  int items = listed ? row_items(is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
-  if (Teams && 2 * n_ch * p.H_kv < p.num_sms &&  // the least that chunk_part_tiles needs
-      __reduce_max_sync(0xffffffffu, is_ch ? ctx : 0) > kMinPartedTiles * kChunkTile) {
-    part_tiles = plan_parts_warp(p, is_ch ? ctx : 0, is_ch ? items : 0, dec_pages);
-    if (part_tiles > 0 && is_ch) items *= parts = chunk_parts(c, d, part_tiles);
+  int items = listed ? items_of<Span>(p, is_ch, c, d, tpt, static_cast<unsigned>(split)) : 0;
+  const int ch_keys = !is_ch ? 0 : Span ? span_keys(p, c, d, tpt) : ctx;  // keys of the row's longest pair
+  if (Parts && 2 * n_ch * p.H_kv < p.num_sms &&  // the least that chunk_part_tiles needs
+      __reduce_max_sync(0xffffffffu, ch_keys) > kMinPartedTiles * kChunkTile) {
+    part_tiles = plan_parts_warp(p, ch_keys, is_ch ? items : 0, dec_pages);
+    if (part_tiles > 0 && is_ch) items *= parts = parts_of<Span>(p, c, d, tpt, part_tiles);
   }
   const int q = (is_ch ? n_dec : 0) + rank;  // queue position
   if (listed) s_items[q] = items;
@@ -542,10 +622,10 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
   const bool ch_over = n_ch_items > (part_tiles > 0 ? p.ch_cap : p.max_ch_items);
   const int64_t tiles =
-      warp_sum31(is_ch ? static_cast<int>(min(static_cast<int64_t>(chunk_tiles(c, d, tpt)) * p.H_kv,
+      warp_sum31(is_ch ? static_cast<int>(min(static_cast<int64_t>(tiles_of<Span>(p, c, d, tpt)) * p.H_kv,
                                                 int64_t{0x7fffffff}))
                        : 0);
-  const int64_t chunk_keys = warp_sum31(is_ch ? ctx : 0);
+  const int64_t chunk_keys = warp_sum31(!is_ch ? 0 : Span ? ctx - span_first(p, c) : ctx);
   if (is_dec) {
     p.dec_rows[rank] = lane;
     p.dec_part_base[rank] = static_cast<int32_t>(static_cast<int64_t>(before) * p.H_q);
@@ -564,7 +644,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const int src = __ffs(pend) - 1;
     const int r_rank = __shfl_sync(0xffffffffu, rank, src), r_items = __shfl_sync(0xffffffffu, items, src);
     const int r_before = __shfl_sync(0xffffffffu, before, src);
-    if (Teams && part_tiles > 0) {
+    if (Parts && part_tiles > 0) {
       chunk_part_table(p, (r_before - dec_tot) * p.H_kv, r_rank, r_items, __shfl_sync(0xffffffffu, parts, src), sp.head_major,
                        lane);
       continue;
@@ -588,10 +668,8 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_DEC_CTR] = 0;
     hdr[H_CH_CTR] = 0;
     hdr[H_SPLIT] = split;
-    if (Teams) {
-      hdr[H_TEAM] = plan.team;
-      hdr[H_CH_TILES] = part_tiles;
-    }
+    if (Teams) hdr[H_TEAM] = plan.team;
+    if (Parts) hdr[H_CH_TILES] = part_tiles;
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -606,8 +684,9 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
 // memory).  It runs once per step from a cold instruction cache, so its loops
 // stay rolled and its code short.  It reads only the row metadata, never the
 // appended K/V, so it may run alongside the append.
-template <bool Teams>
+template <bool Teams, bool Span = false>
 __device__ __forceinline__ void prologue_body(const AttnParams& p) {
+  constexpr bool Parts = Teams || Span;
   extern __shared__ __align__(16) int32_t psm[];
   __shared__ int s_warp[32];
   __shared__ long long s_sum[3][32];
@@ -627,7 +706,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   // (ahead of every status write of this call, all of which come after a barrier or from this thread)
   if (tid == 0 && p.clear_status) hdr[H_STATUS] = 0;
   if (S <= 32) {
-    if (warp == 0) prologue_warp<Teams>(p);
+    if (warp == 0) prologue_warp<Teams, Span>(p);
     return;
   }
   if (tid == 0) s_tiles = 0;
@@ -639,9 +718,11 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   for (int s = tid; s < S; s += nt) {
     const int32_t a = p.cu[s], b = p.cu[s + 1];
     const int32_t d = static_cast<int32_t>(static_cast<uint32_t>(b) - static_cast<uint32_t>(a));  // checked below
-    const int32_t c = p.q_start[s], ctx = p.ctx_lens[s];
+    const bool fixed = Span && p.fixed_span;
+    const int32_t ctx = p.ctx_lens[s], c = fixed ? ctx - 1 : p.q_start[s];
     // d == 0 is a pad row: valid, and neither a decode nor a chunk
-    bool ok = a >= 0 && b >= a && b <= p.num_tokens && c >= 0 && static_cast<int64_t>(ctx) == static_cast<int64_t>(c) + d;
+    bool ok = a >= 0 && b >= a && b <= p.num_tokens &&
+              (fixed ? ctx >= 0 : c >= 0 && static_cast<int64_t>(ctx) == static_cast<int64_t>(c) + d);
     if (p.bt_off != nullptr) {  // the row's pages must lie inside the table
       const int64_t o0 = p.bt_off[s], o1 = p.bt_off[s + 1];
       ok = ok && o0 >= 0 && o1 <= p.bt_len && cdiv64(ctx, kPage) <= o1 - o0;
@@ -656,11 +737,11 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       my_dec += d == 1;
       my_ch += d > 1;
       if (d == 1) {
-        const unsigned n = static_cast<unsigned>(ctx + kPage - 1) / kPage;
+        const unsigned n = Span ? static_cast<unsigned>(span_pages(p, ctx)) : static_cast<unsigned>(ctx + kPage - 1) / kPage;
         my_pages += n;
         my_max = max(my_max, n);
       }
-      if (d > 1) my_ch_keys += ctx;
+      if (d > 1) my_ch_keys += Span ? ctx - span_first(p, c) : ctx;
     }
   }
   my_ctx = warp_sum64(my_ctx);
@@ -695,9 +776,9 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   // 2. decode split size
   const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
   const int split = plan.split;
-  const int part_tiles = Teams && 2 * n_ch * p.H_kv < p.num_sms && chunk_keys > kMinPartedTiles * kChunkTile &&
+  const int part_tiles = Parts && 2 * n_ch * p.H_kv < p.num_sms && chunk_keys > kMinPartedTiles * kChunkTile &&
                                  (p.cu[S] - n_dec) / 128 * p.G * p.H_kv < p.num_sms  // the least that it needs
-                             ? plan_parts_block(p, rd, rc, dec_pages) : 0;
+                             ? plan_parts_block<Span>(p, rd, rc, dec_pages) : 0;
   const int tpt = 128 / p.G;
   const unsigned split32 = static_cast<unsigned>(split);
   // 3. the two lists in input order: decode rows at lst[0, n_dec), chunk rows after them
@@ -726,7 +807,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     const bool ch = j >= n_dec;
     const int pos = ch ? j - n_dec : j, row = lst[j];
     const float d = static_cast<float>(rd[row]), c = static_cast<float>(rc[row]);
-    key[(ch ? ch_base : 0) + pos] = order_key(ch ? 0.5f * d * (2.f * c + d + 1.f) : c + 1.f, pos);
+    key[(ch ? ch_base : 0) + pos] = order_key(cost_of<Span>(p, ch, c, d), pos);
   }
   __syncthreads();
   // 5. each list longest first: a row's rank is the number of larger keys in its
@@ -748,8 +829,8 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     }
     const int row = lst[j], c = rc[row], d = rd[row];
     (ch ? p.ch_rows : p.dec_rows)[rank] = row;
-    pref[(ch ? n_dec : 0) + rank] = row_items(ch, c, d, tpt, split32) * (Teams && ch && part_tiles > 0 ? chunk_parts(c, d, part_tiles) : 1);
-    if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(chunk_tiles(c, d, tpt)) * p.H_kv);
+    pref[(ch ? n_dec : 0) + rank] = items_of<Span>(p, ch, c, d, tpt, split32) * (Parts && ch && part_tiles > 0 ? parts_of<Span>(p, c, d, tpt, part_tiles) : 1);
+    if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(tiles_of<Span>(p, c, d, tpt)) * p.H_kv);
   }
   __syncthreads();
   // 6. exclusive prefix of the item counts in queue order (decode rows, then chunk rows)
@@ -796,9 +877,9 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   __syncthreads();
   for (int q = n_dec + warp; q < n_tot && !ch_over; q += nw) {
     const int np = pref[q + 1] - pref[q];
-    if (Teams && part_tiles > 0) {
+    if (Parts && part_tiles > 0) {
       const int row = p.ch_rows[q - n_dec];
-      chunk_part_table(p, (pref[q] - dec_tot) * p.H_kv, q - n_dec, np, chunk_parts(rc[row], rd[row], part_tiles),
+      chunk_part_table(p, (pref[q] - dec_tot) * p.H_kv, q - n_dec, np, parts_of<Span>(p, rc[row], rd[row], tpt, part_tiles),
                        s_split.head_major, lane);
       continue;
     }
@@ -823,10 +904,8 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_DEC_CTR] = 0;
       hdr[H_CH_CTR] = 0;
       hdr[H_SPLIT] = static_cast<int32_t>(split);
-      if (Teams) {
-        hdr[H_TEAM] = plan.team;
-        hdr[H_CH_TILES] = part_tiles;
-      }
+      if (Teams) hdr[H_TEAM] = plan.team;
+      if (Parts) hdr[H_CH_TILES] = part_tiles;
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }
@@ -836,10 +915,10 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
 // kernel before it on the stream (normally the append): it runs alongside that
 // kernel and waits for it before it exits, so the kernel after it sees the
 // append's writes.
-template <bool Teams>
+template <bool Teams, bool Span>
 __global__ void __launch_bounds__(1024, 1) prologue_kernel(AttnParams p) {
   griddep_launch_dependents();
-  prologue_body<Teams>(p);
+  prologue_body<Teams, Span>(p);
   griddep_wait();
 }
 
@@ -985,6 +1064,15 @@ inline size_t parts_total(int64_t max_tokens, int64_t H_q, int64_t H_kv, int64_t
   return align_up(kPartItems * part_bytes(part_rows(max_tokens, H_q / H_kv), D), 256);
 }
 
+// The room of a call for parts: what its workspace has behind the layout.
+inline void set_parts_room(AttnParams* p, void* workspace, size_t ws_bytes, int64_t context_total) {
+  const size_t used = align_up(ws_layout(p->num_rows, p->num_tokens, context_total, p->H_q, p->H_kv, p->D).total, 256);
+  p->ch_parts = static_cast<uint8_t*>(workspace) + used;
+  p->ch_rec = part_rows(p->num_tokens, p->G);
+  const int64_t cap = ws_bytes > used ? static_cast<int64_t>((ws_bytes - used) / part_bytes(p->ch_rec, p->D)) : 0;
+  p->ch_cap = p->num_tokens < 2 ? 0 : cap > p->num_sms ? p->num_sms : static_cast<int32_t>(cap);
+}
+
 std::atomic<int> g_num_sms[kMaxDevices];
 
 inline int num_sms() {
@@ -1125,6 +1213,9 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.kv_q4 = nullptr;
   p.force_chunk_ctas = -1;
   p.ch_cap = 0;
+  p.sinks = nullptr;
+  p.window = INT32_MAX;
+  p.fixed_span = 0;
   if (device_rates(&p.sm_mhz, &p.hbm_gbs, &p.l2_bytes) != MS_OK) return MS_ERR_CUDA;
   return MS_OK;
 }
@@ -1132,12 +1223,12 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
 // The prologue as its own kernel, a programmatic dependent of the kernel
 // before it: about a thread per row (one warp up to 32 rows, else at least a
 // warp per scheduler).
-template <bool Teams>
+template <bool Teams, bool Span = false>
 int launch_prologue(const AttnParams& p, cudaStream_t st) {
-  if (ensure_smem_limit(prologue_kernel<Teams>, 8, prologue_words(kMaxRows) * 4) != MS_OK) return MS_ERR_CUDA;
+  if (ensure_smem_limit(prologue_kernel<Teams, Span>, 8, prologue_words(kMaxRows) * 4) != MS_OK) return MS_ERR_CUDA;
   const int S = p.num_rows;
   const int threads = S <= 32 ? 32 : S >= 1024 ? 1024 : S <= 128 ? 128 : (S + 31) / 32 * 32;
-  return launch_dependent(prologue_kernel<Teams>, dim3(1), dim3(threads), prologue_words(S) * 4, st, p) == cudaSuccess
+  return launch_dependent(prologue_kernel<Teams, Span>, dim3(1), dim3(threads), prologue_words(S) * 4, st, p) == cudaSuccess
              ? MS_OK
              : MS_ERR_CUDA;
 }

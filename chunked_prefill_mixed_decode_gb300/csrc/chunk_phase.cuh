@@ -38,12 +38,22 @@ struct ChItem {
   int t0[2];    // per Q tile: index of its first KV tile among all tiles its softmax group ran
 };
 
-// Part of an item (4-bit pools): of how many it is which, the place of the first,
-// and the parity of this one among the parts of each softmax group.  The item's c
-// and kv_end then count from the part's first key, and n_kt and nkt are the part's
-// own; ns == 1: the whole item.
+// What the keys of an item are.
+enum ChKind {
+  kCausal = 0,  // bf16 pools, keys 0..p
+  kQ4 = 1,      // a 4-bit pool, keys 0..p
+  kSpan = 2     // bf16 pools, the last keys up to p or a fixed run of keys (AttnParams::window)
+};
+
+// Part of an item (4-bit pools, spans): of how many it is which, the place of the
+// first, and the parity of this one among the parts of each softmax group.  The
+// item's c and kv_end then count from the part's first key, and n_kt and nkt are the
+// part's own; ns == 1: the whole item.  Spans: also the row's key that the item's
+// first tile starts at (c stays the row's own), the first of those tiles that each
+// Q tile sees, and how many of the first tile's keys no query of the pair sees.
 struct ChPart {
   int ns, part, item0, parity[2];
+  int key0, first[2], unseen;
 };
 
 constexpr int kRawStages = 3;  // tiles of 4-bit pages on their way to the dequantizing warps
@@ -72,7 +82,7 @@ static_assert(ChCfg<128>::SMEM <= 232448 && ChCfg<64>::SMEM <= 232448,
               "chunk phase exceeds the per-CTA shared-memory limit");
 static_assert(ChCfg<128>::KVS <= 8 && ChCfg<64>::KVS <= 8, "more K/V stages than barriers");
 
-// Over a 4-bit pool, by one thread once every warp has left the phase: Q tiles that
+// With parts, by one thread once every warp has left the phase: Q tiles that
 // a phase given up early still has in flight land, and its barriers, up to `last`,
 // are invalidated.  (Here and not at the producer's end, where the loops of the phase
 // pay for it in registers: 516 -> 519.6 us, two chunks of 3968 tokens.  The bf16 phase
@@ -240,7 +250,7 @@ __device__ __forceinline__ bool dequant_role(uint8_t* smem, ChBars* bars, const 
 // to a row and a quarter of its 16-byte columns to a lane, so that 8 KB (D = 128)
 // are asked for at once; a row to a warp waits for each row's records in turn (40 us instead of 7
 // for two parts of 128 rows).
-template <int D, int G>
+template <int D, int G, int Kind>
 __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& it, const ChPart& pt, int t, int w, int lane) {
   constexpr int E = D / 16;  // 16-byte columns to a lane
   const int rows = it.ntok[t] * G, ns = pt.ns, q = lane & 3;
@@ -253,6 +263,13 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& i
 #pragma unroll 8
     for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(cp.ml + first + static_cast<int64_t>(i) * p.ch_rec).x);
     float L = 0.f, o[4 * E];
+    if constexpr (Kind == kSpan) {
+      if (p.sinks != nullptr) {
+        const float sink = sink_log2(p, it.hk * G + row % G);
+        M = fmaxf(M, sink);
+        L = ex2(sink - M);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4 * E; ++j) o[j] = 0.f;
 #pragma unroll 1
@@ -283,7 +300,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& i
       }
     }
     if (valid) {
-      const float inv = 4.f / L;  // the records hold quarters
+      const float inv = (Kind == kQ4 ? 4.f : 1.f) / L;  // over a 4-bit pool the records hold quarters
       bf16* dst = p.out + (static_cast<int64_t>(it.tb + it.tok0[t] + row / G) * p.H_q + it.hk * G + row % G) * D;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -296,10 +313,20 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& i
   }
 }
 
+// Zeros for the queries of an item whose row has no keys, by one warp.
+template <int D, int G>
+__device__ __forceinline__ void zero_rows(const AttnParams& p, const ChItem& it, int lane) {
+  constexpr int W = G * D / 8;  // 16-byte words to a token
+  for (int i = lane; i < (it.ntok[0] + it.ntok[1]) * W; i += 32) {
+    const int64_t tok = it.tb + it.tok0[0] + i / W;
+    *reinterpret_cast<uint4*>(p.out + (tok * p.H_q + it.hk * G) * D + i % W * 8) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // The end of a part for the four warps of group t: each row's reference maximum
 // (log2 units), sum and O as it is in TMEM into the part's records; the last part
 // of the item to get here joins them all.  False when a wait gave up.
-template <int D, int G>
+template <int D, int G, int Kind>
 __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slot, int t, float m, float l, uint32_t tO,
                                       const volatile int* abort_flag, uint64_t lim) {
   const ChItem& it = bars->items[slot];
@@ -336,7 +363,7 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
   if (!warp_wait_fast(&bars->part_last[t], pt.parity[t], abort_flag, lim)) return false;
   if (bars->last[t]) {
     __threadfence();
-    merge_parts<D, G>(p, it, pt, t, quad, lane);
+    merge_parts<D, G, Kind>(p, it, pt, t, quad, lane);
   }
   return true;
 }
@@ -371,11 +398,12 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
 // the ring (740 us); where items are few, one Q tile for both softmax groups, every
 // other K/V tile each (a 512-token chunk alone 58 -> 54 us, beside 64 decodes
 // 78 -> 94, and the branches cost the long chunks 4 %).
-template <int D, int G, bool Q4 = false>
+template <int D, int G, int Kind = kCausal>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
                                             const AttnParams& p, uint8_t* smem, uint32_t tmem) {
   using C = ChCfg<D>;
+  constexpr bool Q4 = Kind == kQ4, Span = Kind == kSpan, Parts = Q4 || Span;
   constexpr int NSL = C::NSL;
   constexpr int TPT = 128 / G;  // query tokens per 128-row Q tile
   constexpr int KVS = C::KVS;
@@ -422,13 +450,13 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         mbar_init(&bars->raw_full[i], 1);
         mbar_init(&bars->raw_empty[i], kDequantWarps);
       }
-    if constexpr (Q4)
+    if constexpr (Parts)
       for (int t = 0; t < 2; ++t) {
         mbar_init(&bars->part_done[t], 128);
         mbar_init(&bars->part_last[t], 1);
       }
     bars->abort = 0;
-    if constexpr (Q4) bars->q_asked = 0;
+    if constexpr (Parts) bars->q_asked = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -439,15 +467,28 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   // 3968 tokens at 0 and 6000, 32 / 8 heads.  Over a bf16 pool, where the same change
   // measures 522 -> 527 us there and 2060 -> 2110 us beside long decodes (and 69 -> 61 us
   // for D = 64), lane 0 runs it alone.
-  auto one = [&] { return !Q4 || elect_one(); };
+  constexpr bool Elect = Q4;
+  auto one = [&] { return !Elect || elect_one(); };
   auto join = [&] {
-    if constexpr (Q4) __syncwarp();
+    if constexpr (Elect) __syncwarp();
   };
   auto issue_wait = [&](uint64_t* bar, uint32_t parity) {
-    return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait_fast(bar, parity, abort_flag, 16, lim);
+    return Elect ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait_fast(bar, parity, abort_flag, 16, lim);
   };
   auto issue_wait_item = [&](uint64_t* bar, uint32_t parity) {
-    return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait(bar, parity, abort_flag, lim);
+    return Elect ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait(bar, parity, abort_flag, lim);
+  };
+  // rows lo .. hi - 1 of V stage bv, by the PV issuer
+  auto zero_v = [&](int bv, int lo, int hi) {
+    uint8_t* v0 = smem + v_off(bv);
+    constexpr int W = NSL * 8;  // 16-byte words to a row
+    for (int i = lo * W + (Elect ? lane : 0); i < hi * W; i += Elect ? 32 : 1) {
+      const int r = i / W;
+      *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + (i % W >> 3) * 2048 + (r & 15) * 128 + (i & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    join();
   };
   auto softmax_wait = [&](uint64_t* bar, uint32_t parity) {
     return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : warp_wait(bar, parity, abort_flag, lim);
@@ -501,7 +542,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
       return true;
     };
-    const int part_tiles = Q4 ? p.hdr[H_CH_TILES] : 0;
+    const int part_tiles = Parts ? p.hdr[H_CH_TILES] : 0;
     int kt0 = 0;                // the part's first KV tile
     int parts_run[2] = {0, 0};  // parts run by each softmax group so far
     while (ok) {
@@ -518,12 +559,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       it.row = -1;
       if (item < n_items) {
         // (chunk row index and, above it, the part; KV head << 16 | pair from the last)
-        const int2 kl = __ldg((Q4 && part_tiles > 0 ? ChunkParts(p).items : p.ch_items) + item);
-        const int k = Q4 ? kl.x & 0xffff : kl.x;
+        const int2 kl = __ldg((Parts && part_tiles > 0 ? ChunkParts(p).items : p.ch_items) + item);
+        const int k = Parts ? kl.x & 0xffff : kl.x;
         it.row = __ldg(p.ch_rows + k);
         it.tb = __ldg(p.cu + it.row);
         const int d = __ldg(p.cu + it.row + 1) - it.tb;
-        it.c = __ldg(p.q_start + it.row);
+        it.c = Span ? span_start(p, it.row) : __ldg(p.q_start + it.row);
         const int n_qt = (d + TPT - 1) / TPT;
         const int n_pair = (n_qt + 1) >> 1;
         // the prologue ordered the row's items (KV head by KV head, or longest pair
@@ -536,13 +577,54 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           const bool has = qt < n_qt;
           it.tok0[t] = has ? qt * TPT : 0;
           it.ntok[t] = has ? min(TPT, d - qt * TPT) : 0;
-          it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
+          if constexpr (Span) {
+            // the pair's keys from the page that holds its first query's first key
+            const int lo = span_first(p, it.c + (p.fixed_span ? 0 : it.tok0[t]));
+            if (t == 0) pt.key0 = lo & ~(kPage - 1);
+            if (t == 0) pt.unseen = lo - pt.key0;
+            pt.first[t] = (lo - pt.key0) / kKeys;
+            it.kv_end[t] = has ? it.c + (p.fixed_span ? 1 : it.tok0[t] + it.ntok[t]) - pt.key0 : 0;
+          } else {
+            it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
+          }
           it.nkt[t] = (it.kv_end[t] + kKeys - 1) / kKeys;
-          if constexpr (!Q4) {
+          if constexpr (!Parts) {
             it.t0[t] = t_run[t];
             t_run[t] += it.nkt[t];
           }
           it.n_kt = max(it.n_kt, it.nkt[t]);
+        }
+        if constexpr (Span) {
+          pt.ns = 1;
+          kt0 = 0;
+          if (it.n_kt == 0) {  // a row without keys: zeros, by this warp
+            if (part_tiles == 0 || (kl.x >> 16) == 0) zero_rows<D, G>(p, it, lane);
+            continue;
+          }
+          int n = it.n_kt;  // tiles of the part, or of the whole item
+          if (part_tiles > 0) {
+            const int ns_row = span_parts(p, it.c, d, TPT, part_tiles);
+            n = (it.n_kt + ns_row - 1) / ns_row;
+            pt.ns = (it.n_kt + n - 1) / n;
+            pt.part = kl.x >> 16;
+            pt.item0 = item - pt.part;
+            if (pt.part >= pt.ns) continue;  // another pair of the row has more tiles
+            kt0 = pt.part * n;
+            pt.key0 += kt0 * kKeys;
+            if (kt0 > 0) pt.unseen = 0;
+          }
+          it.n_kt = 0;
+          for (int t = 0; t < 2; ++t) {
+            it.kv_end[t] = it.ntok[t] > 0 ? it.kv_end[t] - kt0 * kKeys : 0;
+            pt.first[t] = max(0, pt.first[t] - kt0);
+            const int end = it.kv_end[t] > 0 ? min(n, (it.kv_end[t] + kKeys - 1) / kKeys) : 0;
+            it.nkt[t] = max(0, end - pt.first[t]);
+            it.n_kt = max(it.n_kt, end);
+            pt.parity[t] = parts_run[t] & 1;
+            parts_run[t] += pt.ns > 1 && it.ntok[t] > 0;
+            it.t0[t] = t_run[t];
+            t_run[t] += it.nkt[t];
+          }
         }
         if constexpr (Q4) {
           pt.ns = 1;
@@ -573,7 +655,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
       if (lane == 0) {
         bars->items[slot] = it;
-        if constexpr (Q4) bars->parts[slot] = pt;
+        if constexpr (Parts) bars->parts[slot] = pt;
         mbar_arrive(&bars->item_full[slot]);
       }
       ++n_done;
@@ -586,7 +668,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       const int nq = it.ntok[1] > 0 ? 2 : 1;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
-        if constexpr (Q4) bars->q_asked = n_done;
+        if constexpr (Parts) bars->q_asked = n_done;
       }
       __syncwarp();
       if (lane < nq * NSL) {
@@ -595,7 +677,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
                     &bars->q_full);
       }
       const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-      const int32_t* btrow = row_table(p, it.row) + (Q4 ? kt0 * kTilePages : 0);
+      const int32_t* btrow = row_table(p, it.row) + (Q4 ? kt0 * kTilePages : Span ? pt.key0 / kPage : 0);
       const int n_pages = (kv_max + kPage - 1) / kPage;
       // lane L < 4 holds the page id of page L of the current tile; the next tile's is in flight
       int pg_cur = lane < kTilePages && lane < n_pages ? __ldg(btrow + lane) : 0;
@@ -681,7 +763,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     // a k-step or a stage only moves the descriptor's start-address field
     // (bytes >> 4, 14 bits, no carry below 256 KB) by a constant.
     const int t = warp == 1 ? 0 : 1;
-    if (Q4 || lane == 0) {
+    if (Elect || lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(sbase + C::Q_OFF + t * C::Q_BYTES, 16, 1024);
       const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, 1024);
       const uint32_t s_tm = tmem + C::S_COL + 2 * t * 64;
@@ -698,9 +780,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const ChItem& it = bars->items[slot];  // stable until this role arrives on item_empty
         const int row = it.row;
         if (row < 0) break;
-        const int nkt = it.nkt[t], t0 = it.t0[t], n_kt = it.n_kt;
+        const int first = Span ? bars->parts[slot].first[t] : 0;  // of the tiles that the Q tile sees
+        const int end = first + it.nkt[t], t0 = it.t0[t] - first, n_kt = it.n_kt;
         const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-        if ((Q4 || nkt > 0) && !issue_wait_item(&bars->q_full, n & 1)) {
+        if ((Parts || end > 0) && !issue_wait_item(&bars->q_full, n & 1)) {
           ok = false;
           break;
         }
@@ -709,7 +792,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             ok = false;
             break;
           }
-          if (kt < nkt) {
+          if (kt < end && (!Span || kt >= first)) {
             const int gt = t0 + kt, b = gt & 1;
             // S buffer b last held P of the group's tile gt - 2: its PV MMA must be done
             if (gt >= 2 && !issue_wait(&bars->o_done[t][b], ((gt - 2) >> 1) & 1)) {
@@ -755,7 +838,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     }
   } else if (warp == 3 + kSoftmaxWarps) {
     // ---------------------------------------------------------------- PV issuer of both groups
-    if (Q4 || lane == 0) {
+    if (Elect || lane == 0) {
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
       // V is the MN-major B operand, one page per k-step of 16 keys: the page's
       // 64-column slabs 2048 B apart (LBO), its two 8-key row groups 1024 B apart
@@ -774,7 +857,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const int row = it.row;
         if (row < 0) break;
         const int n_kt = it.n_kt;
-        const int nkt_[2] = {it.nkt[0], it.nkt[1]}, t0_[2] = {it.t0[0], it.t0[1]};
+        const ChPart& pt = bars->parts[slot];
+        const int first_[2] = {Span ? pt.first[0] : 0, Span ? pt.first[1] : 0}, unseen = Span ? pt.unseen : 0;
+        const int end_[2] = {first_[0] + it.nkt[0], first_[1] + it.nkt[1]};
+        const int t0_[2] = {it.t0[0] - first_[0], it.t0[1] - first_[1]};
         const int ke_[2] = {it.kv_end[0], it.kv_end[1]};
         const int kv_max = max(ke_[0], ke_[1]);
         for (int j = 0; j < n_kt && ok; ++j) {
@@ -783,24 +869,14 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             break;
           }
           const int keys = min(kKeys, kv_max - j * kKeys);  // keys loaded in this tile
-          if (!Q4 && (keys & 15) != 0) {
-            // rows past the context in the last page may hold stale (even non-finite)
-            // data: zero them in V so that P = 0 times V stays 0
-            if (one()) {
-              uint8_t* v0 = smem + v_off(bv);
-              for (int r = keys; r < ((keys + 15) & ~15); ++r)
-                for (int s = 0; s < NSL; ++s)
-                  for (int q16 = 0; q16 < 8; ++q16)
-                    *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + s * 2048 + (r & 15) * 128 + q16 * 16) =
-                        make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
-            }
-            join();
-          }
+          // rows past the context in the last page may hold stale (even non-finite)
+          // data: zero them in V so that P = 0 times V stays 0
+          if (!Q4 && (keys & 15) != 0) zero_v(bv, keys, (keys + 15) & ~15);
+          if (Span && j == 0 && unseen > 0) zero_v(bv, 0, unseen);  // and those in front of every query's window
           const uint64_t vd = vdesc0 + static_cast<uint64_t>((bv * 2 * NSL * kKVSlab) >> 4);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (j < nkt_[t]) {
+            if (j < end_[t] && (!Span || j >= first_[t])) {
               const int gt = t0_[t] + j, b = gt & 1;
               if (!issue_wait(&bars->p_full[t][b], (gt >> 1) & 1)) {
                 ok = false;
@@ -815,12 +891,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
 #pragma unroll
                   for (int kk = 0; kk < kKeys / 16; ++kk)
                     mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                                (j > first_[t] || kk > 0) ? 1u : 0u);
                 } else {
                   const int nk_t = (kr + 15) >> 4;
                   for (int kk = 0; kk < nk_t; ++kk)
                     mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                                (j > first_[t] || kk > 0) ? 1u : 0u);
                 }
                 mma_commit(&bars->o_done[t][b]);
               }
@@ -870,13 +946,29 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       if (nkt > 0) {
         const int tl = it.tok0[t] + r / G;  // token of this row within the chunk
         const bool valid = (r / G) < it.ntok[t];
-        const int pos = it.c + (valid ? tl : it.tok0[t] + it.ntok[t] - 1);
-        const int warp_min_pos = it.c + it.tok0[t] + (quad * 32) / G;  // smallest position of this warp's rows
+        int pos = it.c + (valid ? tl : it.tok0[t] + it.ntok[t] - 1);
+        int warp_min_pos = it.c + it.tok0[t] + (quad * 32) / G;  // smallest position of this warp's rows
         // (a row may see no key of its part: from the lowest finite number its masked
         // scores have weight 0)
-        float m_use = Q4 ? -FLT_MAX : -INFINITY, l = 0.f;
-        for (int kt = 0; kt < nkt; ++kt) {
-          const int gt = it.t0[t] + kt, b = gt & 1;
+        float m_use = Parts ? -FLT_MAX : -INFINITY, l = 0.f;
+        int first = 0, lo = 0, warp_max_lo = 0;  // spans: the Q tile's first tile, this row's first key, the warp's last one
+        if constexpr (Span) {
+          const ChPart& pt = bars->parts[slot];
+          first = pt.first[t];
+          const int warp_max_tok = min((quad * 32 + 31) / G, it.ntok[t] - 1);
+          if (p.fixed_span) pos = warp_min_pos = it.c;
+          lo = span_first(p, pos) - pt.key0;
+          warp_max_lo = span_first(p, it.c + (p.fixed_span ? 0 : it.tok0[t] + warp_max_tok)) - pt.key0;
+          pos -= pt.key0;
+          warp_min_pos -= pt.key0;
+          if (p.sinks != nullptr && pt.ns == 1) {  // with parts their join adds it
+            const float sink = sink_log2(p, it.hk * G + r % G);
+            l = sink > -FLT_MAX ? 1.f : 0.f;
+            m_use = fmaxf(sink, -FLT_MAX);
+          }
+        }
+        for (int kt = first; kt < first + nkt; ++kt) {
+          const int gt = it.t0[t] + kt - first, b = gt & 1;
           if (!softmax_wait(&bars->s_full[t][b], (gt >> 1) & 1)) {
             ok = false;
             break;
@@ -900,6 +992,11 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
 #pragma unroll
             for (int j = 0; j < 64; ++j)
               if (key0 + j > pos) sv[j] = -INFINITY;
+          }
+          if (Span && key0 < warp_max_lo) {  // the window's lower edge
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (key0 + j < lo) sv[j] = -INFINITY;
           }
           // row max: four chains of three-input maxima
           float mxa[4];
@@ -940,7 +1037,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             pw[j] = *reinterpret_cast<uint32_t*>(&h2);
           }
           tmem_st32u(ts, pw);
-          if (kt > 0 && __any_sync(0xffffffffu, grow)) {  // rescale this row's O
+          if (kt > first && __any_sync(0xffffffffu, grow)) {  // rescale this row's O
             // the PV MMA of the previous tile must be done with O first
             if (!softmax_wait(&bars->o_done[t][(gt - 1) & 1], ((gt - 1) >> 1) & 1)) {
               ok = false;
@@ -969,12 +1066,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           break;
         }
         tc_fence_after();
-        if (Q4 && bars->parts[slot].ns > 1) {
-          ok = end_part<D, G>(p, bars, slot, t, m_use, l, tO, abort_flag, lim);
+        if (Parts && bars->parts[slot].ns > 1) {
+          ok = end_part<D, G, Kind>(p, bars, slot, t, m_use, l, tO, abort_flag, lim);
         } else {
           const float inv = (Q4 ? 4.f : 1.f) / l;
-          const bool valid_row = Q4 ? r / G < it.ntok[t] : valid;  // read again: a register less in the loop
-          bf16* dst = p.out + (static_cast<int64_t>(it.tb + (Q4 ? it.tok0[t] + r / G : tl)) * p.H_q + it.hk * G + r % G) * D;
+          const bool valid_row = Parts ? r / G < it.ntok[t] : valid;  // read again: a register less in the loop
+          bf16* dst = p.out + (static_cast<int64_t>(it.tb + (Parts ? it.tok0[t] + r / G : tl)) * p.H_q + it.hk * G + r % G) * D;
 #pragma unroll
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t rr[32];
@@ -1002,10 +1099,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             }
           }
         }
-      } else if (Q4 && bars->parts[slot].ns > 1 && it.ntok[t] > 0) {  // the part's keys come after all of the tile's tokens
-        ok = end_part<D, G>(p, bars, slot, t, -FLT_MAX, 0.f, tO, abort_flag, lim);
+      } else if (Parts && bars->parts[slot].ns > 1 && it.ntok[t] > 0) {  // no key of the part is one of the tile's
+        ok = end_part<D, G, Kind>(p, bars, slot, t, -FLT_MAX, 0.f, tO, abort_flag, lim);
       }
-      if (Q4 && !ok) break;
+      if (Parts && !ok) break;
       // O has been read: the next item's first PV may overwrite it
       tc_fence_before();
       mbar_arrive(&bars->item_empty[slot]);

@@ -10,8 +10,8 @@ from __future__ import annotations
 
 import time
 
-from . import Engine, StepGraph, attention_workspace_size, mixed_step, read_status
-from .step import MetaStager, run_step_q4
+from . import Engine, StepGraph, attention_workspace_size, read_status
+from .step import MetaStager, run_step, run_step_q4
 
 
 class RoundDriver:
@@ -28,16 +28,23 @@ class RoundDriver:
     captured CUDA graph of its bucket (StepGraph) instead of launching the
     kernels one by one; ``max_row_pages`` then bounds every request's pages.
     The record adds the bucket and the pad tokens.
+
+    ``interleaved``, ``window`` and ``sinks`` are those of step.run_step, over bf16 pools and without graphs; ``cos`` and
+    ``sin`` may cover part of the head (step.rotary_tables).
     """
 
     def __init__(self, engine: Engine, k_cache, v_cache, cos, sin, H_q: int, H_kv: int, D: int,
-                 scale: float | None = None, stream=None, graph_buckets=None, max_row_pages: int = 0):
+                 scale: float | None = None, stream=None, graph_buckets=None, max_row_pages: int = 0,
+                 interleaved: bool = False, window: int | None = None, sinks=None):
         import torch
         self.engine = engine
         self.graph = None
         self.q4 = v_cache is None
         if self.q4 and graph_buckets:
             raise ValueError("graph_buckets needs bf16 pools: a step over a 4-bit pool is captured with step.StepTables")
+        self.forms = {"interleaved": interleaved, "window": window, "sinks": sinks}
+        if (interleaved or window is not None or sinks is not None) and (self.q4 or graph_buckets):
+            raise ValueError("interleaved pairs, a window and sinks need bf16 pools and no graph_buckets")
         self.k_cache, self.v_cache = k_cache, v_cache
         self.cos, self.sin = cos, sin
         self.H_q, self.H_kv, self.D = H_q, H_kv, D
@@ -60,7 +67,8 @@ class RoundDriver:
             self.q_rot, self.out = self.graph.q_rot, self.graph.out
             return
         self.stager = MetaStager(max_rows, max(budget, 1), 64 * max_rows, self.device)  # grows on demand
-        ws = attention_workspace_size(max_rows, max(budget, 1), num_pages * 16, H_q, H_kv, D, q4=self.q4)
+        ws = attention_workspace_size(max_rows, max(budget, 1), num_pages * 16, H_q, H_kv, D,
+                                      q4=self.q4 or window is not None or sinks is not None)
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.q_rot = torch.empty((max(budget, 1), H_q, D), dtype=torch.bfloat16, device=self.device)
@@ -99,10 +107,8 @@ class RoundDriver:
                 run_step_q4(q, k, v, batch, self.cos, self.sin, self.k_cache, self.out, self.workspace, q_rot=self.q_rot,
                             dev_status=self.status, scale=self.scale, stream=self.stream)
             else:
-                mixed_step(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, self.cos, self.sin, self.k_cache,
-                           self.v_cache, self.q_rot[:T], batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
-                           batch.block_tables, batch.context_total, self.out[:T], self.workspace,
-                           dev_status=self.status, scale=self.scale, stream=self.stream)
+                run_step(q, k, v, batch, self.cos, self.sin, self.k_cache, self.v_cache, self.out, self.workspace,
+                         q_rot=self.q_rot, dev_status=self.status, scale=self.scale, stream=self.stream, **self.forms)
             self.ev1.record(self.stream)
             self.stream.synchronize()
             st = read_status(self.status, self.stream) | read_status(self.workspace, self.stream)

@@ -10,8 +10,9 @@ import dataclasses
 
 import numpy as np
 
-from . import (attention_workspace_size, build_batch_metadata_device, kv_append_rope_q4, mixed_step,
-               mixed_step_attention, mixed_step_attention_q4, mixed_step_attention_ragged, q4_block_bytes, rope_table)
+from . import (attention_workspace_size, build_batch_metadata_device, kv_append_rope_q4, kv_append_rotary, mixed_step,
+               mixed_step_attention, mixed_step_attention_q4, mixed_step_attention_ragged, mixed_step_attention_window,
+               mixed_step_cross_attention, q4_block_bytes, rope_table, rotary_frequencies, rotary_table_device)
 
 META_KEYS = ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping", "block_tables")
 RAGGED_KEYS = ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping", "bt_offsets", "bt_pages")
@@ -145,9 +146,20 @@ def rope_tables_device(max_pos: int, D: int, device, base: float = 10000.0):
     return torch.from_numpy(cos).to(device), torch.from_numpy(sin).to(device)
 
 
+def rotary_tables(max_pos: int, rotary_dim: int, device, base: float = 10000.0, scaling: dict = None, first_pos: int = 0):
+    """Cosines and sines [max_pos, rotary_dim / 2] of the positions from ``first_pos`` on, made on the GPU, with the
+    frequencies scaled as ``scaling`` says (rotary_frequencies)."""
+    import torch
+    freq, amplitude = rotary_frequencies(rotary_dim, base, scaling)
+    cos, sin = (torch.empty((max_pos, rotary_dim // 2), dtype=torch.float32, device=device) for _ in range(2))
+    with torch.cuda.device(cos.device):
+        rotary_table_device(freq, cos, sin, amplitude=amplitude, first_pos=first_pos)
+    return cos, sin
+
+
 def workspace_for(batch: DeviceBatch, H_q: int, H_kv: int, D: int, device, q4: bool = False):
-    """A zeroed workspace for the attention of this batch; ``q4``: with the room that a step over a 4-bit pool uses to
-    cut few long chunk items into parts (it runs without, on whole items)."""
+    """A zeroed workspace for the attention of this batch; ``q4``: with the room that a step over a 4-bit pool, a window
+    or an encoder's states uses to cut few long chunk items into parts (it runs without, on whole items)."""
     import torch
     n = attention_workspace_size(max(batch.num_rows, 1), max(batch.num_tokens, 1), batch.context_total, H_q, H_kv,
                                  D, q4=q4)
@@ -207,28 +219,65 @@ class StepTables:
 
 
 def run_step(q, k, v, batch: DeviceBatch, cos, sin, k_cache, v_cache, out, workspace, q_rot=None,
-             dev_status=None, scale=None, stream=None):
-    """One step of one layer through ms_mixed_step (the append, then the attention, with the
-    prologue inside the append's launch on small steps); returns q_rot."""
+             dev_status=None, scale=None, stream=None, interleaved: bool = False, window: int = None, sinks=None):
+    """One step of one layer; returns q_rot.
+
+    Where the whole head turns in halves and every token sees all keys up to its own this is ms_mixed_step (the append,
+    then the attention, with the prologue inside the append's launch on small steps).  With tables of fewer pairs (or
+    None: nothing turns), ``interleaved`` pairs, or q, k, v whose tokens' rows lie apart, the append is
+    kv_append_rotary; with a ``window`` or ``sinks`` the attention is mixed_step_attention_window."""
     if q_rot is None:
         q_rot = q
-    T = batch.num_tokens
-    mixed_step(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot[:T],
-               batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens, batch.block_tables, batch.context_total,
-               out[:T], workspace, bt_offsets=batch.bt_offsets if batch.ragged else None, dev_status=dev_status,
-               scale=scale, stream=stream)
+    T, D = batch.num_tokens, q.shape[2]
+    rows = (q[:T], k[:T], v[:T])
+    if interleaved or cos is None or 2 * cos.shape[1] != D or not all(x.is_contiguous() for x in rows):
+        kv_append_rotary(*rows, batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot=q_rot[:T],
+                         interleaved=interleaved, dev_status=dev_status, stream=stream)
+    elif window is None and sinks is None:
+        mixed_step(*rows, batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot[:T], batch.cu_seqlens_q,
+                   batch.q_start_pos, batch.context_lens, batch.block_tables, batch.context_total, out[:T], workspace,
+                   bt_offsets=batch.bt_offsets if batch.ragged else None, dev_status=dev_status, scale=scale,
+                   stream=stream)
+        return q_rot
+    else:
+        kv_append_rotary(*rows, batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot=q_rot[:T],
+                         dev_status=dev_status, stream=stream)
+    attend(q_rot[:T], k_cache, v_cache, batch, out[:T], workspace, scale=scale, stream=stream, window=window, sinks=sinks)
     return q_rot
 
 
-def attend(q_rot, k_cache, v_cache, batch: DeviceBatch, out, workspace, scale=None, stream=None) -> None:
-    """The attention call of a staged batch, with its padded or ragged block table."""
-    if batch.ragged:
+def attend(q_rot, k_cache, v_cache, batch: DeviceBatch, out, workspace, scale=None, stream=None, window: int = None,
+           sinks=None) -> None:
+    """The attention call of a staged batch, with its padded or ragged block table; with a ``window`` or ``sinks`` over
+    the last ``window`` keys (all of them where it is None)."""
+    if window is not None or sinks is not None:
+        mixed_step_attention_window(q_rot, k_cache, v_cache, batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
+                                    batch.block_tables, batch.context_total, out, workspace,
+                                    2 ** 31 - 1 if window is None else window, sinks=sinks,
+                                    bt_offsets=batch.bt_offsets if batch.ragged else None, scale=scale, stream=stream)
+    elif batch.ragged:
         mixed_step_attention_ragged(q_rot, k_cache, v_cache, batch.cu_seqlens_q, batch.q_start_pos,
                                     batch.context_lens, batch.bt_offsets, batch.block_tables, batch.context_total,
                                     out, workspace, scale=scale, stream=stream)
     else:
         mixed_step_attention(q_rot, k_cache, v_cache, batch.cu_seqlens_q, batch.q_start_pos, batch.context_lens,
                              batch.block_tables, batch.context_total, out, workspace, scale=scale, stream=stream)
+
+
+def append_states(k, v, slot_mapping, k_cache, v_cache, dev_status=None, stream=None) -> None:
+    """An encoder's keys and values [n, H_kv, D] into the pages of their pools, as they are."""
+    kv_append_rotary(None, k, v, None, slot_mapping, None, None, k_cache, v_cache, dev_status=dev_status, stream=stream)
+
+
+def cross_attend(q, k_cache, v_cache, batch: DeviceBatch, key_lens, block_tables, key_total: int, out, workspace,
+                 bt_offsets=None, scale=None, stream=None) -> None:
+    """The batch's tokens over the states of their rows' encoders: row s sees the ``key_lens[s]`` keys that row s of
+    ``block_tables`` (or of the ragged list with ``bt_offsets``) names, in pools of their own.  ``workspace`` may be the
+    one of the step's self-attention where it is large enough (attention_workspace_size with ``key_total`` for the
+    contexts' sum)."""
+    T = batch.num_tokens
+    mixed_step_cross_attention(q[:T], k_cache, v_cache, batch.cu_seqlens_q, key_lens, block_tables, key_total, out[:T],
+                               workspace, bt_offsets=bt_offsets, scale=scale, stream=stream)
 
 
 def run_step_q4(q, k, v, batch: DeviceBatch, cos, sin, kv_cache, out, workspace, q_rot=None, dev_status=None,

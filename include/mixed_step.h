@@ -532,6 +532,130 @@ MS_API int ms_build_batch_metadata_device(
     int32_t* bt_offsets, int32_t* bt_pages, int64_t cap_pages, int32_t* info, int32_t* dev_status,
     ms_stream_t stream);
 
+/* ---- Other rotations and other views of the cache --------------------------
+ * Steps of layers whose rotation is not that of ms_kv_append_rope (part of a
+ * head, neighbouring pairs, frequencies scaled for long contexts) or whose
+ * tokens do not see all keys up to their own (a window of the last ones, with
+ * or without a sink; the states of an encoder).  bf16 pools as above.  The
+ * pages have no counterpart. */
+
+/* Scaling of the rotary frequencies f_i = base^(-2i/R), i < R/2, of a model
+ * that was trained to shorter contexts.
+ *   MS_ROTARY_PLAIN   as they are
+ *   MS_ROTARY_LINEAR  f_i / factor
+ *   MS_ROTARY_BASE    the base times factor^(R / (R - 2))
+ *   MS_ROTARY_BANDS   by wavelength: with t = original_len f_i / (2 pi), the turns of
+ *                     pair i over the original length, and keep = (t - low) /
+ *                     (high - low) clamped to 0..1, (1 - keep) f_i / factor + keep f_i
+ *   MS_ROTARY_RAMP    by index: with x(t) the (real) pair that turns t times over the
+ *                     original length, lo = max(floor(x(high)), 0), hi = min(ceil(x(low)),
+ *                     R - 1) (lo + 0.001 if that is not above lo) and stretch = (i - lo) /
+ *                     (hi - lo) clamped to 0..1, stretch f_i / factor + (1 - stretch) f_i;
+ *                     cosines and sines are multiplied by `amplitude`, or where that is 0
+ *                     by 0.1 ln(factor) + 1 (1 for factors up to 1) */
+enum { MS_ROTARY_PLAIN = 0, MS_ROTARY_LINEAR = 1, MS_ROTARY_BASE = 2, MS_ROTARY_BANDS = 3, MS_ROTARY_RAMP = 4 };
+
+typedef struct {
+  int32_t kind;         /* MS_ROTARY_* */
+  int32_t original_len; /* bands, ramp: the length that the model was trained to */
+  double factor;        /* all but plain: > 0 */
+  double low, high;     /* bands, ramp: turns over the original length, 0 < low < high */
+  double amplitude;     /* ramp: >= 0 */
+} ms_rotary_scaling;
+
+/* ms_rotary_frequencies -- host: the scaled frequencies of rotary_dim = R elements
+ * into freq [R/2] (radians a position) and the factor of the cosines and sines into
+ * *amplitude, in double precision.  scaling NULL is MS_ROTARY_PLAIN.
+ * Errors: MS_ERR_ARG (R odd, < 2 or > 128, base <= 0, a bad scaling). */
+MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, const ms_rotary_scaling* scaling, double* freq,
+                                 double* amplitude);
+
+/* ms_rotary_table_device -- device: cos_tab[r][i] = amplitude cos(p freq[i]) and
+ * sin_tab[r][i] alike for p = first_pos + r, r < n, as ms_rope_table lays them out.
+ * Angles are exact in 64-bit fixed point whatever the position (error below 1e-9
+ * at 2^31, 1e-12 up to 2^20); beside that a result is within 0.8 of a step of fp32 of
+ * the exact one.
+ *   freq      host double [pairs], |freq| <= 1024; read before the call returns
+ *   pairs     R / 2: 4 .. 64, a multiple of 4
+ *   cos_tab, sin_tab  device fp32 [n, pairs], 16-byte aligned
+ * Errors: MS_ERR_ARG (also first_pos + n > 2^31), MS_ERR_CUDA. */
+MS_API int ms_rotary_table_device(const double* freq, int32_t pairs, double amplitude, int32_t first_pos, int32_t n,
+                                  float* cos_tab, float* sin_tab, ms_stream_t stream);
+
+/* ms_kv_append_rotary -- ms_kv_append_rope with the rotation's other forms: the
+ * first rotary_dim = R elements of every head of q and k turn, the others are copied.
+ * The pairs are elements (i, i + R/2), or with interleaved = 1 (2i, 2i + 1); pair i
+ * turns by entry i of the position's table row; rounding as there, so that R = D with
+ * interleaved = 0 gives its results bit for bit.
+ *   q, k, v    device bf16, token t's heads back to back from element
+ *              t * {q,k,v}_stride (H_q D, H_kv D, H_kv D elements or more, a multiple
+ *              of 8): rows of one fused projection need no copy.  H_q = 0: no q and
+ *              no q_rot (then NULL; q_stride is not looked at)
+ *   q_rot      device bf16 [T, H_q, D]; may be q itself where q_stride is H_q D, and
+ *              overlaps neither k, v nor another part of q
+ *   cos_tab, sin_tab  device fp32 [max_pos, R/2]
+ *   R          a multiple of 16, 0 .. D.  With R = 0 nothing turns: positions,
+ *              tables and max_pos are not looked at (an encoder's states)
+ * H_q needs not be a multiple of H_kv.  Slots, positions, dev_status and alignment as
+ * ms_kv_append_rope.  Two tokens of one call with the same slot leave a mixture of
+ * their rows there.  Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_kv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t T,
+                               const float* cos_tab, const float* sin_tab, int32_t max_pos, int32_t rotary_dim,
+                               int32_t interleaved, void* k_cache, void* v_cache, int32_t num_pages, void* q_rot,
+                               int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, int32_t* dev_status,
+                               ms_stream_t stream);
+
+/* ms_mixed_step_attention_window -- the attention of ms_mixed_step_attention
+ * (block_tables padded with bt_stride, bt_offsets == NULL) or of
+ * ms_mixed_step_attention_ragged (bt_offsets given, block_tables = bt_pages with
+ * bt_len entries) where the query at position p sees the keys p - window + 1 .. p,
+ * and with sinks given
+ *     out[t, h] = sum_j e^(s_j) V[j] / (e^(sinks[h]) + sum_j e^(s_j)).
+ * Rows, pad rows, causal bounds, status bits, limits and errors as there.  Nothing
+ * is read of a row's pages that lie wholly in front of its first new token's window,
+ * their table entries included: they may have been given back.  Values in cells that
+ * no token of the row sees do not matter, infinities and NaN included.
+ *   window     >= 1; a window of a row's length or more changes nothing
+ *   sinks      device fp32 [H_q] or NULL; finite or -infinity (no sink)
+ *   workspace  as for ms_mixed_step_attention; with one of
+ *              ms_attention_workspace_size_q4 bytes few long chunk items are cut into
+ *              parts that run at once
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_mixed_step_attention_window(const void* q_rot, const void* k_cache, const void* v_cache, int32_t num_pages,
+                                          const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                          const int32_t* context_lens, const int32_t* block_tables,
+                                          const int32_t* bt_offsets, int64_t bt_len, int32_t bt_stride,
+                                          int32_t num_rows, int32_t num_tokens, int64_t context_total, int32_t H_q,
+                                          int32_t H_kv, int32_t D, int32_t page_size, float scale, int32_t window,
+                                          const float* sinks, void* out, void* workspace, size_t ws_bytes,
+                                          ms_stream_t stream);
+
+/* ms_mixed_step_cross_attention -- every token of row s attends to all key_lens[s]
+ * keys in the row's pages (an encoder's states, put there by ms_kv_append_rotary with
+ * R = 0), whatever its position: rows of one and of more tokens in one call, as
+ * packed for the step's self-attention.  The tokens of a row with key_lens[s] = 0 get
+ * zeros.  key_total bounds the sum of key_lens (pad rows' too).  Tables, workspace,
+ * status bits, limits and errors as ms_mixed_step_attention_window; a row needs
+ * ceil(key_lens[s] / 16) pages.  Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_mixed_step_cross_attention(const void* q, const void* k_cache, const void* v_cache, int32_t num_pages,
+                                         const int32_t* cu_seqlens_q, const int32_t* key_lens,
+                                         const int32_t* block_tables, const int32_t* bt_offsets, int64_t bt_len,
+                                         int32_t bt_stride, int32_t num_rows, int32_t num_tokens, int64_t key_total,
+                                         int32_t H_q, int32_t H_kv, int32_t D, int32_t page_size, float scale, void* out,
+                                         void* workspace, size_t ws_bytes, ms_stream_t stream);
+
+/* ms_test_attention_stall_window -- ms_test_attention_stall (padded table) over a
+ * window, of chunk rows in parts or whole.  Not for production use.
+ * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
+MS_API int ms_test_attention_stall_window(const void* q_rot, const void* k_cache, const void* v_cache, int32_t num_pages,
+                                          const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
+                                          const int32_t* context_lens, const int32_t* block_tables, int32_t bt_stride,
+                                          int32_t num_rows, int32_t num_tokens, int64_t context_total, int32_t H_q,
+                                          int32_t H_kv, int32_t D, int32_t page_size, float scale, int32_t window,
+                                          void* out, void* workspace, size_t ws_bytes, int64_t wait_limit_ns,
+                                          ms_stream_t stream);
+
 /* ---- Multi-round engine (host) ------------------------------------------
  * A page pool with full-input admission and a plan/commit round driver over
  * ms_build_batch_metadata.  A request reserves ceil((prompt_len +

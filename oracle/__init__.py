@@ -20,6 +20,8 @@ in the pages' order and notation:
   keys 0..p read through the block table (zwjcode sections 02 and 07);
 * ``q4``        -- the 4-bit cache's rounding and bytes, and step metadata built
   from request lengths;
+* ``rotary``    -- the rotary embedding's other forms: scaled frequencies, part of a
+  head, neighbouring pairs;
 * ``engine``    -- a multi-round driver over a page pool that reserves a
   request's full input plus its new tokens at admission (zwjcode section 11;
   "Splitting Prefill From Decode Inside a Step").
@@ -34,11 +36,12 @@ from .rope import bf16_to_f64, f32_to_bf16_bits, rope_tables, rope_rotate, kv_ap
 from .attention import attention_rows, attention_all
 from .engine import AdmissionError, Engine
 from .q4 import metadata_from_lengths, q4_read, q4_round, q4_values, q4_write
+from . import rotary
 
 __all__ = [
     "BudgetError", "NoPagesError", "schedule", "batch_metadata", "commit_round", "DECODE_FIRST",
     "PREFILL_FIRST", "FAIR_SHARE",
     "bf16_to_f64", "f32_to_bf16_bits", "rope_tables", "rope_rotate", "kv_append",
     "attention_rows", "attention_all", "AdmissionError", "Engine",
-    "metadata_from_lengths", "q4_read", "q4_round", "q4_values", "q4_write",
+    "metadata_from_lengths", "q4_read", "q4_round", "q4_values", "q4_write", "rotary",
 ]
