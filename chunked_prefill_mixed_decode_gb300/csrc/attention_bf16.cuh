@@ -99,6 +99,80 @@ __device__ __forceinline__ DecItem describe_dec(const AttnParams& p, int item, i
 // not fit here: its M is at least 64 rows, while a decode page is 16 rows per
 // warp and a row's G query heads fill only part of N.
 
+// merge_splits for a KV head's G heads at once, sixteen 16-byte loads of a lane in flight: a lane looks after
+// the weights of head lane % G and every (32 / G)th split, and owns D / 32 columns of every head.  (Head after
+// head, two splits of eight heads took 10 us to join where their pages took 9.)  Records of splits past the
+// last are those of the last with weight 0.
+template <int D, int G>
+__device__ __noinline__ void merge_heads(const AttnParams& p, int k, int h0, int tok, int ns, int lane) {
+  constexpr int EPL = D / 32, NS = 32 / G;  // columns to a lane; splits whose weights the warp holds at a time
+  constexpr int B = 16 / G;                 // splits to a batch of loads
+  const int64_t base = __ldcg(p.dec_part_base + k) + h0;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + base + (lane & (G - 1));
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int j = lane / G; j < ns; j += NS) M = fmaxf(M, __ldcg(ml + static_cast<int64_t>(j) * p.H_q).x);
+#pragma unroll
+  for (int o = G; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, out[G][EPL];
+#pragma unroll
+  for (int h = 0; h < G; ++h)
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) out[h][e] = 0.f;
+  for (int j0 = 0; j0 < ns; j0 += NS) {
+    const int j = j0 + lane / G;
+    float w = 0.f;
+    if (j < ns) {
+      const float2 x = __ldcg(ml + static_cast<int64_t>(j) * p.H_q);
+      w = ex2(x.x - M);
+      L += w * x.y;
+    }
+    const int nj = min(NS, ns - j0);
+#pragma unroll 1
+    for (int b = 0; b < nj; b += B) {
+      float a[B][G][EPL];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const float* src = p.part_acc + (base + static_cast<int64_t>(min(j0 + b + u, ns - 1)) * p.H_q) * D + lane * EPL;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          if constexpr (EPL == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + h * D));
+            a[u][h][0] = v.x; a[u][h][1] = v.y; a[u][h][2] = v.z; a[u][h][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src + h * D));
+            a[u][h][0] = v.x; a[u][h][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float x = __shfl_sync(0xffffffffu, w, ((b + u) * G + h) & 31);
+          const float wj = b + u < nj ? x : 0.f;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) out[h][e] += wj * a[u][h][e];
+        }
+    }
+  }
+#pragma unroll
+  for (int o = G; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  bf16* dst = p.out + (static_cast<int64_t>(tok) * p.H_q + h0) * D + lane * EPL;
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    const float inv = 1.f / __shfl_sync(0xffffffffu, L, h);
+    uint32_t x[EPL / 2];
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(out[h][e] * inv, out[h][e + 1] * inv);
+      x[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    if constexpr (EPL == 4) *reinterpret_cast<uint2*>(dst + h * D) = make_uint2(x[0], x[1]);
+    else *reinterpret_cast<uint32_t*>(dst + h * D) = x[0];
+  }
+}
+
 // Out of line, as is chunk_phase: each phase gets its own register allocation
 // (inlined into one kernel body the two spill).
 template <int D, int G, bool Span = false>
@@ -342,7 +416,8 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
       last = __shfl_sync(0xffffffffu, last, 0);
       if (last) {
         __threadfence();
-        merge_splits<D>(p, cur.k, cur.hk * G, G, cur.tok, cur.ns, lane);
+        if constexpr (Span) merge_heads<D, G>(p, cur.k, cur.hk * G, cur.tok, cur.ns, lane);
+        else merge_splits<D>(p, cur.k, cur.hk * G, G, cur.tok, cur.ns, lane);
       }
     }
     if (!nxt_valid) break;

@@ -83,7 +83,7 @@ struct AttnParams {
   int32_t* ch_rows;
   int2* dec_items;  // per decode split (items / H_kv entries): (decode row index, split within the row)
   int32_t* dec_cnt; // per (decode row, KV head): splits finished, for the last one to merge
-  int2* ch_items;   // per chunk item: (chunk row index, KV head << 16 | Q-tile pair counted from the last)
+  int2* ch_items;   // per chunk item: (chunk row index; spans: row, KV head << 16 | Q-tile pair counted from the last)
   // the attention kernel's alone
   const bf16* q_rot;
   const uint8_t* kv_q4;   // 4-bit pool (q4.cuh), in the calls that take one
@@ -243,16 +243,13 @@ __device__ __forceinline__ int parts_of(const AttnParams& p, int c, int d, int t
   return Span ? span_parts(p, c, d, tpt, tiles) : chunk_parts(c, d, tiles);
 }
 
-template <bool Span>
-__device__ __forceinline__ unsigned tiles_of(const AttnParams& p, int c, int d, int tpt) {
-  if (!Span) return chunk_tiles(c, d, tpt);
-  if (p.fixed_span) return static_cast<unsigned>(d + tpt - 1) / tpt * ((static_cast<unsigned>(c) + 128u) >> 7);
-  unsigned tiles = 0;
-  for (int tok = 0; tok < d; tok += tpt) {
-    const int end = c + min(d, tok + tpt);
-    tiles += static_cast<unsigned>(end - span_first(p, c + tok) + 127) >> 7;
-  }
-  return tiles;
+// 128x128 tiles of a chunk row (one KV head) for the cost model, without a loop over its Q tiles: each sees the keys
+// of its tokens on average, half its own tokens more, and fills half of its last tile.
+__device__ __forceinline__ float span_tiles(const AttnParams& p, int c, int d, int tpt) {
+  const float cf = static_cast<float>(c), df = static_cast<float>(d), w = static_cast<float>(p.window);
+  const float low = fminf(df, fmaxf(0.f, w - cf));  // tokens that see everything up to their own key
+  const float keys = p.fixed_span ? cf + 1.f : __fdividef(low * (cf + 0.5f * (low + 1.f)) + (df - low) * w, df);
+  return static_cast<float>((d + tpt - 1) / tpt) * (keys + 0.5f * tpt + 64.f) * (1.f / 128);
 }
 
 template <bool Span>
@@ -424,6 +421,42 @@ __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_
   return dec_candidate(static_cast<int>(best & 31u));
 }
 
+// Split of the decode rows of a span: equal splits of the longest row, 1 to 512 of them, a lane a count; the
+// smallest estimate of the decode rows' time wins.  With x = items / warps, and a page's time a warp of tp alone
+// and of ts with every warp at the memory's rate,
+//     floor(x) L max(tp, ts) + max(s tp, frac(x) L ts) + 6.5 ceil(x) + (2 + 0.1 G splits where there is a join)
+// us, s: pages of a split, L: of an item on average.  Fitted to sweeps over 29 steps (1 to 512 rows of 1 to 40 KV
+// heads, 1 to 6251 pages, 14 to 500 us) in a build that forced the split for the purpose: its choices took 0.2 %
+// longer than the best of each sweep, 2.2 % the worst.  warps: those that decode rows get beside chunk rows.
+// Rows of up to kWholePages pages are not split (nor does the prologue, which runs from a cold instruction cache,
+// then come here: 2 us).  Called by whole warps.
+constexpr int kWholePages = 18;
+
+__device__ __noinline__ int span_split(const AttnParams& p, int64_t dec_pages, int n_dec, int max_pages, float warps) {
+  const int lane = threadIdx.x & 31, n = lane < 8 ? lane + 1 : (((lane & 3) + 5) << ((lane >> 2) - 1));
+  const int s = (max_pages + n - 1) / n;
+  const float P = static_cast<float>(dec_pages), R = static_cast<float>(n_dec), sf = static_cast<float>(s);
+  const float items = fmaxf(R, fminf(n * R, __fdividef(P, sf) + 0.5f * R)), x = __fdividef(items * p.H_kv, warps);
+  const float L = __fdividef(P, items), tp = p.D == 128 ? 1.1f : 0.73f;
+  const float ts = __fdividef(kPage * p.key_bytes * warps, 1135.f * p.hbm_gbs);  // us a page, every warp at 1.135 hbm_gbs
+  const float full = floorf(x), f = x - full;
+  const int joined = (max_pages + s - 1) / s;
+  float t = full * L * fmaxf(tp, ts) + fmaxf(f > 0.f ? sf * tp : 0.f, f * L * ts) + 6.5f * ceilf(x);
+  if (joined > 1) t += 2.f + 0.1f * p.G * joined;
+  // splits of at least two pages, and no more than the workspace has places for (a row's last one counted whole)
+  const int64_t most = p.max_dec_items / p.H_kv;
+  if (n > 1 && (s < 2 || R + __fdividef(P, sf) * 1.001f > static_cast<float>(most))) t = 3.0e38f;
+  const unsigned best = __reduce_min_sync(0xffffffffu, (__float_as_uint(t) & ~31u) | static_cast<unsigned>(lane));
+  return max(1, __shfl_sync(0xffffffffu, s, static_cast<int>(best & 31u)));
+}
+
+// Warps that decode rows get beside `tiles` 128x128 tiles of chunk work: the balance of chunk_cta_split.
+__device__ __forceinline__ float span_warps(const AttnParams& p, float tiles, float dec_pages) {
+  const float B = dec_pages * p.H_kv * kPage * p.key_bytes;
+  const float C = tiles * p.tile_cycles * p.dec_bytes_cycle;  // bytes that decode rows would read in the tiles' time
+  return fmaxf(1.f, p.dec_workers * __fdividef(B, B + C));
+}
+
 // KV tiles to a part of a chunk item, or 0 for whole items.  Items are cut where
 // they are fewer than half the CTAs that chunk work gets beside the decodes (k,
 // the balance of chunk_cta_split): every part then starts at once.  Parts are
@@ -497,7 +530,7 @@ __device__ __noinline__ int plan_parts_block(const AttnParams& p, const int* rd,
 
 // Table entries and counters of a chunk row in parts, from place `first`: `items` of
 // them per KV head, the parts of a pair neighbours.  The first word is the row's
-// position k in the list and, above it, the part.  By one warp.
+// position k in the list (spans: the row) and, above it, the part.  By one warp.
 __device__ __noinline__ void chunk_part_table(const AttnParams& p, int first, int k, int items, int parts, bool head_major,
                                               int lane) {
   const ChunkParts cp(p);
@@ -568,8 +601,21 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int tpt = 128 / p.G;
   const unsigned bd = __ballot_sync(0xffffffffu, is_dec), bc = __ballot_sync(0xffffffffu, is_ch);
   const int n_dec = __popc(bd), n_ch = __popc(bc);
-  const int max_pages = Teams ? __reduce_max_sync(0xffffffffu, is_dec ? (ctx + kPage - 1) / kPage : 0) : 0;
-  const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  const int max_pages = Teams || Span ? __reduce_max_sync(0xffffffffu, is_dec ? dec_pages_of<Span>(p, ctx) : 0) : 0;
+  DecPlan plan;
+  float work = 0.f;  // spans: 128x128 tiles of the chunk rows
+  if constexpr (Span) {
+    if (n_ch > 0) {
+      work = is_ch ? span_tiles(p, c, d, tpt) * p.H_kv : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    }
+    plan = {max(1, max_pages), 1};
+    if (max_pages > kWholePages)
+      plan.split = span_split(p, dec_pages, n_dec, max_pages, span_warps(p, work, static_cast<float>(dec_pages)));
+  } else {
+    plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  }
   const int split = plan.split;
   // position in its list, then rank by key within the list (longest first):
   // the keys sit in shared memory by list position, zero-padded, read 16 bytes at a time
@@ -621,10 +667,9 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
   const int64_t n_ch_items = static_cast<int64_t>(ch_tot) * p.H_kv;
   const bool dec_over = n_dec_items > p.max_dec_items || static_cast<int64_t>(dec_tot) * p.H_q > p.max_partials;
   const bool ch_over = n_ch_items > (part_tiles > 0 ? p.ch_cap : p.max_ch_items);
-  const int64_t tiles =
-      warp_sum31(is_ch ? static_cast<int>(min(static_cast<int64_t>(tiles_of<Span>(p, c, d, tpt)) * p.H_kv,
-                                                int64_t{0x7fffffff}))
-                       : 0);
+  if constexpr (!Span)
+    work = static_cast<float>(warp_sum31(
+        is_ch ? static_cast<int>(min(static_cast<int64_t>(chunk_tiles(c, d, tpt)) * p.H_kv, int64_t{0x7fffffff})) : 0));
   const int64_t chunk_keys = warp_sum31(!is_ch ? 0 : Span ? ctx - span_first(p, c) : ctx);
   if (is_dec) {
     p.dec_rows[rank] = lane;
@@ -634,7 +679,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
       for (int i = 0; i < items; ++i) p.dec_items[before + i] = make_int2(dec_entry<Teams>(rank, lane), i);
   }
   if (is_ch) p.ch_rows[rank] = lane;
-  const SmSplit sp = chunk_cta_split(p, static_cast<float>(tiles), static_cast<float>(dec_pages),
+  const SmSplit sp = chunk_cta_split(p, work, static_cast<float>(dec_pages),
                                      ch_over ? 0 : static_cast<int>(n_ch_items),
                                      dec_over ? 0 : dec_item_warps(n_dec_items, plan.team), static_cast<float>(chunk_keys),
                                      measured_mhz, lane);
@@ -645,13 +690,13 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     const int r_rank = __shfl_sync(0xffffffffu, rank, src), r_items = __shfl_sync(0xffffffffu, items, src);
     const int r_before = __shfl_sync(0xffffffffu, before, src);
     if (Parts && part_tiles > 0) {
-      chunk_part_table(p, (r_before - dec_tot) * p.H_kv, r_rank, r_items, __shfl_sync(0xffffffffu, parts, src), sp.head_major,
+      chunk_part_table(p, (r_before - dec_tot) * p.H_kv, Span ? src : r_rank, r_items, __shfl_sync(0xffffffffu, parts, src), sp.head_major,
                        lane);
       continue;
     }
     int2* out = p.ch_items + static_cast<int64_t>(r_before - dec_tot) * p.H_kv;
     for (int i = lane; i < r_items * p.H_kv; i += 32)
-      out[i] = make_int2(r_rank, chunk_entry(i, r_items, p.H_kv, sp.head_major));
+      out[i] = make_int2(Span ? src : r_rank, chunk_entry(i, r_items, p.H_kv, sp.head_major));
   }
   if (!dec_over) {
     const int n_cnt = n_dec * p.H_kv;  // the counters start 16-byte aligned in the workspace
@@ -691,6 +736,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   __shared__ int s_warp[32];
   __shared__ long long s_sum[3][32];
   __shared__ unsigned s_cnt[3][32];
+  __shared__ float s_work[32];
   __shared__ unsigned long long s_tiles;
   __shared__ SmSplit s_split;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
@@ -714,6 +760,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   // 1. load and validate the rows; count decodes, chunks, context and decode pages
   int64_t my_ctx = 0, my_pages = 0, my_ch_keys = 0;
   unsigned my_dec = 0, my_ch = 0, my_max = 0;
+  float my_work = 0.f;
   int my_bad = 0;
   for (int s = tid; s < S; s += nt) {
     const int32_t a = p.cu[s], b = p.cu[s + 1];
@@ -742,6 +789,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
         my_max = max(my_max, n);
       }
       if (d > 1) my_ch_keys += Span ? ctx - span_first(p, c) : ctx;
+      if (Span && d > 1) my_work += span_tiles(p, c, d, 128 / p.G) * p.H_kv;
     }
   }
   my_ctx = warp_sum64(my_ctx);
@@ -749,32 +797,45 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
   my_ch_keys = warp_sum64(my_ch_keys);
   my_dec = __reduce_add_sync(0xffffffffu, my_dec);
   my_ch = __reduce_add_sync(0xffffffffu, my_ch);
-  if (Teams) my_max = __reduce_max_sync(0xffffffffu, my_max);
+  if (Teams || Span) my_max = __reduce_max_sync(0xffffffffu, my_max);
+  if (Span) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) my_work += __shfl_xor_sync(0xffffffffu, my_work, o);
+  }
   if (lane == 0) {
     s_sum[0][warp] = my_ctx;
     s_sum[1][warp] = my_pages;
     s_sum[2][warp] = my_ch_keys;
     s_cnt[0][warp] = my_dec;
     s_cnt[1][warp] = my_ch;
-    if (Teams) s_cnt[2][warp] = my_max;
+    if (Teams || Span) s_cnt[2][warp] = my_max;
+    if (Span) s_work[warp] = my_work;
   }
   const int bad = __syncthreads_or(my_bad);
   int64_t ctx_sum = 0, dec_pages = 0, chunk_keys = 0;
   int n_dec = 0, n_ch = 0, max_pages = 0;
+  float work = 0.f;
   for (int j = 0; j < nw; ++j) {
     ctx_sum += s_sum[0][j];
     dec_pages += s_sum[1][j];
     chunk_keys += s_sum[2][j];
     n_dec += static_cast<int>(s_cnt[0][j]);
     n_ch += static_cast<int>(s_cnt[1][j]);
-    if (Teams) max_pages = max(max_pages, static_cast<int>(s_cnt[2][j]));
+    if (Teams || Span) max_pages = max(max_pages, static_cast<int>(s_cnt[2][j]));
+    if (Span) work += s_work[j];
   }
   if (bad || ctx_sum > p.context_total) {
     if (tid == 0) header_bad_meta(hdr);
     return;
   }
   // 2. decode split size
-  const DecPlan plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
+  DecPlan plan;
+  if constexpr (Span)
+    plan = {max_pages > kWholePages
+                ? span_split(p, dec_pages, n_dec, max_pages, span_warps(p, work, static_cast<float>(dec_pages)))
+                : max(1, max_pages), 1};
+  else
+    plan = decode_plan<Teams>(p, dec_pages, n_dec, max_pages, n_ch > 0);
   const int split = plan.split;
   const int part_tiles = Parts && 2 * n_ch * p.H_kv < p.num_sms && chunk_keys > kMinPartedTiles * kChunkTile &&
                                  (p.cu[S] - n_dec) / 128 * p.G * p.H_kv < p.num_sms  // the least that it needs
@@ -830,7 +891,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     const int row = lst[j], c = rc[row], d = rd[row];
     (ch ? p.ch_rows : p.dec_rows)[rank] = row;
     pref[(ch ? n_dec : 0) + rank] = items_of<Span>(p, ch, c, d, tpt, split32) * (Parts && ch && part_tiles > 0 ? parts_of<Span>(p, c, d, tpt, part_tiles) : 1);
-    if (ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(tiles_of<Span>(p, c, d, tpt)) * p.H_kv);
+    if (!Span && ch) atomicAdd(&s_tiles, static_cast<unsigned long long>(chunk_tiles(c, d, tpt)) * p.H_kv);
   }
   __syncthreads();
   // 6. exclusive prefix of the item counts in queue order (decode rows, then chunk rows)
@@ -868,7 +929,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     for (int i = 0; i < cnt; ++i) out[i] = make_int2(x, i);
   }
   if (warp == 0) {
-    const SmSplit sp = chunk_cta_split(p, static_cast<float>(s_tiles), static_cast<float>(dec_pages),
+    const SmSplit sp = chunk_cta_split(p, Span ? work : static_cast<float>(s_tiles), static_cast<float>(dec_pages),
                                        ch_over ? 0 : static_cast<int>(n_ch_items),
                                        dec_over ? 0 : dec_item_warps(n_dec_items, plan.team), static_cast<float>(chunk_keys),
                                        measured_mhz, lane);
@@ -879,13 +940,14 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
     const int np = pref[q + 1] - pref[q];
     if (Parts && part_tiles > 0) {
       const int row = p.ch_rows[q - n_dec];
-      chunk_part_table(p, (pref[q] - dec_tot) * p.H_kv, q - n_dec, np, parts_of<Span>(p, rc[row], rd[row], tpt, part_tiles),
+      chunk_part_table(p, (pref[q] - dec_tot) * p.H_kv, Span ? row : q - n_dec, np, parts_of<Span>(p, rc[row], rd[row], tpt, part_tiles),
                        s_split.head_major, lane);
       continue;
     }
     int2* out = p.ch_items + static_cast<int64_t>(pref[q] - dec_tot) * p.H_kv;
+    const int x = Span ? p.ch_rows[q - n_dec] : q - n_dec;  // a span's entries name the row itself: one look-up less
     for (int i = lane; i < np * p.H_kv; i += 32)
-      out[i] = make_int2(q - n_dec, chunk_entry(i, np, p.H_kv, s_split.head_major));
+      out[i] = make_int2(x, chunk_entry(i, np, p.H_kv, s_split.head_major));
   }
   if (!dec_over) {
     const int n_cnt = n_dec * p.H_kv;  // the counters start 16-byte aligned in the workspace

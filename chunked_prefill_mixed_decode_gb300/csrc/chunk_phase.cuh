@@ -72,7 +72,7 @@ struct ChBars {
   ChItem items[2];
   ChPart parts[2];
   int last[2];
-  // 4-bit pools: items whose Q tiles have been asked for.  Behind the rest: ahead of
+  // 4-bit pools, spans: items whose Q tiles have been asked for.  Behind the rest: ahead of
   // `items` it costs a GQA 8B step over bf16 pools 0.6 %.
   int q_asked;
 };
@@ -313,6 +313,55 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const ChItem& i
   }
 }
 
+// The end of a whole item for one warp of the group of Q tile t: O, divided by its rows' sums, from
+// TMEM to the output, by way of the warp's 4 KB of shared memory (32 rows of 64 columns, 128-byte
+// swizzled) and a TMA store of each: a thread holds a row, and 32 threads storing 16 bytes of 32 rows
+// each took 1.8 us an item, which shows where spans are short (two chunks of 3968 tokens over 64 keys, 32 / 8
+// heads: 57 -> 49 us).  A warp with the tile's last, ragged rows stores them itself.
+template <int D, int G>
+__device__ __forceinline__ void store_rows(const AttnParams& p, const CUtensorMap* tm_o, uint8_t* stage, const ChItem& it, int t,
+                                           int quad, uint32_t tO, float inv) {
+  const int lane = threadIdx.x & 31, r = quad * 32 + lane, rows = it.ntok[t] * G;
+  const bool whole = quad * 32 + 32 <= rows;
+  const int tok = it.tb + it.tok0[t];
+  bf16* dst = p.out + (static_cast<int64_t>(tok + r / G) * p.H_q + it.hk * G + r % G) * D;
+  const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+  for (int s = 0; s < D / 64; ++s) {
+    uint4 w[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t rr[32];
+      tmem_ld32(tO + s * 64 + h * 32, rr);
+      tmem_wait_ld();
+      reg_fence32(rr);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = fmul2(make_float2(__uint_as_float(rr[8 * j + 2 * e]), __uint_as_float(rr[8 * j + 2 * e + 1])), inv2);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+          x[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        w[4 * h + j] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    if (whole) {
+      if (lane == 0) bulk_wait_read();  // the stage's last store has read it
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w[j];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_3d(tm_o, stage, s * 64, it.hk * G, tok + quad * 32 / G);
+    } else if (r < rows) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + s * 64 + j * 8) = w[j];
+    }
+  }
+}
+
 // Zeros for the queries of an item whose row has no keys, by one warp.
 template <int D, int G>
 __device__ __forceinline__ void zero_rows(const AttnParams& p, const ChItem& it, int lane) {
@@ -368,6 +417,223 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
   return true;
 }
 
+// ---- spans: the producer
+
+// Warp 0 of a chunk phase over spans: queue and TMA as in chunk_phase, which has the causal form.  At
+// D = 128 a page of K is one 4 KB box too, laid out by groups of 8 keys with both 64-column slabs of a group
+// together (1 KB each): over the pages of a tile the groups of a slab are then one stride of 2 KB apart, as an
+// S MMA's descriptor wants them.  The K/V stream is what bounds the tiles: with K in two boxes a page, chunks of
+// 3968 tokens at 0 and 6000 (32 / 8 heads) over all keys took 525 us, now 465 (1.40 PFLOP/s, 0.72 of the measured
+// dense rate), over 1024 keys 150 and 135.  A second pair of Q tiles, so that the next item's are there early, with
+// three K/V stages: 539 against 525, over 64 keys 57 us either way; at D = 64, beside six stages, no change.
+template <int D, int G>
+__device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                              const AttnParams& p, uint8_t* smem, ChBars* bars, int n_items) {
+  using C = ChCfg<D>;
+  constexpr int NSL = C::NSL, TPT = 128 / G, KVS = C::KVS, kVPage = NSL * 2048;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort;
+  const uint64_t lim = p.wait_limit_ns;
+  if (lane == 0) {
+    prefetch_tmap(tm_q);
+    prefetch_tmap(tm_k);
+    prefetch_tmap(tm_v);
+  }
+  const int my_pg = lane / NSL, my_s = lane % NSL;
+  const bool loader = lane < kTilePages * NSL;
+  auto k_off = [](int b) { return C::KV_OFF + b * 2 * NSL * kKVSlab; };
+  auto v_off = [](int b) { return C::KV_OFF + b * 2 * NSL * kKVSlab + NSL * kKVSlab; };
+  auto lane0_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    int r = 1;
+    if (lane == 0) r = mbar_wait(bar, parity, abort_flag, lim) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, r, 0) != 0;
+  };
+  int g = 0, g_v = 0;                                // CTA-global KV tiles: K asked for, V asked for
+  auto load_v = [&](int gv, int row0, int npg) -> bool {
+    const int bv = gv % KVS;
+    if (gv >= KVS && !lane0_wait(&bars->v_empty[bv], ((gv / KVS) - 1) & 1)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[bv], npg * kPage * D * 2);
+    __syncwarp();
+    if (loader && my_s == 0 && my_pg < npg) {
+      if constexpr (NSL == 2)
+        tma_load_4d(smem + v_off(bv) + my_pg * kVPage, tm_v, 0, 0, 0, row0 / kPage, &bars->v_full[bv]);
+      else
+        tma_load_2d(smem + v_off(bv) + my_pg * kVPage, tm_v, 0, row0, &bars->v_full[bv]);
+    }
+    return true;
+  };
+  const int part_tiles = p.hdr[H_CH_TILES];
+  const int2* items = part_tiles > 0 ? ChunkParts(p).items : p.ch_items;
+  int t_run[2] = {0, 0}, parts_run[2] = {0, 0};  // KV tiles and parts run by each softmax group so far
+  // The item taken next: its entry and its row's words.  Taken behind the last tile of the one before: earlier
+  // look-ups, a step a tile, cost every tile more than they gain an item (544 -> 554 us for chunks of 3968 tokens
+  // at 0 and 6000 over all their keys, as the kernel was then), and the queue would be dealt out ahead.
+  int item = 0, tb = 0, end_tok = 0, c = 0;
+  int2 kl = make_int2(0, 0);
+  const int32_t* table = nullptr;
+  const auto take = [&] {
+    item = 0;
+    if (lane == 0) item = atomicAdd(p.hdr + H_CH_CTR, 1);
+    item = __shfl_sync(0xffffffffu, item, 0);
+    if (item >= n_items) return;
+    kl = __ldg(items + item);
+    const int row = kl.x & 0xffff;
+    tb = __ldg(p.cu + row);
+    end_tok = __ldg(p.cu + row + 1);
+    c = span_start(p, row);
+    table = row_table(p, row);
+  };
+  // Test hook (never set by a real call), as in chunk_phase: no item is published and no copy issued.
+  const bool stalled = p.test_stall != 0;
+  bool ok = !stalled;
+  int n_done = 0;  // items published by this CTA
+  if (ok) take();
+  while (ok) {
+    ChItem it;
+    ChPart pt{};
+    it.row = -1;
+    if (item < n_items) {
+      const int d = end_tok - tb, n_qt = (d + TPT - 1) / TPT, n_pair = (n_qt + 1) >> 1;
+      const int pair = n_pair - 1 - (kl.y & 0xffff);
+      it.row = kl.x & 0xffff;
+      it.tb = tb;
+      it.c = c;
+      it.hk = kl.y >> 16;
+      it.n_kt = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int qt = 2 * pair + t;
+        const bool has = qt < n_qt;
+        it.tok0[t] = has ? qt * TPT : 0;
+        it.ntok[t] = has ? min(TPT, d - qt * TPT) : 0;
+        // the pair's keys from the page that holds its first query's first key
+        const int lo = span_first(p, c + (p.fixed_span ? 0 : it.tok0[t]));
+        if (t == 0) {
+          pt.key0 = lo & ~(kPage - 1);
+          pt.unseen = lo - pt.key0;
+        }
+        pt.first[t] = (lo - pt.key0) / kKeys;
+        it.kv_end[t] = has ? c + (p.fixed_span ? 1 : it.tok0[t] + it.ntok[t]) - pt.key0 : 0;
+        it.n_kt = max(it.n_kt, (it.kv_end[t] + kKeys - 1) / kKeys);
+      }
+      pt.ns = 1;
+      int n = it.n_kt, kt0 = 0;  // tiles of the part, or of the whole item, and the first of them
+      if (part_tiles > 0 && n > 0) {
+        const int ns_row = span_parts(p, c, d, TPT, part_tiles);
+        n = (it.n_kt + ns_row - 1) / ns_row;
+        pt.ns = (it.n_kt + n - 1) / n;
+        pt.part = kl.x >> 16;
+        pt.item0 = item - pt.part;
+        kt0 = pt.part * n;
+        pt.key0 += kt0 * kKeys;
+        if (kt0 > 0) pt.unseen = 0;
+      }
+      // a row without keys: zeros, by this warp; a part that another pair of the row has more tiles for: nothing
+      if (n == 0 || pt.part >= pt.ns) {
+        if (n == 0 && (part_tiles == 0 || (kl.x >> 16) == 0)) zero_rows<D, G>(p, it, lane);
+        take();
+        continue;
+      }
+      it.n_kt = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        it.kv_end[t] = it.ntok[t] > 0 ? it.kv_end[t] - kt0 * kKeys : 0;
+        pt.first[t] = max(0, pt.first[t] - kt0);
+        const int end = it.kv_end[t] > 0 ? min(n, (it.kv_end[t] + kKeys - 1) / kKeys) : 0;
+        it.nkt[t] = max(0, end - pt.first[t]);
+        it.n_kt = max(it.n_kt, end);
+        pt.parity[t] = parts_run[t] & 1;
+        parts_run[t] += pt.ns > 1 && it.ntok[t] > 0;
+        it.t0[t] = t_run[t];
+        t_run[t] += it.nkt[t];
+      }
+    }
+    const int kv_max = max(it.kv_end[0], it.kv_end[1]), n_kt = it.n_kt, hk = it.hk;
+    const int32_t* btrow = table + pt.key0 / kPage;
+    const int n_pages = it.row < 0 ? 0 : (kv_max + kPage - 1) / kPage;
+    // lane L < 4 holds the page id of page L of the current tile; the next tile's is in flight
+    int pg_cur = lane < kTilePages && lane < n_pages ? __ldg(btrow + lane) : 0;
+    const int slot = n_done & 1;
+    if (n_done >= 2 && !lane0_wait(&bars->item_empty[slot], ((n_done >> 1) - 1) & 1)) {
+      ok = false;
+      break;
+    }
+    if (lane == 0) {
+      bars->items[slot] = it;
+      bars->parts[slot] = pt;
+      mbar_arrive(&bars->item_full[slot]);
+    }
+    ++n_done;
+    if (it.row < 0) break;
+    // Q tiles: the previous item's S MMAs must be done with them
+    if (n_done >= 2 && !lane0_wait(&bars->q_empty, (n_done - 2) & 1)) {
+      ok = false;
+      break;
+    }
+    const int nq = it.ntok[1] > 0 ? 2 : 1;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
+      bars->q_asked = n_done;
+    }
+    __syncwarp();
+    if (lane < nq * NSL) {
+      const int t = lane / NSL, s = lane % NSL;
+      tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + s * kQSlab, tm_q, s * 64, it.hk * G, it.tb + it.tok0[t],
+                  &bars->q_full);
+    }
+    int row0_prev = 0, npg_prev = 0;
+    for (int kt = 0; kt < n_kt; ++kt, ++g) {
+      const int lp = (kt + 1) * kTilePages + lane;
+      const int pg_nxt = lane < kTilePages && lp < n_pages ? __ldg(btrow + lp) : 0;
+      const int b = g % KVS;
+      const int npg = (min(kKeys, kv_max - kt * kKeys) + kPage - 1) / kPage;
+      int phys = __shfl_sync(0xffffffffu, pg_cur, my_pg & (kTilePages - 1));
+      if (loader && my_pg < npg && (phys < 0 || phys >= p.num_pages)) {
+        atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
+        phys = 0;
+      }
+      const int row0 = (phys * p.H_kv + hk) * kPage;
+      // K of tile g: its stage was last read by the S MMAs of tile g - KVS
+      if (g >= KVS && !lane0_wait(&bars->k_empty[b], ((g / KVS) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[b], npg * kPage * D * 2);
+      __syncwarp();
+      if (loader && my_s == 0 && my_pg < npg) {
+        if constexpr (NSL == 2)
+          tma_load_4d(smem + k_off(b) + my_pg * 4096, tm_k, 0, 0, 0, row0 / 8, &bars->k_full[b]);
+        else
+          tma_load_2d(smem + k_off(b) + my_pg * 2048, tm_k, 0, row0, &bars->k_full[b]);
+      }
+      if (kt >= 1) {  // V one tile behind
+        if (!load_v(g - 1, row0_prev, npg_prev)) {
+          ok = false;
+          break;
+        }
+        g_v = g;
+      }
+      row0_prev = row0;
+      npg_prev = npg;
+      pg_cur = pg_nxt;
+    }
+    if (!ok) break;
+    if (!load_v(g - 1, row0_prev, npg_prev)) {
+      ok = false;
+      break;
+    }
+    g_v = g;
+    take();
+  }
+  if (lane == 0) {
+    if (!ok && !stalled) *abort_flag = 1;
+    // copies still in flight must land before the CTA moves on (Q's: close_chunk_barriers)
+    for (int t = (g > KVS ? g - KVS : 0); t < g; ++t) mbar_wait(&bars->k_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
+    for (int t = (g_v > KVS ? g_v - KVS : 0); t < g_v; ++t)
+      mbar_wait(&bars->v_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
+  }
+}
+
 // Chunk phase.  Warp 0 owns the work queue and streams Q and K/V with TMA (K
 // one tile ahead of V); warps 2-5 and 6-9 are two softmax groups, group t
 // owning Q tile t of the current pair, one query row per thread over 64-key
@@ -401,9 +667,10 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
 template <int D, int G, int Kind = kCausal>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
-                                            const AttnParams& p, uint8_t* smem, uint32_t tmem) {
-  using C = ChCfg<D>;
+                                            const AttnParams& p, uint8_t* smem, uint32_t tmem,
+                                            const CUtensorMap* tm_o_p = nullptr) {
   constexpr bool Q4 = Kind == kQ4, Span = Kind == kSpan, Parts = Q4 || Span;
+  using C = ChCfg<D>;
   constexpr int NSL = C::NSL;
   constexpr int TPT = 128 / G;  // query tokens per 128-row Q tile
   constexpr int KVS = C::KVS;
@@ -466,8 +733,10 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   // issues, which takes the issue off the critical path: 605 -> 507 us then for chunks of
   // 3968 tokens at 0 and 6000, 32 / 8 heads.  Over a bf16 pool, where the same change
   // measures 522 -> 527 us there and 2060 -> 2110 us beside long decodes (and 69 -> 61 us
-  // for D = 64), lane 0 runs it alone.
-  constexpr bool Elect = Q4;
+  // for D = 64), lane 0 runs it alone.  Spans, whose issuers do more a tile, take the elected
+  // lane: the same chunks over all keys 570 -> 525 us, over 1024 keys 168 -> 157 us, 777
+  // tokens at D = 64 over 1024 keys 33 -> 28 us.
+  constexpr bool Elect = Parts;
   auto one = [&] { return !Elect || elect_one(); };
   auto join = [&] {
     if constexpr (Elect) __syncwarp();
@@ -494,7 +763,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : warp_wait(bar, parity, abort_flag, lim);
   };
 
-  if (warp == 0) {
+  if (Span && warp == 0) {
+    if constexpr (Span) span_producer<D, G>(&tm_q, &tm_k, NSL == 2 ? &tm_vp : &tm_v, p, smem, bars, n_items);
+  } else if (warp == 0) {
     // ---------------------------------------------------------------- work queue + TMA producer
     // The whole warp runs this loop: lane 0 owns the queue, the waits and the
     // barrier bookkeeping; a tile's K boxes -- one per (page, 64-column slab)
@@ -542,7 +813,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
       return true;
     };
-    const int part_tiles = Parts ? p.hdr[H_CH_TILES] : 0;
+    const int part_tiles = Q4 ? p.hdr[H_CH_TILES] : 0;
     int kt0 = 0;                // the part's first KV tile
     int parts_run[2] = {0, 0};  // parts run by each softmax group so far
     while (ok) {
@@ -559,12 +830,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       it.row = -1;
       if (item < n_items) {
         // (chunk row index and, above it, the part; KV head << 16 | pair from the last)
-        const int2 kl = __ldg((Parts && part_tiles > 0 ? ChunkParts(p).items : p.ch_items) + item);
-        const int k = Parts ? kl.x & 0xffff : kl.x;
+        const int2 kl = __ldg((Q4 && part_tiles > 0 ? ChunkParts(p).items : p.ch_items) + item);
+        const int k = Q4 ? kl.x & 0xffff : kl.x;
         it.row = __ldg(p.ch_rows + k);
         it.tb = __ldg(p.cu + it.row);
         const int d = __ldg(p.cu + it.row + 1) - it.tb;
-        it.c = Span ? span_start(p, it.row) : __ldg(p.q_start + it.row);
+        it.c = __ldg(p.q_start + it.row);
         const int n_qt = (d + TPT - 1) / TPT;
         const int n_pair = (n_qt + 1) >> 1;
         // the prologue ordered the row's items (KV head by KV head, or longest pair
@@ -577,54 +848,13 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           const bool has = qt < n_qt;
           it.tok0[t] = has ? qt * TPT : 0;
           it.ntok[t] = has ? min(TPT, d - qt * TPT) : 0;
-          if constexpr (Span) {
-            // the pair's keys from the page that holds its first query's first key
-            const int lo = span_first(p, it.c + (p.fixed_span ? 0 : it.tok0[t]));
-            if (t == 0) pt.key0 = lo & ~(kPage - 1);
-            if (t == 0) pt.unseen = lo - pt.key0;
-            pt.first[t] = (lo - pt.key0) / kKeys;
-            it.kv_end[t] = has ? it.c + (p.fixed_span ? 1 : it.tok0[t] + it.ntok[t]) - pt.key0 : 0;
-          } else {
-            it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
-          }
+          it.kv_end[t] = has ? it.c + it.tok0[t] + it.ntok[t] : 0;
           it.nkt[t] = (it.kv_end[t] + kKeys - 1) / kKeys;
-          if constexpr (!Parts) {
+          if constexpr (!Q4) {
             it.t0[t] = t_run[t];
             t_run[t] += it.nkt[t];
           }
           it.n_kt = max(it.n_kt, it.nkt[t]);
-        }
-        if constexpr (Span) {
-          pt.ns = 1;
-          kt0 = 0;
-          if (it.n_kt == 0) {  // a row without keys: zeros, by this warp
-            if (part_tiles == 0 || (kl.x >> 16) == 0) zero_rows<D, G>(p, it, lane);
-            continue;
-          }
-          int n = it.n_kt;  // tiles of the part, or of the whole item
-          if (part_tiles > 0) {
-            const int ns_row = span_parts(p, it.c, d, TPT, part_tiles);
-            n = (it.n_kt + ns_row - 1) / ns_row;
-            pt.ns = (it.n_kt + n - 1) / n;
-            pt.part = kl.x >> 16;
-            pt.item0 = item - pt.part;
-            if (pt.part >= pt.ns) continue;  // another pair of the row has more tiles
-            kt0 = pt.part * n;
-            pt.key0 += kt0 * kKeys;
-            if (kt0 > 0) pt.unseen = 0;
-          }
-          it.n_kt = 0;
-          for (int t = 0; t < 2; ++t) {
-            it.kv_end[t] = it.ntok[t] > 0 ? it.kv_end[t] - kt0 * kKeys : 0;
-            pt.first[t] = max(0, pt.first[t] - kt0);
-            const int end = it.kv_end[t] > 0 ? min(n, (it.kv_end[t] + kKeys - 1) / kKeys) : 0;
-            it.nkt[t] = max(0, end - pt.first[t]);
-            it.n_kt = max(it.n_kt, end);
-            pt.parity[t] = parts_run[t] & 1;
-            parts_run[t] += pt.ns > 1 && it.ntok[t] > 0;
-            it.t0[t] = t_run[t];
-            t_run[t] += it.nkt[t];
-          }
         }
         if constexpr (Q4) {
           pt.ns = 1;
@@ -655,7 +885,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       }
       if (lane == 0) {
         bars->items[slot] = it;
-        if constexpr (Parts) bars->parts[slot] = pt;
+        if constexpr (Q4) bars->parts[slot] = pt;
         mbar_arrive(&bars->item_full[slot]);
       }
       ++n_done;
@@ -668,7 +898,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       const int nq = it.ntok[1] > 0 ? 2 : 1;
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
-        if constexpr (Parts) bars->q_asked = n_done;
+        if constexpr (Q4) bars->q_asked = n_done;
       }
       __syncwarp();
       if (lane < nq * NSL) {
@@ -677,7 +907,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
                     &bars->q_full);
       }
       const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-      const int32_t* btrow = row_table(p, it.row) + (Q4 ? kt0 * kTilePages : Span ? pt.key0 / kPage : 0);
+      const int32_t* btrow = row_table(p, it.row) + (Q4 ? kt0 * kTilePages : 0);
       const int n_pages = (kv_max + kPage - 1) / kPage;
       // lane L < 4 holds the page id of page L of the current tile; the next tile's is in flight
       int pg_cur = lane < kTilePages && lane < n_pages ? __ldg(btrow + lane) : 0;
@@ -765,7 +995,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     const int t = warp == 1 ? 0 : 1;
     if (Elect || lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(sbase + C::Q_OFF + t * C::Q_BYTES, 16, 1024);
-      const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, 1024);
+      // K's 64-column slabs, and its groups of 8 keys: slab after slab, or (spans, D = 128) the slabs of a group together
+      constexpr int kKSlab = Span && NSL == 2 ? 1024 : kKVSlab, kKGroup = Span && NSL == 2 ? 2048 : 1024;
+      const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, kKGroup);
       const uint32_t s_tm = tmem + C::S_COL + 2 * t * 64;
       constexpr uint32_t idesc_full = idesc_bf16_f32(128, kKeys, 0);
       int bk = 0;        // K stage of the next tile
@@ -808,7 +1040,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * kQSlab + (kk & 3) * 32) >> 4);
-                const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * kKVSlab + (kk & 3) * 32) >> 4);
+                const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * kKSlab + (kk & 3) * 32) >> 4);
                 mma_bf16_ss(dcol, qdesc + qo, kd + ko, idesc_s, kk > 0 ? 1u : 0u);
               }
               mma_commit(&bars->s_full[t][b]);
@@ -988,15 +1220,17 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             sv[32 + j] = __uint_as_float(r1[j]);
           }
           const int key0 = kt * kKeys;
-          if (key0 + kKeys - 1 > warp_min_pos) {  // diagonal or ragged tile: causal mask (warp-uniform test)
+          if constexpr (Span) {  // a tile at either edge of the warp's spans
+            if (key0 + kKeys - 1 > warp_min_pos || key0 < warp_max_lo) {
+              const unsigned at = static_cast<unsigned>(key0 - lo), seen = static_cast<unsigned>(pos - lo);
+#pragma unroll
+              for (int j = 0; j < 64; ++j)
+                if (at + j > seen) sv[j] = -INFINITY;
+            }
+          } else if (key0 + kKeys - 1 > warp_min_pos) {  // diagonal or ragged tile: causal mask (warp-uniform test)
 #pragma unroll
             for (int j = 0; j < 64; ++j)
               if (key0 + j > pos) sv[j] = -INFINITY;
-          }
-          if (Span && key0 < warp_max_lo) {  // the window's lower edge
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (key0 + j < lo) sv[j] = -INFINITY;
           }
           // row max: four chains of three-input maxima
           float mxa[4];
@@ -1068,6 +1302,8 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         tc_fence_after();
         if (Parts && bars->parts[slot].ns > 1) {
           ok = end_part<D, G, Kind>(p, bars, slot, t, m_use, l, tO, abort_flag, lim);
+        } else if constexpr (Span) {
+          store_rows<D, G>(p, tm_o_p, smem + C::SMEM + (warp - 2) * 4096, it, t, quad, tO, 1.f / l);
         } else {
           const float inv = (Q4 ? 4.f : 1.f) / l;
           const bool valid_row = Parts ? r / G < it.ntok[t] : valid;  // read again: a register less in the loop
@@ -1110,6 +1346,9 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) atomicOr(p.hdr + H_STATUS, MS_STATUS_TIMEOUT);
+    }
+    if constexpr (Span) {
+      if (lane == 0) bulk_wait_all();  // of the stores
     }
   }
   if constexpr (Q4) {

@@ -186,6 +186,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst_smem, const void* tmap, in
       : "memory");
 }
 
+// Tile in shared memory (complete to the async proxy) -> global, as a bulk group of its own; then:
+// until all groups of this thread have read their tiles, and until they are written.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src_smem, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+               "r"(smem_u32(src_smem)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
