@@ -10,8 +10,13 @@
 #include "append_rope.cuh"
 #include "device_state.cuh"
 #include "mixed_step.h"
+#include "ptx.cuh"
 
 namespace {
+
+using ms::fadd2;
+using ms::ffma2;
+using ms::fmul2;
 
 constexpr int kMaxPairs = 64;  // rotary_dim / 2 at most
 
@@ -55,60 +60,92 @@ uint64_t turns_fixed(double f) {
 // rounding of the cubic term's factors: 3.5 of them, 2^-24 each, of at most 0.08 beside a step of
 // 2^-24, so a result is off by at most 0.8 of a step.  (FP64 has 1/64 of the fp32 rate on this GPU.)
 
+// The amplitude m in two floats, and m times the Taylor coefficients.
+struct Series {
+  float hi, lo, s3, s5, s7, s9, c2, c4, c6, c8, c10;
+};
+
 struct TableArgs {
   uint64_t turns[kMaxPairs];
   float* cos_tab;
   float* sin_tab;
   int64_t first;  // position of row 0
   int32_t n, half;
-  float amp_hi, amp_lo;  // amplitude in two floats
+  Series m;
 };
 
-// s = a + b rounded, and what the rounding left out (|a| >= |b|)
-__device__ __forceinline__ float2 two_sum_ordered(float a, float b) {
-  const float s = __fadd_rn(a, b);
-  return make_float2(s, __fsub_rn(b, __fsub_rn(s, a)));
+// Two pairs at a time, in the halves of float2s: a packed operation of two products or sums is one instruction,
+// and instructions are what the kernel spends beside its 8 bytes a pair (131072 rows of 64 pairs: 19.1 us one pair at a
+// time, 13.4 now, 0.74 of the measured copy rate; with an amplitude 23.1, and 16.7 where cosines and sines were
+// multiplied at the end, 14.6 with it in the series).
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+
+// The whole-number part of an angle, t of 2^64 turns: u holds the nearest quarter turn in its two top bits, and the
+// rest (less an eighth of a turn) below them; upper and lower are the rest's upper 22 bits, signed, and next 23.
+struct Rest {
+  uint32_t u;
+  float upper, lower;
+};
+
+__device__ __forceinline__ Rest split_turns(uint64_t t) {
+  Rest r;
+  r.u = static_cast<uint32_t>(t >> 32) + 0x20000000u;  // an eighth of a turn on: 4 quarters wrap to 0
+  // whole numbers below 2^23 become floats as the mantissa of one whose step is 1
+  r.upper = __uint_as_float(((r.u >> 8) & 0x3fffffu) | 0x4b000000u) - (8388608.f + 2097152.f);
+  r.lower = __uint_as_float((__funnelshift_r(static_cast<uint32_t>(t), r.u, 17) & 0x7fffffu) | 0x4b000000u) - 8388608.f;
+  return r;
 }
 
-// cosine and sine of 2 pi t / 2^64, each as a sum of two floats
-__device__ __forceinline__ void cos_sin_turns(uint64_t t, float2& cos2, float2& sin2) {
-  const uint32_t quarter = static_cast<uint32_t>((t + (uint64_t{1} << 61)) >> 62);  // 0 .. 3 (4 wraps to 0)
-  const int64_t rest = static_cast<int64_t>(t - (static_cast<uint64_t>(quarter) << 62));  // in [-2^61, 2^61)
-  // 2 pi rest / 2^64 from its upper 22 and next 24 bits
-  const float a = static_cast<float>(static_cast<int32_t>(rest >> 40)) * 0x1p-24f;
-  const float b = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(rest >> 16) & 0xffffffu)) * 0x1p-48f;
+// Cosine and sine of two angles, rounded, times an amplitude m.hi + m.lo (1 + 0 where not Scaled): m times the series,
+// with m in its coefficients and the leading terms' products in two floats too.
+template <bool Scaled>
+__device__ __forceinline__ void cos_sin(uint64_t t0, uint64_t t1, const Series& m, float2& c_out, float2& s_out) {
+  const Rest r0 = split_turns(t0), r1 = split_turns(t1);
+  // x = 2 pi rest, |x| <= pi / 4, as the two floats x and y
   constexpr float kHi = 6.28318548202514648f, kLo = -1.74845553146951715e-7f;  // 2 pi
-  const float p = __fmul_rn(a, kHi);
-  const float q = __fmaf_rn(b, kHi, __fmaf_rn(a, kLo, __fmaf_rn(a, kHi, -p)));
-  const float2 x = fabsf(p) >= fabsf(q) ? two_sum_ordered(p, q) : two_sum_ordered(q, p);
-  const float z = __fmul_rn(x.x, x.x);
-  const float z_lo = __fmaf_rn(2.f * x.x, x.y, __fmaf_rn(x.x, x.x, -z));
+  const float2 a = make_float2(r0.upper, r1.upper), b = make_float2(r0.lower, r1.lower);
+  const float2 p = fmul2(a, splat(kHi * 0x1p-24f));
+  const float2 q = ffma2(b, splat(kHi * 0x1p-47f), ffma2(a, splat(kLo * 0x1p-24f), ffma2(a, splat(kHi * 0x1p-24f), neg2(p))));
+  // their sum rounded, and what the rounding left out (|p| >= |q|, or p = 0)
+  const float2 x = fadd2(p, q), y = fadd2(q, neg2(fadd2(x, neg2(p))));
+  const float2 z = fmul2(x, x);
+  const float2 z_lo = ffma2(fadd2(x, x), y, ffma2(x, x, neg2(z)));  // x^2 and what its rounding left out
   // sin x = x - x^3 / 3! + ...
-  float ps = __fmaf_rn(z, 1.f / 362880.f, -1.f / 5040.f);
-  ps = __fmaf_rn(z, ps, 1.f / 120.f);
-  ps = __fmaf_rn(z, ps, -1.f / 6.f);
-  const float2 s = two_sum_ordered(x.x, __fmaf_rn(__fmul_rn(z, x.x), ps, x.y));
+  float2 ps = ffma2(z, splat(m.s9), splat(m.s7));
+  ps = ffma2(z, ps, splat(m.s5));
+  ps = ffma2(z, ps, splat(m.s3));
+  float2 s_hi = x, s_left = y;
+  if constexpr (Scaled) {
+    s_hi = fmul2(x, splat(m.hi));
+    s_left = ffma2(y, splat(m.hi), ffma2(x, splat(m.lo), ffma2(x, splat(m.hi), neg2(s_hi))));
+  }
+  const float2 s = fadd2(s_hi, ffma2(fmul2(z, x), ps, s_left));
   // cos x = 1 - x^2 / 2 + x^4 / 4! - ...
-  float pc = __fmaf_rn(z, -1.f / 3628800.f, 1.f / 40320.f);
-  pc = __fmaf_rn(z, pc, -1.f / 720.f);
-  pc = __fmaf_rn(z, pc, 1.f / 24.f);
-  const float2 c0 = two_sum_ordered(1.f, -0.5f * z);
-  const float2 c = two_sum_ordered(c0.x, __fmaf_rn(__fmul_rn(z, z), pc, __fmaf_rn(-0.5f, z_lo, c0.y)));
+  float2 pc = ffma2(z, splat(m.c10), splat(m.c8));
+  pc = ffma2(z, pc, splat(m.c6));
+  pc = ffma2(z, pc, splat(m.c4));
+  const float2 c_hi = ffma2(z, splat(m.c2), splat(m.hi));
+  float2 c_left = ffma2(z_lo, splat(m.c2), ffma2(z, splat(m.c2), fadd2(splat(m.hi), neg2(c_hi))));
+  if constexpr (Scaled) c_left = fadd2(c_left, ffma2(z, splat(-0.5f * m.lo), splat(m.lo)));
+  const float2 c = fadd2(c_hi, ffma2(fmul2(z, z), pc, c_left));
   // by quarters: (c, s), (-s, c), (-c, -s), (s, -c)
-  const float sign_c = quarter == 1 || quarter == 2 ? -1.f : 1.f, sign_s = quarter >= 2 ? -1.f : 1.f;
-  const float2 uc = quarter & 1 ? s : c, us = quarter & 1 ? c : s;
-  cos2 = make_float2(sign_c * uc.x, sign_c * uc.y);
-  sin2 = make_float2(sign_s * us.x, sign_s * us.y);
-}
-
-__device__ __forceinline__ float times(float2 v, float hi, float lo) {
-  const float p = __fmul_rn(v.x, hi);
-  return __fadd_rn(p, __fmaf_rn(v.y, hi, __fmaf_rn(v.x, lo, __fmaf_rn(v.x, hi, -p))));
+  const auto turn = [](uint32_t u, float cc, float ss, float& co, float& so) {
+    const bool odd = (u & 0x40000000u) != 0;
+    const float x = odd ? ss : cc, y = odd ? cc : ss;
+    co = __uint_as_float(__float_as_uint(x) ^ ((u + 0x40000000u) & 0x80000000u));
+    so = __uint_as_float(__float_as_uint(y) ^ (u & 0x80000000u));
+  };
+  turn(r0.u, c.x, s.x, c_out.x, s_out.x);
+  turn(r1.u, c.y, s.y, c_out.y, s_out.y);
 }
 
 // A thread makes four neighbouring pairs of every row `rows` apart and stores 16 bytes of each table.
 template <bool Scaled>
 __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant__ TableArgs a) {
+  __shared__ uint64_t turns[kMaxPairs];  // lanes read different ones: from the parameters one after another
+  if (threadIdx.x < kMaxPairs) turns[threadIdx.x] = a.turns[threadIdx.x];
+  __syncthreads();
   const int quads = a.half >> 2, per_block = 256 / quads;  // rows of the block at a time
   const int r = threadIdx.x / quads, i0 = (threadIdx.x - r * quads) * 4;
   if (r >= per_block) return;
@@ -117,23 +154,19 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant
   uint64_t t[4], step[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t f = a.turns[i0 + j];
+    const uint64_t f = turns[i0 + j];
     t[j] = static_cast<uint64_t>(a.first + row) * f;
     step[j] = static_cast<uint64_t>(rows) * f;
   }
   for (; row < a.n; row += rows) {
-    float c[4], s[4];
+    float2 c[2], s[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float2 c2, s2;
-      cos_sin_turns(t[j], c2, s2);
-      c[j] = Scaled ? times(c2, a.amp_hi, a.amp_lo) : c2.x;
-      s[j] = Scaled ? times(s2, a.amp_hi, a.amp_lo) : s2.x;
-      t[j] += step[j];
-    }
+    for (int j = 0; j < 2; ++j) cos_sin<Scaled>(t[2 * j], t[2 * j + 1], a.m, c[j], s[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] += step[j];
     const int64_t at = row * a.half + i0;
-    *reinterpret_cast<float4*>(a.cos_tab + at) = make_float4(c[0], c[1], c[2], c[3]);
-    *reinterpret_cast<float4*>(a.sin_tab + at) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(a.cos_tab + at) = make_float4(c[0].x, c[0].y, c[1].x, c[1].y);
+    *reinterpret_cast<float4*>(a.sin_tab + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
   }
 }
 
@@ -145,7 +178,11 @@ __global__ void __launch_bounds__(256) rotary_table_kernel(const __grid_constant
 // chunks of every head and keeps the token's cosines and sines for them.  In halves a lane's
 // chunks are a pair's two sides, R / 2 apart, or, past the rotary part, two chunks that are
 // copied; in neighbouring pairs a chunk holds four whole pairs.  It has to move
-// (4 H_q + 8 H_kv) D bytes a token and 4 R of the tables.
+// (4 H_q + 8 H_kv) D bytes a token and 4 R of the tables: 203 MB for 8192 tokens of 32 / 8 heads,
+// D = 128, R = 64, in 34.8 us, 0.86 of the measured copy rate; 6000 tokens of 8 KV heads alone 10.2
+// us, 0.71 (a replayed graph, inputs past L2).  What counts is bytes in flight: 64 to 80 KB an SM, by
+// two groups of heads ahead in small blocks (four ahead, in blocks of 256: 41 us; one: 37.7; loads
+// marked as streaming: 35.6; several warps a token, whose tables then count again: 50).
 
 struct RotaryArgs {
   AppendArgs a;
@@ -155,7 +192,8 @@ struct RotaryArgs {
 };
 
 enum { kNoTurn = 0, kHalves = 1, kPairs = 2 };
-constexpr int kGroupsAhead = 4;  // head groups whose words a lane asks for before it stores the first
+constexpr int kRotaryThreads = 128;
+constexpr int kGroupsAhead = 2;  // head groups whose words a lane asks for before it stores the first
 
 // four neighbouring pairs of a 16-byte chunk, as rotate8 rounds
 __device__ __forceinline__ uint4 rotate_pairs(const uint4& w, const float* c, const float* s) {
@@ -173,13 +211,13 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4& w, const float* c, co
 }
 
 template <int D, int Turn>
-__global__ void __launch_bounds__(kAppendThreads) append_rotary_kernel(const __grid_constant__ RotaryArgs args) {
+__global__ void __launch_bounds__(kRotaryThreads) append_rotary_kernel(const __grid_constant__ RotaryArgs args) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const AppendArgs& a = args.a;
   constexpr int LPH = D / 16, HPW = 32 / LPH;  // lanes to a head, heads at a time
   const int heads = a.H_q + 2 * a.H_kv, groups = (heads + HPW - 1) / HPW;
   const int lane = threadIdx.x & 31, part = lane % LPH;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kRotaryThreads + threadIdx.x) >> 5;
   const int t = static_cast<int>(w / args.chunks);
   if (t >= a.T) return;
   const int g0 = static_cast<int>(w % args.chunks) * args.span, g1 = min(groups, g0 + args.span);
@@ -224,7 +262,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rotary_kernel(const __g
 #pragma unroll
     for (int u = 0; u < kGroupsAhead; ++u) {
       const int h = (g + u) * HPW + lane / LPH;
-      if (g + u >= g1 || skipped(h)) continue;
+      if (g + u >= g1 || h >= heads) continue;
       const __nv_bfloat16* src = h < a.H_q            ? a.q + t * args.q_stride + h * D
                                  : h < a.H_q + a.H_kv ? a.k + t * args.k_stride + (h - a.H_q) * D
                                                       : a.v + t * args.v_stride + (h - a.H_q - a.H_kv) * D;
@@ -314,7 +352,7 @@ extern "C" MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, con
 extern "C" MS_API int ms_rotary_table_device(const double* freq, int32_t pairs, double amplitude, int32_t first_pos, int32_t n,
                                              float* cos_tab, float* sin_tab, ms_stream_t stream) {
   if (freq == nullptr || pairs < 4 || pairs % 4 != 0 || pairs > kMaxPairs || first_pos < 0 || n < 0 ||
-      static_cast<int64_t>(first_pos) + n > (int64_t{1} << 31) || !std::isfinite(amplitude) || std::fabs(amplitude) > 0x1p100)
+      static_cast<int64_t>(first_pos) + n > (int64_t{1} << 31) || !(amplitude == 0.0 || (std::fabs(amplitude) >= 0x1p-40 && std::fabs(amplitude) <= 0x1p40)))
     return MS_ERR_ARG;
   for (int i = 0; i < pairs; ++i)
     if (!(std::fabs(freq[i]) <= 1024.0)) return MS_ERR_ARG;
@@ -330,10 +368,20 @@ extern "C" MS_API int ms_rotary_table_device(const double* freq, int32_t pairs, 
   a.first = first_pos;
   a.n = n;
   a.half = pairs;
-  a.amp_hi = static_cast<float>(amplitude);
-  a.amp_lo = static_cast<float>(amplitude - static_cast<double>(a.amp_hi));
+  const auto times = [&](double coefficient) { return static_cast<float>(amplitude * coefficient); };
+  a.m.hi = times(1.0);
+  a.m.lo = static_cast<float>(amplitude - static_cast<double>(a.m.hi));
+  a.m.s3 = times(-1.0 / 6.0);
+  a.m.s5 = times(1.0 / 120.0);
+  a.m.s7 = times(-1.0 / 5040.0);
+  a.m.s9 = times(1.0 / 362880.0);
+  a.m.c2 = -0.5f * a.m.hi;  // exactly: what c_hi leaves out is taken from it
+  a.m.c4 = times(1.0 / 24.0);
+  a.m.c6 = times(-1.0 / 720.0);
+  a.m.c8 = times(1.0 / 40320.0);
+  a.m.c10 = times(-1.0 / 3628800.0);
   const int per_block = 256 / (pairs / 4);
-  const int64_t need = (static_cast<int64_t>(n) + per_block - 1) / per_block, most = static_cast<int64_t>(sms) * 8;
+  const int64_t need = (static_cast<int64_t>(n) + per_block - 1) / per_block, most = static_cast<int64_t>(sms) * 4;
   const unsigned blocks = static_cast<unsigned>(need < most ? need : most);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (amplitude == 1.0)
@@ -398,7 +446,7 @@ extern "C" MS_API int ms_kv_append_rotary(const void* q, int64_t q_stride, const
   args.span = static_cast<int32_t>((groups + chunks - 1) / chunks);
   args.chunks = (groups + args.span - 1) / args.span;
   const int64_t warps = static_cast<int64_t>(T) * args.chunks;
-  const int64_t blocks64 = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const int64_t blocks64 = (warps + kRotaryThreads / 32 - 1) / (kRotaryThreads / 32);
   if (blocks64 > INT32_MAX) return MS_ERR_ARG;
   const unsigned blocks = static_cast<unsigned>(blocks64);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -408,6 +456,6 @@ extern "C" MS_API int ms_kv_append_rotary(const void* q, int64_t q_stride, const
                                : (R == 0        ? append_rotary_kernel<64, kNoTurn>
                                   : interleaved ? append_rotary_kernel<64, kPairs>
                                                 : append_rotary_kernel<64, kHalves>);
-  kernel<<<blocks, kAppendThreads, 0, st>>>(args);
+  kernel<<<blocks, kRotaryThreads, 0, st>>>(args);
   return cudaGetLastError() == cudaSuccess ? MS_OK : MS_ERR_CUDA;
 }

@@ -577,6 +577,7 @@ MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, const ms_rotar
  * the exact one.
  *   freq      host double [pairs], |freq| <= 1024; read before the call returns
  *   pairs     R / 2: 4 .. 64, a multiple of 4
+ *   amplitude 0, or of a magnitude of 2^-40 .. 2^40
  *   cos_tab, sin_tab  device fp32 [n, pairs], 16-byte aligned
  * Errors: MS_ERR_ARG (also first_pos + n > 2^31), MS_ERR_CUDA. */
 MS_API int ms_rotary_table_device(const double* freq, int32_t pairs, double amplitude, int32_t first_pos, int32_t n,

@@ -113,7 +113,7 @@ def test_table_refusals(ms):
     big = np.full(64, 1025.0)
     for change in ({"freq": None}, {"pairs": 0}, {"pairs": 6}, {"pairs": 68}, {"amp": float("nan")}, {"first": -1}, {"n": -1},
                    {"first": 2 ** 31 - 5}, {"cos": None}, {"sin": P + 4}, {"freq": inf.ctypes.data}, {"freq": big.ctypes.data},
-                   {"amp": 1e31}):
+                   {"amp": 1e31}, {"amp": 1e-13}, {"amp": float("inf")}):
         a = {**good, **change}
         assert call(a["freq"], a["pairs"], a["amp"], a["first"], a["n"], a["cos"], a["sin"], None) == ms.MS_ERR_ARG, change
     assert call(f.ctypes.data, 64, 1.0, 0, 0, None, None, None) == ms.MS_OK  # no rows
