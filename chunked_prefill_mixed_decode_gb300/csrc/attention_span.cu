@@ -19,12 +19,16 @@
 
 namespace {
 
+// Tensor maps of the chunk rows: K, V and both by groups of 8 keys, and the output.
+struct SpanMaps {
+  CUtensorMap k, v, kv, out;
+};
+
 template <int D, int G>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attention_span_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vp,
-                          const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_kc,
-                          const __grid_constant__ CUtensorMap tm_o, AttnParams p) {
+                          const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ SpanMaps m, AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -53,7 +57,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   for (int ph = 0; ph < 2; ++ph) {
     const bool chunk = (ph == 0) == chunk_first;
     if (chunk && n_ch_items > 0) {
-      chunk_phase<D, G, kSpan>(&tm_q, &tm_kc, &tm_v, &tm_vp, p, smem, tmem, &tm_o);
+      chunk_phase<D, G, kSpan>(&tm_q, &m.k, &m.v, &m.kv, p, smem, tmem, &m.out);
       tc_fence_before();
       __syncthreads();
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
@@ -80,14 +84,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 }
 
 template <int D, int G>
-int launch_span(const AttnPlan& L, const CUtensorMap& tkc, const CUtensorMap& to, cudaStream_t st) {
+int launch_span(const AttnPlan& L, const SpanMaps& m, cudaStream_t st) {
   constexpr int chunk = ChCfg<D>::SMEM + kSoftmaxWarps * 4096;  // and the stages of store_rows
   constexpr int smem = chunk > DecCfg<D, G>::SMEM ? chunk : DecCfg<D, G>::SMEM;
   static_assert(smem <= 232448, "attention kernel exceeds the per-CTA shared-memory limit");
   const int slot = (D == 128 ? 4 : 0) + (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3);  // one bit per instance
   if (ensure_smem_limit(attention_span_kernel<D, G>, slot, smem) != MS_OK) return MS_ERR_CUDA;
   if (launch_dependent(attention_span_kernel<D, G>, dim3(L.p.num_sms), dim3(kChunkThreads), smem, st, L.tq, L.tk, L.tv,
-                       L.tvp, L.tkp, tkc, to, L.p) != cudaSuccess)
+                       L.tvp, L.tkp, m, L.p) != cudaSuccess)
     return MS_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MS_OK : MS_ERR_CUDA;
 }
@@ -110,32 +114,47 @@ int span_call(const void* q, const void* k_cache, const void* v_cache, int32_t n
   L.p.fixed_span = window == 0 ? 1 : 0;
   L.p.window = window == 0 ? INT32_MAX : window;
   set_parts_room(&L.p, workspace, ws_bytes, key_total);
-  CUtensorMap tkc = L.tk;
-  if (D == 128) {
-    // K pages of the chunk tiles as one box each, laid out group by group of 8 keys, both 64-column slabs of
-    // a group together: the groups of a tile's pages are then one stride apart, as the S MMA's descriptor has it
-    const cuuint64_t dims[4] = {64, 8, 2, 2 * static_cast<cuuint64_t>(num_pages) * H_kv};
-    const cuuint64_t strides[3] = {256, 128, 8 * 256};
+  // K and V of the chunk tiles, by groups of 8 keys and 64-column slabs (SpanTile): maps of one pool, and of both
+  // where the pools' distance is a stride that a map can have
+  SpanMaps m;
+  const EncodeTiledFn enc = get_encode_fn();
+  const cuuint64_t slabs = static_cast<cuuint64_t>(D) / 64, groups = 2 * static_cast<cuuint64_t>(num_pages) * H_kv;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  {
+    const cuuint64_t dims[4] = {64, 8, D == 128 ? slabs : groups, groups}, strides[3] = {row, D == 128 ? 128 : 8 * row, 8 * row};
     const cuuint32_t box[4] = {64, 8, 2, 2};
-    if (!encode_bf16(get_encode_fn(), &tkc, k_cache, 4, dims, strides, box)) return MS_ERR_ARG;
+    const int rank = D == 128 ? 4 : 3;
+    if (!encode_bf16(enc, &m.k, k_cache, rank, dims, strides, box) || !encode_bf16(enc, &m.v, v_cache, rank, dims, strides, box))
+      return MS_ERR_ARG;
   }
-  CUtensorMap to;  // 32 rows (32 / G tokens of G heads) of 64 columns of the output
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(k_cache), va = reinterpret_cast<uintptr_t>(v_cache);
+  const uintptr_t apart = ka < va ? va - ka : ka - va;  // both 16-byte aligned
+  m.kv = m.k;
+  if (apart != 0 && apart < (uintptr_t{1} << 40)) {
+    const void* low = ka < va ? k_cache : v_cache;
+    const cuuint64_t dims5[5] = {64, 8, slabs, 2, groups}, strides5[4] = {row, 128, apart, 8 * row};
+    const cuuint64_t dims4[4] = {64, 8, 2, groups}, strides4[3] = {row, apart, 8 * row};
+    const cuuint32_t box[5] = {64, 8, 2, 2, 2};
+    if (D == 128 ? encode_bf16(enc, &m.kv, low, 5, dims5, strides5, box) : encode_bf16(enc, &m.kv, low, 4, dims4, strides4, box))
+      L.p.kv_form = ka < va ? kKvKFirst : kKvVFirst;
+  }
+  // 32 rows (32 / G tokens of G heads) of 64 columns of the output
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(num_tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(H_q) * D * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(L.p.G), static_cast<cuuint32_t>(32 / L.p.G)};
-  if (!encode_bf16(get_encode_fn(), &to, out, 3, dims, strides, box)) return MS_ERR_ARG;
+  if (!encode_bf16(enc, &m.out, out, 3, dims, strides, box)) return MS_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = launch_prologue<false, true>(L.p, st);
   if (rc != MS_OK) return rc;
   switch (D * 100 + L.p.G) {
-    case 6401: return launch_span<64, 1>(L, tkc, to, st);
-    case 6402: return launch_span<64, 2>(L, tkc, to, st);
-    case 6404: return launch_span<64, 4>(L, tkc, to, st);
-    case 6408: return launch_span<64, 8>(L, tkc, to, st);
-    case 12801: return launch_span<128, 1>(L, tkc, to, st);
-    case 12802: return launch_span<128, 2>(L, tkc, to, st);
-    case 12804: return launch_span<128, 4>(L, tkc, to, st);
-    default: return launch_span<128, 8>(L, tkc, to, st);
+    case 6401: return launch_span<64, 1>(L, m, st);
+    case 6402: return launch_span<64, 2>(L, m, st);
+    case 6404: return launch_span<64, 4>(L, m, st);
+    case 6408: return launch_span<64, 8>(L, m, st);
+    case 12801: return launch_span<128, 1>(L, m, st);
+    case 12802: return launch_span<128, 2>(L, m, st);
+    case 12804: return launch_span<128, 4>(L, m, st);
+    default: return launch_span<128, 8>(L, m, st);
   }
 }
 

@@ -104,7 +104,12 @@ struct AttnParams {
   // joins the softmax's sum without a value, or nullptr.
   const float* sinks;
   int32_t window, fixed_span;
+  int32_t kv_form;  // KvForm
 };
+
+// How the chunk tiles of a span get K and V (chunk_phase.cuh): a box of each a page, or one of both, the pool at the
+// lower address first.
+enum KvForm { kKvApart = 0, kKvKFirst = 1, kKvVFirst = 2 };
 
 // Where the parts' records lie: sums of O first ([part][row][D]), (max, sum)
 // ([part][row]), the parts' table, then counters per item and Q tile.
@@ -1278,6 +1283,7 @@ inline int step_setup(const void* q_rot, const void* k_cache, const void* v_cach
   p.sinks = nullptr;
   p.window = INT32_MAX;
   p.fixed_span = 0;
+  p.kv_form = kKvApart;
   if (device_rates(&p.sm_mhz, &p.hbm_gbs, &p.l2_bytes) != MS_OK) return MS_ERR_CUDA;
   return MS_OK;
 }

@@ -417,7 +417,23 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
   return true;
 }
 
-// ---- spans: the producer
+// ---- spans: K and V tiles, and the producer
+
+// A K/V stage of a tile.  A group is 8 keys (rows of 128 bytes) by 64-column slabs, 1 KB a slab; the groups of K, and
+// those of V, are `group` bytes apart, as the descriptors of their MMAs want them: a K tile has its keys in groups of
+// one stride, a k-step of V is two groups.  Where the pools' distance fits a tensor map (`paired`), a page of K and of
+// V is one box, group by group with K's and V's slabs side by side; else a box each.
+template <int D>
+struct SpanTile {
+  static constexpr int NSL = D / 64;
+  uint32_t group, k, v;  // bytes: between groups, and from the stage's start to K and to V
+  __device__ __forceinline__ explicit SpanTile(const AttnParams& p) {
+    const bool paired = p.kv_form != kKvApart;
+    group = (paired ? 2 : 1) * NSL * 1024;
+    k = p.kv_form == kKvVFirst ? NSL * 1024 : 0;
+    v = p.kv_form == kKvVFirst ? 0 : paired ? NSL * 1024 : NSL * 8192;
+  }
+};
 
 // Warp 0 of a chunk phase over spans: queue and TMA as in chunk_phase, which has the causal form.  At
 // D = 128 a page of K is one 4 KB box too, laid out by groups of 8 keys with both 64-column slabs of a group
@@ -428,40 +444,25 @@ __device__ __noinline__ bool end_part(const AttnParams& p, ChBars* bars, int slo
 // three K/V stages: 539 against 525, over 64 keys 57 us either way; at D = 64, beside six stages, no change.
 template <int D, int G>
 __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                              const AttnParams& p, uint8_t* smem, ChBars* bars, int n_items) {
+                                              const CUtensorMap* tm_kv, const AttnParams& p, uint8_t* smem, ChBars* bars, int n_items) {
   using C = ChCfg<D>;
-  constexpr int NSL = C::NSL, TPT = 128 / G, KVS = C::KVS, kVPage = NSL * 2048;
+  constexpr int NSL = C::NSL, TPT = 128 / G, KVS = C::KVS;
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort;
   const uint64_t lim = p.wait_limit_ns;
+  const SpanTile<D> lay(p);
+  const bool paired = p.kv_form != kKvApart;
   if (lane == 0) {
     prefetch_tmap(tm_q);
-    prefetch_tmap(tm_k);
-    prefetch_tmap(tm_v);
+    prefetch_tmap(paired ? tm_kv : tm_k);
+    if (!paired) prefetch_tmap(tm_v);
   }
-  const int my_pg = lane / NSL, my_s = lane % NSL;
-  const bool loader = lane < kTilePages * NSL;
-  auto k_off = [](int b) { return C::KV_OFF + b * 2 * NSL * kKVSlab; };
-  auto v_off = [](int b) { return C::KV_OFF + b * 2 * NSL * kKVSlab + NSL * kKVSlab; };
   auto lane0_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     int r = 1;
     if (lane == 0) r = mbar_wait(bar, parity, abort_flag, lim) ? 1 : 0;
     return __shfl_sync(0xffffffffu, r, 0) != 0;
   };
-  int g = 0, g_v = 0;                                // CTA-global KV tiles: K asked for, V asked for
-  auto load_v = [&](int gv, int row0, int npg) -> bool {
-    const int bv = gv % KVS;
-    if (gv >= KVS && !lane0_wait(&bars->v_empty[bv], ((gv / KVS) - 1) & 1)) return false;
-    if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[bv], npg * kPage * D * 2);
-    __syncwarp();
-    if (loader && my_s == 0 && my_pg < npg) {
-      if constexpr (NSL == 2)
-        tma_load_4d(smem + v_off(bv) + my_pg * kVPage, tm_v, 0, 0, 0, row0 / kPage, &bars->v_full[bv]);
-      else
-        tma_load_2d(smem + v_off(bv) + my_pg * kVPage, tm_v, 0, row0, &bars->v_full[bv]);
-    }
-    return true;
-  };
+  int g = 0;  // CTA-global KV tiles asked for
   const int part_tiles = p.hdr[H_CH_TILES];
   const int2* items = part_tiles > 0 ? ChunkParts(p).items : p.ch_items;
   int t_run[2] = {0, 0}, parts_run[2] = {0, 0};  // KV tiles and parts run by each softmax group so far
@@ -581,56 +582,45 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
       tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + s * kQSlab, tm_q, s * 64, it.hk * G, it.tb + it.tok0[t],
                   &bars->q_full);
     }
-    int row0_prev = 0, npg_prev = 0;
     for (int kt = 0; kt < n_kt; ++kt, ++g) {
       const int lp = (kt + 1) * kTilePages + lane;
       const int pg_nxt = lane < kTilePages && lp < n_pages ? __ldg(btrow + lp) : 0;
       const int b = g % KVS;
       const int npg = (min(kKeys, kv_max - kt * kKeys) + kPage - 1) / kPage;
-      int phys = __shfl_sync(0xffffffffu, pg_cur, my_pg & (kTilePages - 1));
-      if (loader && my_pg < npg && (phys < 0 || phys >= p.num_pages)) {
+      if (lane < npg && (pg_cur < 0 || pg_cur >= p.num_pages)) {
         atomicOr(p.hdr + H_STATUS, MS_STATUS_BAD_PAGE);
-        phys = 0;
+        pg_cur = 0;
       }
-      const int row0 = (phys * p.H_kv + hk) * kPage;
-      // K of tile g: its stage was last read by the S MMAs of tile g - KVS
+      // the stage was last read by the MMAs of tile g - KVS
       if (g >= KVS && !lane0_wait(&bars->k_empty[b], ((g / KVS) - 1) & 1)) {
         ok = false;
         break;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[b], npg * kPage * D * 2);
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[b], 2 * npg * kPage * D * 2);
       __syncwarp();
-      if (loader && my_s == 0 && my_pg < npg) {
-        if constexpr (NSL == 2)
-          tma_load_4d(smem + k_off(b) + my_pg * 4096, tm_k, 0, 0, 0, row0 / 8, &bars->k_full[b]);
-        else
-          tma_load_2d(smem + k_off(b) + my_pg * 2048, tm_k, 0, row0, &bars->k_full[b]);
-      }
-      if (kt >= 1) {  // V one tile behind
-        if (!load_v(g - 1, row0_prev, npg_prev)) {
-          ok = false;
-          break;
+      if (lane < npg) {
+        uint8_t* dst = smem + C::KV_OFF + b * 2 * NSL * kKVSlab + lane * 2 * lay.group;
+        const int grp = (pg_cur * p.H_kv + hk) * 2;  // the page's first group in its pool
+        if (paired) {
+          if constexpr (NSL == 2) tma_load_5d(dst, tm_kv, 0, 0, 0, 0, grp, &bars->k_full[b]);
+          else tma_load_4d(dst, tm_kv, 0, 0, 0, grp, &bars->k_full[b]);
+        } else if constexpr (NSL == 2) {
+          tma_load_4d(dst + lay.k, tm_k, 0, 0, 0, grp, &bars->k_full[b]);
+          tma_load_4d(dst + lay.v, tm_v, 0, 0, 0, grp, &bars->k_full[b]);
+        } else {
+          tma_load_3d(dst + lay.k, tm_k, 0, 0, grp, &bars->k_full[b]);
+          tma_load_3d(dst + lay.v, tm_v, 0, 0, grp, &bars->k_full[b]);
         }
-        g_v = g;
       }
-      row0_prev = row0;
-      npg_prev = npg;
       pg_cur = pg_nxt;
     }
     if (!ok) break;
-    if (!load_v(g - 1, row0_prev, npg_prev)) {
-      ok = false;
-      break;
-    }
-    g_v = g;
     take();
   }
   if (lane == 0) {
     if (!ok && !stalled) *abort_flag = 1;
     // copies still in flight must land before the CTA moves on (Q's: close_chunk_barriers)
     for (int t = (g > KVS ? g - KVS : 0); t < g; ++t) mbar_wait(&bars->k_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
-    for (int t = (g_v > KVS ? g_v - KVS : 0); t < g_v; ++t)
-      mbar_wait(&bars->v_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
   }
 }
 
@@ -696,7 +686,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     mbar_init(&bars->q_empty, 2);  // one commit per S issuer
     for (int b = 0; b < 8; ++b) {  // all of them, so that all can be invalidated
       mbar_init(&bars->k_full[b], Q4 ? kDequantWarps : 1);
-      mbar_init(&bars->k_empty[b], 2);
+      mbar_init(&bars->k_empty[b], Span ? 3 : 2);  // a commit per S issuer; spans, whose stages hold V too, and PV's
       mbar_init(&bars->v_full[b], Q4 ? kDequantWarps : 1);
       mbar_init(&bars->v_empty[b], 1);
     }
@@ -750,11 +740,18 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   // rows lo .. hi - 1 of V stage bv, by the PV issuer
   auto zero_v = [&](int bv, int lo, int hi) {
     uint8_t* v0 = smem + v_off(bv);
+    uint32_t group = 1024, slab = 2048;
+    if constexpr (Span) {
+      const SpanTile<D> lay(p);
+      v0 = smem + k_off(bv) + lay.v;
+      group = lay.group;
+      slab = 1024;
+    }
     constexpr int W = NSL * 8;  // 16-byte words to a row
     for (int i = lo * W + (Elect ? lane : 0); i < hi * W; i += Elect ? 32 : 1) {
       const int r = i / W;
-      *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + (i % W >> 3) * 2048 + (r & 15) * 128 + (i & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
+      const uint32_t at = Span ? (r >> 3) * group + (r & 7) * 128 : (r >> 4) * kVPage + (r & 15) * 128;
+      *reinterpret_cast<uint4*>(v0 + at + (i % W >> 3) * slab + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     join();
@@ -764,7 +761,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   };
 
   if (Span && warp == 0) {
-    if constexpr (Span) span_producer<D, G>(&tm_q, &tm_k, NSL == 2 ? &tm_vp : &tm_v, p, smem, bars, n_items);
+    if constexpr (Span) span_producer<D, G>(&tm_q, &tm_k, &tm_v, &tm_vp, p, smem, bars, n_items);  // tm_vp: K and V
   } else if (warp == 0) {
     // ---------------------------------------------------------------- work queue + TMA producer
     // The whole warp runs this loop: lane 0 owns the queue, the waits and the
@@ -995,9 +992,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     const int t = warp == 1 ? 0 : 1;
     if (Elect || lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(sbase + C::Q_OFF + t * C::Q_BYTES, 16, 1024);
-      // K's 64-column slabs, and its groups of 8 keys: slab after slab, or (spans, D = 128) the slabs of a group together
-      constexpr int kKSlab = Span && NSL == 2 ? 1024 : kKVSlab, kKGroup = Span && NSL == 2 ? 2048 : 1024;
-      const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, kKGroup);
+      constexpr int kKSlab = Span ? 1024 : kKVSlab;  // between K's 64-column slabs
+      uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, 1024);
+      if constexpr (Span) {
+        const SpanTile<D> lay(p);
+        kdesc0 = smem_desc_sw128(sbase + C::KV_OFF + lay.k, 16, lay.group);
+      }
       const uint32_t s_tm = tmem + C::S_COL + 2 * t * 64;
       constexpr uint32_t idesc_full = idesc_bf16_f32(128, kKeys, 0);
       int bk = 0;        // K stage of the next tile
@@ -1075,7 +1075,14 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
       // V is the MN-major B operand, one page per k-step of 16 keys: the page's
       // 64-column slabs 2048 B apart (LBO), its two 8-key row groups 1024 B apart
       // (SBO).  P (A operand) is in TMEM: 16 keys = 8 packed columns per k-step.
-      const uint64_t vdesc0 = smem_desc_sw128(sbase + C::KV_OFF + NSL * kKVSlab, 2048, 1024);
+      uint64_t vdesc0 = smem_desc_sw128(sbase + C::KV_OFF + NSL * kKVSlab, 2048, 1024), vstep = kVPage >> 4;
+      if constexpr (Span) {
+        const SpanTile<D> lay(p);
+        vdesc0 = smem_desc_sw128(sbase + C::KV_OFF + lay.v, 1024, lay.group);
+        vstep = 2 * lay.group >> 4;
+      }
+      uint64_t* const v_full = Span ? bars->k_full : bars->v_full;
+      uint64_t* const v_empty = Span ? bars->k_empty : bars->v_empty;
       int bv = 0;        // V stage of the next tile
       uint32_t vph = 0;  // its phase parity
       bool ok = true;
@@ -1096,7 +1103,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const int ke_[2] = {it.kv_end[0], it.kv_end[1]};
         const int kv_max = max(ke_[0], ke_[1]);
         for (int j = 0; j < n_kt && ok; ++j) {
-          if (!issue_wait(&bars->v_full[bv], vph)) {
+          if (!issue_wait(&v_full[bv], vph)) {
             ok = false;
             break;
           }
@@ -1122,12 +1129,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
                 if (kr >= kKeys) {
 #pragma unroll
                   for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + kk * vstep, idesc_pv,
                                 (j > first_[t] || kk > 0) ? 1u : 0u);
                 } else {
                   const int nk_t = (kr + 15) >> 4;
                   for (int kk = 0; kk < nk_t; ++kk)
-                    mma_bf16_ts(dcol, acol + kk * 8, vd + static_cast<uint64_t>((kk * kVPage) >> 4), idesc_pv,
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + kk * vstep, idesc_pv,
                                 (j > first_[t] || kk > 0) ? 1u : 0u);
                 }
                 mma_commit(&bars->o_done[t][b]);
@@ -1136,7 +1143,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
             }
           }
           if (!ok) break;
-          if (one()) mma_commit(&bars->v_empty[bv]);
+          if (one()) mma_commit(&v_empty[bv]);
           join();
           if (++bv == KVS) {
             bv = 0;
