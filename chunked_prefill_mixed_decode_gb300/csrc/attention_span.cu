@@ -24,6 +24,12 @@ struct SpanMaps {
   CUtensorMap k, v, kv, out;
 };
 
+// The cost model's SM time of a 128x128 chunk tile beside decode rows (attention_step.cuh): from sweeps of the split
+// over eleven mixed steps, in a build that forced it for the purpose (256 decodes and two chunks of 3968 tokens over
+// 1024 keys: 263 us at the causal kernel's 5820, 235 here; 100 decodes and 2000 tokens, D = 64, over 1500 keys 113
+// and 103).
+constexpr float kSpanTileCycles = 4000.f;
+
 template <int D, int G>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attention_span_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -110,6 +116,7 @@ int span_call(const void* q, const void* k_cache, const void* v_cache, int32_t n
                            key_total, H_q, H_kv, D, page_size, scale, out, workspace, ws_bytes, false, stall_limit_ns, &L,
                            &empty);
   if (rc != MS_OK || empty) return rc;
+  L.p.tile_cycles = kSpanTileCycles;
   L.p.sinks = sinks;
   L.p.fixed_span = window == 0 ? 1 : 0;
   L.p.window = window == 0 ? INT32_MAX : window;

@@ -409,6 +409,29 @@ def test_page_ids_past_32_bit_offsets(env):
 
 
 @pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("where", ["v above k", "v below k", "one pool for both", "side by side"])
+def test_pools_in_any_place(env, H_q, H_kv, D, where):
+    """A page of K and of V comes as one box where the pools' distance is one that a tensor map can have, whichever pool
+    lies lower; one tensor as both pools comes as two.  Hidden cells of both hold infinities and NaN."""
+    torch = env[0]
+    for window in (70, None):
+        a = Span(env, [(333, 130), (40, 1), (1000, 3), (17, 17), (2500, 1)], H_q, H_kv, D, window, 1.0 if window else None, seed=6)
+        n = a.k.numel()
+        if where == "one pool for both":
+            a.v = a.k
+        else:
+            gap = {"side by side": 0, "v above k": 8 * 1234567, "v below k": 8 * 7}[where]
+            both = torch.empty(2 * n + gap, dtype=torch.bfloat16, device="cuda")
+            low, high = both[:n].view(a.k.shape), both[n + gap:].view(a.k.shape)
+            k, v = (high, low) if where == "v below k" else (low, high)
+            k.copy_(a.k)
+            v.copy_(a.v)
+            a.k, a.v = k, v
+        a.call()
+        a.check()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64)])
 @pytest.mark.parametrize("rows", [[(500, 300), (20, 40)], [(9000, 20)]])
 def test_stalled_producers_time_out_and_the_workspace_recovers(env, H_q, H_kv, D, rows):
     torch, ms, _ = env
