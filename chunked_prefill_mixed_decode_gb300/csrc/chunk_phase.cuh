@@ -737,24 +737,18 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   auto issue_wait_item = [&](uint64_t* bar, uint32_t parity) {
     return Elect ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait(bar, parity, abort_flag, lim);
   };
-  // rows lo .. hi - 1 of V stage bv, by the PV issuer
+  // spans: keys lo .. hi - 1 of V stage bv, by the PV issuer's warp
   auto zero_v = [&](int bv, int lo, int hi) {
-    uint8_t* v0 = smem + v_off(bv);
-    uint32_t group = 1024, slab = 2048;
-    if constexpr (Span) {
-      const SpanTile<D> lay(p);
-      v0 = smem + k_off(bv) + lay.v;
-      group = lay.group;
-      slab = 1024;
-    }
-    constexpr int W = NSL * 8;  // 16-byte words to a row
-    for (int i = lo * W + (Elect ? lane : 0); i < hi * W; i += Elect ? 32 : 1) {
+    const SpanTile<D> lay(p);
+    uint8_t* v0 = smem + k_off(bv) + lay.v;
+    constexpr int W = NSL * 8;  // 16-byte words to a key
+    for (int i = lo * W + lane; i < hi * W; i += 32) {
       const int r = i / W;
-      const uint32_t at = Span ? (r >> 3) * group + (r & 7) * 128 : (r >> 4) * kVPage + (r & 15) * 128;
-      *reinterpret_cast<uint4*>(v0 + at + (i % W >> 3) * slab + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(v0 + (r >> 3) * lay.group + (r & 7) * 128 + (i % W >> 3) * 1024 + (i & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
-    join();
+    __syncwarp();
   };
   auto softmax_wait = [&](uint64_t* bar, uint32_t parity) {
     return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : warp_wait(bar, parity, abort_flag, lim);
@@ -1110,8 +1104,21 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           const int keys = min(kKeys, kv_max - j * kKeys);  // keys loaded in this tile
           // rows past the context in the last page may hold stale (even non-finite)
           // data: zero them in V so that P = 0 times V stays 0
-          if (!Q4 && (keys & 15) != 0) zero_v(bv, keys, (keys + 15) & ~15);
-          if (Span && j == 0 && unseen > 0) zero_v(bv, 0, unseen);  // and those in front of every query's window
+          if constexpr (Span) {
+            if ((keys & 15) != 0) zero_v(bv, keys, (keys + 15) & ~15);
+            if (j == 0 && unseen > 0) zero_v(bv, 0, unseen);  // and those in front of every query's window
+          } else if (!Q4 && (keys & 15) != 0) {
+            if (one()) {
+              uint8_t* v0 = smem + v_off(bv);
+              for (int r = keys; r < ((keys + 15) & ~15); ++r)
+                for (int s = 0; s < NSL; ++s)
+                  for (int q16 = 0; q16 < 8; ++q16)
+                    *reinterpret_cast<uint4*>(v0 + (r >> 4) * kVPage + s * 2048 + (r & 15) * 128 + q16 * 16) =
+                        make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+            join();
+          }
           const uint64_t vd = vdesc0 + static_cast<uint64_t>((bv * 2 * NSL * kKVSlab) >> 4);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -1129,12 +1136,12 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
                 if (kr >= kKeys) {
 #pragma unroll
                   for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_bf16_ts(dcol, acol + kk * 8, vd + kk * vstep, idesc_pv,
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + (Span ? kk * vstep : static_cast<uint64_t>((kk * kVPage) >> 4)), idesc_pv,
                                 (j > first_[t] || kk > 0) ? 1u : 0u);
                 } else {
                   const int nk_t = (kr + 15) >> 4;
                   for (int kk = 0; kk < nk_t; ++kk)
-                    mma_bf16_ts(dcol, acol + kk * 8, vd + kk * vstep, idesc_pv,
+                    mma_bf16_ts(dcol, acol + kk * 8, vd + (Span ? kk * vstep : static_cast<uint64_t>((kk * kVPage) >> 4)), idesc_pv,
                                 (j > first_[t] || kk > 0) ? 1u : 0u);
                 }
                 mma_commit(&bars->o_done[t][b]);
