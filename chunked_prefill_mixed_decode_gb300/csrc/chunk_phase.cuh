@@ -114,6 +114,17 @@ __device__ __forceinline__ bool warp_wait_fast(uint64_t* bar, uint32_t parity, c
   return warp_wait(bar, parity, abort, limit_ns);
 }
 
+// The same with one vote, behind the polls.  The issuers' and softmax warps' waits are what a tile of a span spends
+// its time on: with a vote a poll, chunks of 3968 tokens at 0 and 6000 (32 / 8 heads) over all their keys took 444 us,
+// so 420; over 1024 keys 128 and 123; three of 777 at D = 64 55.2 and 54.4.
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const volatile int* abort, uint64_t limit_ns) {
+  bool done = mbar_try_wait(bar, parity);
+#pragma unroll 1
+  for (int i = 0; i < 16 && !done; ++i) done = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, done)) return true;
+  return warp_wait(bar, parity, abort, limit_ns);
+}
+
 // ---- 4-bit pools: K and V tiles by warps instead of TMA
 
 constexpr int kDequantWarps = kTilePages;            // one per page of a tile
@@ -435,13 +446,15 @@ struct SpanTile {
   }
 };
 
-// Warp 0 of a chunk phase over spans: queue and TMA as in chunk_phase, which has the causal form.  At
-// D = 128 a page of K is one 4 KB box too, laid out by groups of 8 keys with both 64-column slabs of a group
-// together (1 KB each): over the pages of a tile the groups of a slab are then one stride of 2 KB apart, as an
-// S MMA's descriptor wants them.  The K/V stream is what bounds the tiles: with K in two boxes a page, chunks of
-// 3968 tokens at 0 and 6000 (32 / 8 heads) over all keys took 525 us, now 465 (1.40 PFLOP/s, 0.72 of the measured
-// dense rate), over 1024 keys 150 and 135.  A second pair of Q tiles, so that the next item's are there early, with
-// three K/V stages: 539 against 525, over 64 keys 57 us either way; at D = 64, beside six stages, no change.
+// Warp 0 of a chunk phase over spans: queue and TMA as in chunk_phase, which has the causal form.  The K/V stream
+// from L2 bounds the tiles, and it runs the faster the larger its boxes: chunks of 3968 tokens at 0 and 6000, 32 / 8
+// heads, D = 128, over all their keys took 525 us with a page of K in two boxes and one of V in one, 465 with one of
+// each, 459 to 463 with one of both (over 1024 keys 150, 136 and 134), and 420 since the waits are shorter (1.54
+// PFLOP/s, 0.80 of the measured dense rate; over 1024 keys 123); three chunks of 777 tokens at D = 64 60.4 us with a
+// box of each, 56.9 with one of both.  Where the time of an item of
+// a short span goes: some 4 us beside its tiles, for Q's copy, the first tile's and the last product's and O's way out.
+// A second pair of Q tiles, so that the next item's are there early, with three K/V stages: 539 against 525 then, over
+// 64 keys 57 us either way; at D = 64, beside six stages, no change.
 template <int D, int G>
 __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                               const CUtensorMap* tm_kv, const AttnParams& p, uint8_t* smem, ChBars* bars, int n_items) {
@@ -467,8 +480,8 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
   const int2* items = part_tiles > 0 ? ChunkParts(p).items : p.ch_items;
   int t_run[2] = {0, 0}, parts_run[2] = {0, 0};  // KV tiles and parts run by each softmax group so far
   // The item taken next: its entry and its row's words.  Taken behind the last tile of the one before: earlier
-  // look-ups, a step a tile, cost every tile more than they gain an item (544 -> 554 us for chunks of 3968 tokens
-  // at 0 and 6000 over all their keys, as the kernel was then), and the queue would be dealt out ahead.
+  // look-ups, a step a tile, cost every tile more than they gain an item (the chunks above over all keys 469 -> 489
+  // us; a step behind each of the last tiles, 473), and the queue would be dealt out ahead.
   int item = 0, tb = 0, end_tok = 0, c = 0;
   int2 kl = make_int2(0, 0);
   const int32_t* table = nullptr;
@@ -654,6 +667,11 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
 // the ring (740 us); where items are few, one Q tile for both softmax groups, every
 // other K/V tile each (a 512-token chunk alone 58 -> 54 us, beside 64 decodes
 // 78 -> 94, and the branches cost the long chunks 4 %).
+//
+// Over spans (kSpan) warp 0 is span_producer, a stage's K and V arrive together, each
+// Q tile runs only the tiles that it sees, and whole items leave by store_rows.  tm_k_p,
+// tm_v_p and tm_vp_p are then maps of K, of V and of both by groups of 8 keys, tm_o_p of the
+// output.
 template <int D, int G, int Kind = kCausal>
 __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtensorMap* tm_k_p,
                                             const CUtensorMap* tm_v_p, const CUtensorMap* tm_vp_p,
@@ -725,13 +743,15 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
   // measures 522 -> 527 us there and 2060 -> 2110 us beside long decodes (and 69 -> 61 us
   // for D = 64), lane 0 runs it alone.  Spans, whose issuers do more a tile, take the elected
   // lane: the same chunks over all keys 570 -> 525 us, over 1024 keys 168 -> 157 us, 777
-  // tokens at D = 64 over 1024 keys 33 -> 28 us.
+  // tokens at D = 64 over 1024 keys 33 -> 28 us.  Their softmax warps poll as whole warps too:
+  // 461 -> 446 and 134 -> 130 us.
   constexpr bool Elect = Parts;
   auto one = [&] { return !Elect || elect_one(); };
   auto join = [&] {
     if constexpr (Elect) __syncwarp();
   };
   auto issue_wait = [&](uint64_t* bar, uint32_t parity) {
+    if constexpr (Span) return warp_poll(bar, parity, abort_flag, lim);
     return Elect ? warp_wait_fast(bar, parity, abort_flag, lim) : mbar_wait_fast(bar, parity, abort_flag, 16, lim);
   };
   auto issue_wait_item = [&](uint64_t* bar, uint32_t parity) {
@@ -751,6 +771,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
     __syncwarp();
   };
   auto softmax_wait = [&](uint64_t* bar, uint32_t parity) {
+    if constexpr (Span) return warp_poll(bar, parity, abort_flag, lim);
     return Q4 ? warp_wait_fast(bar, parity, abort_flag, lim) : warp_wait(bar, parity, abort_flag, lim);
   };
 
