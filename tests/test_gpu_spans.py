@@ -222,7 +222,7 @@ def test_cross_few_rows(env, H_q, H_kv, D, rows):
     a.check()
 
 
-@pytest.mark.parametrize("n", [31, 32, 33, 64, 600, 3000])
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 600, 3000, 8192])
 @pytest.mark.parametrize("window", [37, None])
 def test_many_rows(env, n, window):
     """Around the row counts at which the prologue changes its form; pad rows, chunks and rows without keys among them."""
@@ -440,6 +440,31 @@ def test_stalled_producers_time_out_and_the_workspace_recovers(env, H_q, H_kv, D
     assert ms.read_status(a.ws) == ms.STATUS_TIMEOUT and (a.out == 5.0).all()
     a.call()
     a.check()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_steps(env, seed):
+    """Random rows, shapes, windows, sinks, tables and bounds on the contexts' sum, with and without the room for parts."""
+    torch, ms, _ = env
+    rng = np.random.default_rng(1000 + seed)
+    G, H_kv, D = int(rng.choice([1, 2, 4, 8])), int(rng.choice([1, 2, 3, 5])), int(rng.choice([64, 128]))
+    n = int(rng.choice([1, 2, 7, 40]))
+    most = int(rng.choice([20, 300, 7000]))
+    rows = [(int(rng.integers(0, most)), int(rng.choice([0, 1, 1, 1, 2, 5, 17, 130, 400])) if i < 6 else int(rng.choice([0, 1, 1, 1])))
+            for i in range(n)]
+    window = None if rng.random() < 0.3 else int(rng.choice([1, 2, 15, 16, 33, 64, 127, 500, 2000, ALL]))
+    a = Span(env, rows, G * H_kv, H_kv, D, window, 2.0 if window and rng.random() < 0.5 else None, seed=seed, ragged=bool(rng.random() < 0.5),
+             slack=int(rng.integers(0, 4)))
+    scale = None if rng.random() < 0.7 else float(rng.uniform(0.02, 0.3))
+    for q4 in (True, False):
+        total = a.total + int(rng.integers(0, 500))
+        ws = torch.zeros(ms.attention_workspace_size(n, a.q.shape[0], total, G * H_kv, H_kv, D, q4=q4), dtype=torch.uint8, device="cuda")
+        a.out.fill_(5.0)
+        a.total, keep = total, a.total
+        a.call(scale, ws=ws)
+        a.total = keep
+        assert ms.read_status(ws) == 0
+        a.check(scale)
 
 
 # ---------------------------------------------------------------------------- together
