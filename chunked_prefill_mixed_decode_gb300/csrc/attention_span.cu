@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncthreads();
       ChBars* bars = reinterpret_cast<ChBars*>(smem + ChCfg<D>::BAR_OFF);
       const bool aborted = bars->abort != 0;
-      if (threadIdx.x == 0) close_chunk_barriers(bars, &bars->part_last[1]);
+      if (threadIdx.x == 0) close_span_barriers(bars);
       __syncthreads();
       if (aborted) break;
     } else if (!chunk && n_dec_items > 0) {

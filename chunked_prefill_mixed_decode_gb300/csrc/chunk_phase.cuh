@@ -72,7 +72,7 @@ struct ChBars {
   ChItem items[2];
   ChPart parts[2];
   int last[2];
-  // 4-bit pools, spans: items whose Q tiles have been asked for.  Behind the rest: ahead of
+  // 4-bit pools: items whose Q tiles have been asked for; spans: Q tiles asked for.  Behind the rest: ahead of
   // `items` it costs a GQA 8B step over bf16 pools 0.6 %.
   int q_asked;
 };
@@ -92,6 +92,17 @@ __device__ __forceinline__ void close_chunk_barriers(ChBars* bars, uint64_t* las
   const int n_q = bars->q_asked;
   if (n_q > 0) mbar_wait(&bars->q_full, (n_q - 1) & 1, nullptr, 200000000ull);
   for (uint64_t* b = &bars->q_full; b <= last; ++b) mbar_inval(b);
+}
+
+// Over spans, whose stages' one barrier leaves V's free, each Q tile has barriers of its own.
+__device__ __forceinline__ uint64_t* span_q_full(ChBars* bars, int t) { return &bars->v_full[t]; }
+__device__ __forceinline__ uint64_t* span_q_empty(ChBars* bars, int t) { return &bars->v_empty[t]; }
+
+__device__ __forceinline__ void close_span_barriers(ChBars* bars) {
+  const int n_q = bars->q_asked;  // tiles asked for, an item's first and second in turn
+  for (int t = 0; t < 2 && t < n_q; ++t)
+    mbar_wait(span_q_full(bars, t), ((n_q - t - 1) >> 1) & 1, nullptr, 200000000ull);
+  for (uint64_t* b = &bars->q_full; b <= &bars->part_last[1]; ++b) mbar_inval(b);
 }
 
 // wait by lane 0, result and ordering shared with the whole warp
@@ -501,6 +512,26 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
   const bool stalled = p.test_stall != 0;
   bool ok = !stalled;
   int n_done = 0;  // items published by this CTA
+  // An item's Q tiles, each as soon as the S MMAs of the item before are done with its place.  At D = 128 behind the
+  // item's first K/V tile, whose stage is free earlier (two chunks of 3968 tokens, 32 heads over 8, 128 keys a query:
+  // 54.1 -> 50.4 us; 4096: 271.3 -> 270.0).  At D = 64, with 6 stages to 4, in front of it: 64 heads over 8, all keys
+  // 764 us against 775, 777-token chunks over all keys 54.5 against 55.2, though 128 keys take 71.9 against 70.7.
+  constexpr bool kKvFirst = D == 128;
+  const auto ask_q = [&](const ChItem& it) {
+    for (int t = 0; t < 2; ++t) {
+      if (n_done >= 2 && !lane0_wait(span_q_empty(bars, t), (n_done - 2) & 1)) return false;
+      const bool has = it.ntok[t] > 0;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(span_q_full(bars, t), has ? 128 * D * 2 : 0);
+        bars->q_asked = 2 * n_done - 1 + t;
+      }
+      __syncwarp();
+      if (has && lane < NSL)
+        tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + lane * kQSlab, tm_q, lane * 64, it.hk * G, it.tb + it.tok0[t],
+                    span_q_full(bars, t));
+    }
+    return true;
+  };
   if (ok) take();
   while (ok) {
     ChItem it;
@@ -579,21 +610,9 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
     }
     ++n_done;
     if (it.row < 0) break;
-    // Q tiles: the previous item's S MMAs must be done with them
-    if (n_done >= 2 && !lane0_wait(&bars->q_empty, (n_done - 2) & 1)) {
+    if (!kKvFirst && !ask_q(it)) {
       ok = false;
       break;
-    }
-    const int nq = it.ntok[1] > 0 ? 2 : 1;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bars->q_full, nq * 128 * D * 2);
-      bars->q_asked = n_done;
-    }
-    __syncwarp();
-    if (lane < nq * NSL) {
-      const int t = lane / NSL, s = lane % NSL;
-      tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + s * kQSlab, tm_q, s * 64, it.hk * G, it.tb + it.tok0[t],
-                  &bars->q_full);
     }
     for (int kt = 0; kt < n_kt; ++kt, ++g) {
       const int lp = (kt + 1) * kTilePages + lane;
@@ -626,13 +645,20 @@ __device__ __forceinline__ void span_producer(const CUtensorMap* tm_q, const CUt
         }
       }
       pg_cur = pg_nxt;
+      if constexpr (kKvFirst) {
+        if (kt == 0 && !ask_q(it)) {
+          ++g;  // this tile's copies are in flight
+          ok = false;
+          break;
+        }
+      }
     }
     if (!ok) break;
     take();
   }
   if (lane == 0) {
     if (!ok && !stalled) *abort_flag = 1;
-    // copies still in flight must land before the CTA moves on (Q's: close_chunk_barriers)
+    // copies still in flight must land before the CTA moves on (Q's: close_span_barriers)
     for (int t = (g > KVS ? g - KVS : 0); t < g; ++t) mbar_wait(&bars->k_full[t % KVS], (t / KVS) & 1, nullptr, 200000000ull);
   }
 }
@@ -1030,7 +1056,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
         const int first = Span ? bars->parts[slot].first[t] : 0;  // of the tiles that the Q tile sees
         const int end = first + it.nkt[t], t0 = it.t0[t] - first, n_kt = it.n_kt;
         const int kv_max = max(it.kv_end[0], it.kv_end[1]);
-        if ((Parts || end > 0) && !issue_wait_item(&bars->q_full, n & 1)) {
+        if ((Parts || end > 0) && !issue_wait_item(Span ? span_q_full(bars, t) : &bars->q_full, n & 1)) {
           ok = false;
           break;
         }
@@ -1064,7 +1090,7 @@ __device__ __noinline__ void chunk_phase(const CUtensorMap* tm_q_p, const CUtens
           }
           if (one()) {
             mma_commit(&bars->k_empty[bk]);
-            if (kt == n_kt - 1) mma_commit(&bars->q_empty);
+            if (kt == n_kt - 1) mma_commit(Span ? span_q_empty(bars, t) : &bars->q_empty);
           }
           join();
           if (++bk == KVS) {
