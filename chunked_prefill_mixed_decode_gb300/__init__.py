@@ -516,7 +516,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict = N
     (ms_rotary_frequencies).  ``scaling``: None, or a dict of ``kind`` ("plain", "linear", "base", "bands" or "ramp"),
     ``factor`` and, for bands and ramp, ``original_len``, ``low`` and ``high`` (turns over the original length); for
     ramp also ``amplitude``, by default 0.1 ln(factor) + 1."""
-    freq = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.float64)
+    freq = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
     amplitude = ctypes.c_double(1.0)
     sc = None
     if scaling is not None:
@@ -531,8 +531,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict = N
         sc = RotaryScaling(_ROTARY_KINDS[kind], int(d.get("original_len", 0)), float(d.get("factor", 1.0)),
                            float(d.get("low", 0.0)), float(d.get("high", 0.0)), float(d.get("amplitude") or 0.0))
     _check(lib().ms_rotary_frequencies(int(rotary_dim), float(base), None if sc is None else ctypes.byref(sc),
-                                       freq.ctypes.data, ctypes.addressof(amplitude)), "ms_rotary_frequencies")
-    return freq, amplitude.value
+                                       freq, ctypes.addressof(amplitude)), "ms_rotary_frequencies")
+    return np.frombuffer(freq), amplitude.value
 
 
 def attention_workspace_size(max_rows: int, max_tokens: int, max_context_total: int, H_q: int, H_kv: int,
@@ -959,7 +959,7 @@ def rotary_table_device(freq, cos_tab, sin_tab, amplitude: float = 1.0, first_po
     _dev(cos_tab, "cos_tab", torch.float32, (cos_tab.shape[0], freq.shape[0]))
     _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
     st = _stream_of(stream, "cos_tab sin_tab", cos_tab, sin_tab)
-    _check(lib().ms_rotary_table_device(freq.ctypes.data, freq.shape[0], float(amplitude), int(first_pos), cos_tab.shape[0],
+    _check(lib().ms_rotary_table_device(freq.tobytes(), freq.shape[0], float(amplitude), int(first_pos), cos_tab.shape[0],
                                         cos_tab.data_ptr(), sin_tab.data_ptr(), st), "ms_rotary_table_device")
 
 
