@@ -151,6 +151,19 @@ def test_window_decode_rows(env, H_q, H_kv, D, window, sinks, ragged):
     a.check()
 
 
+@pytest.mark.parametrize("H_q,H_kv,D", [x for x in SHAPES if x[0] <= 4 * x[1]])
+@pytest.mark.parametrize("window,sinks", [(16, 2.0), (100, None), (1500, 1.0), (ALL, None), (None, None)])
+def test_decode_weights_keep_what_rounding_leaves(env, H_q, H_kv, D, window, sinks):
+    """Up to 4 heads to a KV head a decode row's weights are two bf16 numbers, off by 2^-8 of 2^-8 at most: of the bound's
+    rounding of the weights 2^-16 A is left, and what is in fp32 and the output's half step stay."""
+    a = Span(env, [(c + (window is None), 1) for c in CTX], H_q, H_kv, D, window, sinks, seed=3 * D + H_q)
+    a.call()
+    a.check()
+    ref, A = a.reference()
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -16 + 2.0 ** -10) * A + 1e-30
+    assert ((a.out.double() - ref).abs() / bound).max().item() <= 1
+
+
 @pytest.mark.parametrize("H_q,H_kv,D", SHAPES)
 @pytest.mark.parametrize("window,sinks,ragged", [(1, 2.0, False), (7, None, True), (64, None, False), (129, 2.0, True),
                                                  (400, None, False), (ALL, 1.0, False)])
