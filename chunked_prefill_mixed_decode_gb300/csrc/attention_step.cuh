@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -197,9 +198,11 @@ __device__ __forceinline__ int span_keys(const AttnParams& p, int c, int d, int 
   return most < c + d ? static_cast<int>(most) : c + d;
 }
 
-// log2 units, as the scores are
+// log2 units, as the scores are; finite where the sink is (from 2.36e38 on the product is not, and the joins'
+// differences of two such maxima would be NaN): any sink up there leaves the keys a weight of zero
 __device__ __forceinline__ float sink_log2(const AttnParams& p, int head) {
-  return __ldg(p.sinks + head) * 1.4426950408889634f;
+  const float x = __ldg(p.sinks + head) * 1.4426950408889634f;
+  return x > FLT_MAX ? FLT_MAX : x;
 }
 
 // Work items of one row: decode splits of `split` pages, or pairs of 128-row Q tiles.

@@ -618,7 +618,7 @@ MS_API int ms_kv_append_rotary(const void* q, int64_t q_stride, const void* k, i
  * their table entries included: they may have been given back.  Values in cells that
  * no token of the row sees do not matter, infinities and NaN included.
  *   window     >= 1; a window of a row's length or more changes nothing
- *   sinks      device fp32 [H_q] or NULL; finite or -infinity (no sink)
+ *   sinks      device fp32 [H_q] or NULL; any finite value, or -infinity (no sink)
  *   workspace  as for ms_mixed_step_attention; with one of
  *              ms_attention_workspace_size_q4 bytes few long chunk items are cut into
  *              parts that run at once

@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 
 ALL = 2 ** 31 - 1
 CH_TILES, CH_ITEMS = 12, 6  # words of the workspace header: KV tiles to a part, chunk items
+SPLIT = 7  # pages to a decode split
 
 
 @pytest.fixture(scope="module")
@@ -294,6 +295,27 @@ def test_sinks_at_the_ends_of_their_range(env):
         a = Span(env, rows, 8, 2, 64, window, [-inf, 0.0, 5.0, -5.0, 10.0, 300.0, -300.0, 1.0], seed=3)
         a.call()
         a.check()
+
+
+def test_finite_sinks_beyond_what_their_logarithm_to_base_2_holds(env):
+    """A finite sink takes part as it is up to the type's end, where times log2 e it would be infinite, in whole rows and in
+    rows that are cut: a decode row in splits, a chunk row in parts, with the room for them and without.  Beside such a
+    sink every weight is zero in 64 bits, and so is the row; heads with other sinks are those of the plain form."""
+    torch, ms, _ = env
+    top = float(torch.finfo(torch.float32).max)
+    for H_q, H_kv, D in ((8, 2, 64), (8, 1, 128)):
+        for rows, window in (([(9001, 1), (9001, 40)], ALL), ([(9001, 1), (9001, 40)], 5000), ([(40, 1), (90, 30)], 64)):
+            a = Span(env, rows, H_q, H_kv, D, window, [3e38, top, 2.4e38, 0.0, -top, 2.3e38, 2.0, top], seed=8)
+            a.call()
+            if window > 64:
+                assert a.word(SPLIT) < min(window, 9002) // 16 and a.word(CH_TILES) > 0
+            a.check()
+            assert (a.out[:, [0, 1, 2, 5, 7]] == 0).all()
+            whole = torch.zeros(ms.attention_workspace_size(len(rows), a.T, a.total, H_q, H_kv, D, q4=False), dtype=torch.uint8,
+                                device="cuda")
+            a.out.fill_(5.0)
+            a.call(ws=whole)
+            a.check()
 
 
 def test_sink_above_all_scores_and_then_keys_far_above_it(env):
