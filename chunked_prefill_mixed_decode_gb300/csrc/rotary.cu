@@ -31,9 +31,9 @@ double pair_of_turns(double turns, double n, double base, double R) {
   return R * std::log(n / (turns * kTwoPi)) / (2.0 * std::log(base));
 }
 
-// f / (2 pi) modulo 1 in units of 2^-64, from 128 bits of 1 / (2 pi): exact but for the last unit,
-// so that row * unit, which wraps as turns do, is the angle of any int32 position to 2^-34 turns
-// and that of the first million to 2^-45.
+// f / (2 pi) modulo 1 in units of 2^-64, from 128 bits of 1 / (2 pi), to half a unit: row * unit,
+// which wraps as turns do, is then the angle of any int32 position to 2^-34 turns and that of the first
+// million to 2^-45.
 uint64_t turns_fixed(double f) {
   constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 1 / (2 pi) times 2^128
   if (f == 0.0) return 0;
@@ -53,12 +53,15 @@ uint64_t turns_fixed(double f) {
 // table (device)
 // ----------------------------------------------------------------------------
 //
-// The angle of (position p, pair i) is p * turns[i] modulo 1 in 64-bit whole numbers, without
-// rounding.  It is split into the nearest quarter turn and a rest x of at most pi / 4, in two
-// floats; cosine and sine of x by their Taylor series in fp32 (the first term left out is below
-// 3e-9), with the leading terms kept in two floats.  What the last rounding does not cause is the
-// rounding of the cubic term's factors: 3.5 of them, 2^-24 each, of at most 0.08 beside a step of
-// 2^-24, so a result is off by at most 0.8 of a step.  (FP64 has 1/64 of the fp32 rate on this GPU.)
+// The angle of (position p, pair i) is p * turns[i] modulo 1 in 64-bit whole numbers, off by the frequency's
+// last bit p times, (p + 1) 2^-65 turns at most.  It is split into the nearest quarter turn and a rest x of at most
+// pi / 4, in two floats: of the rest's 62 bits the upper 45 are taken (2 pi 2^-47 left out), and the small
+// part's own roundings are below that too, so that x is off by 2 pi 2^-46 at most beside the angle's error.  Cosine
+// and sine of x by their Taylor series in fp32 (the first term left out is below 3e-9), with the leading terms kept
+// in two floats.  What the last rounding does not cause is the rounding of the cubic term's factors: 3.5 of them,
+// 2^-24 each, of at most 0.115 of a sine.  A result is off by at most 0.8 * 2^-23 of its size (0.5 + 0.2 + 0.03) and by the
+// angle's error times the amplitude, which shows where a sine is below 1e-6: there it is several of its steps, if 1e-13 in
+// all: a rotation passes absolute errors on, so the 17 bits below are not carried as a third float.  (FP64 has 1/64 of the fp32 rate on this GPU.)
 
 // The amplitude m in two floats, and m times the Taylor coefficients.
 struct Series {

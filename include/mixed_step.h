@@ -572,9 +572,10 @@ MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, const ms_rotar
 
 /* ms_rotary_table_device -- device: cos_tab[r][i] = amplitude cos(p freq[i]) and
  * sin_tab[r][i] alike for p = first_pos + r, r < n, as ms_rope_table lays them out.
- * Angles are exact in 64-bit fixed point whatever the position (error below 1e-9
- * at 2^31, 1e-12 up to 2^20); beside that a result is within 0.8 of a step of fp32 of
- * the exact one.
+ * Angles are reduced in 64-bit fixed point whatever the position, to 2 pi ((p + 1)
+ * 2^-65 + 2^-46) radians (1e-9 at 2^31, 1e-12 up to 2^20, 1e-13 up to 2^14).  A result
+ * is off by at most 0.8 * 2^-23 of its size (0.8 to 1.6 of its steps), and by that angle times the
+ * amplitude: sines below 1e-6 can be several of their steps from the exact ones.
  *   freq      host double [pairs], |freq| <= 1024; read before the call returns
  *   pairs     R / 2: 4 .. 64, a multiple of 4
  *   amplitude 0, or of a magnitude of 2^-40 .. 2^40

@@ -59,6 +59,28 @@ def test_table(env, R, base, first, n, scaling):
     _check_table(env, freq, amp, first, n, rows=sorted({0, 1, 2, n // 3, n // 2, n - 2, n - 1} & set(range(n))))
 
 
+@pytest.mark.parametrize("R,base,factor,amp", [(128, 1e6, 32.0, 1.0), (128, 5e5, 8.0, 1.0), (128, 1e4, 1.0, 1.1386), (64, 1e4, 4.0, -2.5),
+                                               (128, 1e6, 1.0, 1.41)])
+@pytest.mark.parametrize("first,n", [(0, 12), (4095, 4), (2 ** 20 - 2, 4), (2 ** 31 - 4, 4)])
+def test_table_entry_by_entry(env, R, base, factor, amp, first, n):
+    """Every entry, the smallest sines among them, against the arithmetic's own error and nothing beside it.
+
+    Of the value's size, in units of 2^-23: 0.5 for the last rounding; 3.5 roundings of 2^-24 in the cubic term, at most
+    0.115 of a sine up to pi / 4: 0.2; the first term left out, x^11 / 11! or x^12 / 12!, 0.02; 0.005 for the fifth
+    power's: 0.73 in all, 0.8 here.  Of the angle: (p + 1) 2^-65 turns from the frequency's last bit and the product; what the
+    series takes of the rest of the turn, 2 pi 2^-47 for the bits left out below it, and roundings of its small part of 2 pi
+    2^-48 and 2^-49 at most: 2 pi 2^-46 in all.  (A step-by-step emulation in fp32 comes to 0.73 of this bound.)"""
+    torch, ms, _ = env
+    freq, _ = ms.rotary_frequencies(R, base, {"kind": "linear", "factor": factor})
+    cos, sin = (torch.empty(n, R // 2, device="cuda") for _ in range(2))
+    ms.rotary_table_device(freq, cos, sin, amplitude=amp, first_pos=first)
+    for r in range(n):
+        want = np.array([rotary.table_entry(first + r, f, amp) for f in freq])
+        for got, w in ((cos[r], want[:, 0]), (sin[r], want[:, 1])):
+            bound = 0.8 * 2.0 ** -23 * np.abs(w) + abs(amp) * 2 * np.pi * ((first + r + 1) * 2.0 ** -65 + 2.0 ** -46)
+            assert (np.abs(got.cpu().numpy().astype(np.float64) - w) <= bound).all(), first + r
+
+
 def test_table_of_special_angles(env):
     """Zero, negative and large frequencies, exact quarters' neighbourhood, a negative and a zero amplitude."""
     f = np.array([0.0, -0.7, 1024.0, -1024.0, np.pi / 2, np.pi / 4, -np.pi, 2 * np.pi, 1e-300, 1e-12, 5e-324, 0.5])
