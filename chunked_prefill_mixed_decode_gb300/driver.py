@@ -11,7 +11,7 @@ from __future__ import annotations
 import time
 
 from . import Engine, StepGraph, attention_workspace_size, read_status
-from .step import MetaStager, run_step, run_step_q4
+from .step import MetaStager, check_rotary_tables, run_step, run_step_q4
 
 
 class RoundDriver:
@@ -29,22 +29,24 @@ class RoundDriver:
     kernels one by one; ``max_row_pages`` then bounds every request's pages.
     The record adds the bucket and the pad tokens.
 
-    ``interleaved``, ``window`` and ``sinks`` are those of step.run_step, over bf16 pools and without graphs; ``cos`` and
-    ``sin`` may cover part of the head (step.rotary_tables).
+    ``interleaved``, ``window``, ``sinks`` and ``rotary_dim`` are those of step.run_step, over bf16 pools and without
+    graphs; with ``rotary_dim`` ``cos`` and ``sin`` cover part of the head (step.rotary_tables).
     """
 
     def __init__(self, engine: Engine, k_cache, v_cache, cos, sin, H_q: int, H_kv: int, D: int,
                  scale: float | None = None, stream=None, graph_buckets=None, max_row_pages: int = 0,
-                 interleaved: bool = False, window: int | None = None, sinks=None):
+                 interleaved: bool = False, window: int | None = None, sinks=None, rotary_dim: int | None = None):
         import torch
         self.engine = engine
         self.graph = None
         self.q4 = v_cache is None
         if self.q4 and graph_buckets:
             raise ValueError("graph_buckets needs bf16 pools: a step over a 4-bit pool is captured with step.StepTables")
-        self.forms = {"interleaved": interleaved, "window": window, "sinks": sinks}
-        if (interleaved or window is not None or sinks is not None) and (self.q4 or graph_buckets):
-            raise ValueError("interleaved pairs, a window and sinks need bf16 pools and no graph_buckets")
+        self.forms = {"interleaved": interleaved, "window": window, "sinks": sinks, "rotary_dim": rotary_dim}
+        if (interleaved or window is not None or sinks is not None or rotary_dim not in (None, D)) and (self.q4 or graph_buckets):
+            raise ValueError("interleaved pairs, a window, sinks and a part of the head need bf16 pools and no graph_buckets")
+        if not self.q4 and not graph_buckets:
+            check_rotary_tables(cos, sin, D, rotary_dim, interleaved)
         self.k_cache, self.v_cache = k_cache, v_cache
         self.cos, self.sin = cos, sin
         self.H_q, self.H_kv, self.D = H_q, H_kv, D

@@ -218,17 +218,38 @@ class StepTables:
         return self.batch
 
 
+def check_rotary_tables(cos, sin, D: int, rotary_dim: int = None, interleaved: bool = False) -> None:
+    """The tables of a step are [max_pos, rotary_dim / 2], or None for a ``rotary_dim`` of 0 (nothing turns).  Without
+    ``rotary_dim`` the whole head turns, D elements; in ``interleaved`` pairs as many as the tables have."""
+    if rotary_dim is not None and (rotary_dim % 16 != 0 or not 0 <= rotary_dim <= D):
+        raise ValueError(f"rotary_dim must be a multiple of 16 from 0 to {D}, got {rotary_dim}")
+    if cos is None or sin is None:
+        if cos is not sin or rotary_dim != 0:
+            raise ValueError("cos and sin are required, both of them, unless rotary_dim is 0")
+        return
+    if cos.dim() != 2:
+        raise ValueError("cos must be [max_pos, rotary_dim/2]")
+    R = (min(2 * cos.shape[1], D) if interleaved else D) if rotary_dim is None else rotary_dim
+    if 2 * cos.shape[1] != R or R == 0:
+        raise ValueError(f"cos must be [max_pos, {R // 2}] for {R} of {D} elements that turn (rotary_dim), got {tuple(cos.shape)}")
+
+
 def run_step(q, k, v, batch: DeviceBatch, cos, sin, k_cache, v_cache, out, workspace, q_rot=None,
-             dev_status=None, scale=None, stream=None, interleaved: bool = False, window: int = None, sinks=None):
+             dev_status=None, scale=None, stream=None, interleaved: bool = False, window: int = None, sinks=None,
+             rotary_dim: int = None):
     """One step of one layer; returns q_rot.
 
     Where the whole head turns in halves and every token sees all keys up to its own this is ms_mixed_step (the append,
-    then the attention, with the prologue inside the append's launch on small steps).  With tables of fewer pairs (or
-    None: nothing turns), ``interleaved`` pairs, or q, k, v whose tokens' rows lie apart, the append is
-    kv_append_rotary; with a ``window`` or ``sinks`` the attention is mixed_step_attention_window."""
+    then the attention, with the prologue inside the append's launch on small steps).  With a ``rotary_dim`` of less than
+    the head (0, with tables of None: nothing turns), ``interleaved`` pairs, or q, k, v whose tokens' rows lie apart, the
+    append is kv_append_rotary; with a ``window`` or ``sinks`` the attention is mixed_step_attention_window.  Tables of
+    another width than ``rotary_dim`` says (check_rotary_tables) are refused."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H_q, D], got {tuple(q.shape)}")
     if q_rot is None:
         q_rot = q
     T, D = batch.num_tokens, q.shape[2]
+    check_rotary_tables(cos, sin, D, rotary_dim, interleaved)
     rows = (q[:T], k[:T], v[:T])
     if interleaved or cos is None or 2 * cos.shape[1] != D or not all(x.is_contiguous() for x in rows):
         kv_append_rotary(*rows, batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot=q_rot[:T],

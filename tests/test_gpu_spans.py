@@ -604,6 +604,34 @@ def test_run_step_picks_the_plain_step(env):
     assert ms.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("R", [32, 0])
+def test_step_turns_the_part_of_the_head_that_it_is_told(env, R):
+    """With rotary_dim given, halves of a part of the head, or nothing, turn: the separate calls' bits, eager and by rounds."""
+    torch, ms, step = env
+    from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
+    H_q, H_kv, D, budget, pages = 4, 2, 64, 24, 12
+    g = torch.Generator(device="cuda").manual_seed(R)
+    tabs = step.rotary_tables(200, R, "cuda") if R else (None, None)
+    pools = [torch.zeros(pages, H_kv, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    eng = ms.Engine(pages, budget)
+    drv = RoundDriver(eng, pools[0], pools[1], *tabs, H_q, H_kv, D, rotary_dim=R)
+    eng.add_request(37, 3)
+    eng.add_request(5, 4)
+    for _ in range(4):
+        q, k, v = (torch.randn(budget, H, D, generator=g, device="cuda").to(torch.bfloat16) for H in (H_q, H_kv, H_kv))
+        m = drv.step(q, k, v)["meta"]
+        T = m["num_tokens"]
+        assert T > 0
+        batch = step.to_device(m, "cuda")
+        ws = step.workspace_for(batch, H_q, H_kv, D, "cuda")
+        q_rot, out = torch.empty(T, H_q, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H_q, D, dtype=torch.bfloat16, device="cuda")
+        ms.kv_append_rotary(q[:T], k[:T], v[:T], batch.positions, batch.slot_mapping, *tabs, pools[2], pools[3], q_rot=q_rot)
+        step.attend(q_rot, pools[2], pools[3], batch, out, ws)
+        assert torch.equal(drv.q_rot[:T], q_rot) and torch.equal(drv.out[:T], out)
+        assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+        assert torch.equal(q_rot, q[:T]) == (R == 0)
+
+
 @pytest.mark.parametrize("window,sinks", [(24, True), (None, True), (9, False)])
 def test_engine_rounds_with_a_window(env, window, sinks):
     """The round driver over pools with pages reused: every round's windowed attention against the plain form."""

@@ -209,3 +209,48 @@ def test_round_driver_refuses_forms_without_their_kernels(ms):
             RoundDriver(ms.Engine(2, 8), q4, None, None, None, 4, 2, 64, **kw)
         with pytest.raises(ValueError):
             RoundDriver(ms.Engine(2, 8), pool, pool, None, None, 4, 2, 64, graph_buckets=[8], **kw)
+
+
+def _host_step(ms, D=128, H_q=4, H_kv=2, T=3):
+    """Arguments of step.run_step on the host: what is refused by shape alone is refused before a device is looked for."""
+    torch = pytest.importorskip("torch")
+    from chunked_prefill_mixed_decode_gb300 import step
+    q, k = torch.zeros(T, H_q, D, dtype=torch.bfloat16), torch.zeros(T, H_kv, D, dtype=torch.bfloat16)
+    i = torch.zeros(T, dtype=torch.int32)
+    batch = step.DeviceBatch(i[:2], i[:1], i[:1], i, i, i[:1].view(1, 1), 1, T, 0, 16, {})  # one row, one page
+    pool = torch.zeros(2, H_kv, 16, D, dtype=torch.bfloat16)
+    return torch, step, [q, k, k.clone(), batch], [pool, pool.clone(), torch.zeros_like(q), torch.zeros(1 << 16, dtype=torch.uint8)]
+
+
+def test_step_refuses_tables_of_another_width(ms):
+    """Tables that are not [max_pos, D / 2] are a mistake unless the call says that a part of the head, or none of it, turns:
+    a table made for D = 64 does not turn half of every head of 128 without a word."""
+    torch, step, a, b = _host_step(ms)
+    tab = lambda n: torch.zeros(10, n)  # noqa: E731
+    for cos, kw in ((tab(32), {}), (tab(128), {}), (None, {}), (tab(32), {"window": 16}), (None, {"window": 16}), (None, {"interleaved": True}),
+                    (tab(32), {"rotary_dim": 128}), (tab(32), {"rotary_dim": 32}), (tab(64), {"rotary_dim": 64}), (tab(32), {"rotary_dim": 0}),
+                    (None, {"rotary_dim": 64}), (tab(32), {"rotary_dim": 32, "interleaved": True}), (tab(128), {"interleaved": True}),
+                    (tab(64).view(-1), {}), (tab(4), {"rotary_dim": 8}), (None, {"rotary_dim": -16})):
+        with pytest.raises(ValueError, match="rotary_dim|must be .max_pos"):
+            step.run_step(*a, cos, cos, *b, **kw)
+    # what the call says and the tables bear out goes on, to the check of the device
+    for cos, kw in ((tab(64), {}), (tab(32), {"rotary_dim": 64}), (tab(64), {"rotary_dim": 128}), (None, {"rotary_dim": 0}),
+                    (tab(32), {"rotary_dim": 64, "interleaved": True}), (tab(32), {"interleaved": True})):
+        with pytest.raises(ValueError, match="CUDA"):
+            step.run_step(*a, cos, cos, *b, **kw)
+    with pytest.raises(ValueError, match="q must be"):
+        step.run_step(a[0].flatten(1), *a[1:], tab(64), tab(64), *b)
+
+
+def test_round_driver_refuses_tables_of_another_width(ms):
+    torch = pytest.importorskip("torch")
+    from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
+    pool = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    q4 = torch.zeros(2, 2, 1152, dtype=torch.uint8)
+    narrow, whole = torch.zeros(8, 16), torch.zeros(8, 32)
+    for tabs, kw in ((narrow, {}), (None, {}), (narrow, {"window": 8}), (whole, {"rotary_dim": 32}), (narrow, {"rotary_dim": 64})):
+        with pytest.raises(ValueError, match="rotary_dim|must be .max_pos"):
+            RoundDriver(ms.Engine(2, 8), pool, pool, tabs, tabs, 4, 2, 64, **kw)
+    for v, kw in ((None, {}), (pool, {"graph_buckets": [8]})):
+        with pytest.raises(ValueError, match="need bf16 pools"):
+            RoundDriver(ms.Engine(2, 8), q4 if v is None else pool, v, narrow, narrow, 4, 2, 64, rotary_dim=32, **kw)
