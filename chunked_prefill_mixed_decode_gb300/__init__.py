@@ -1029,6 +1029,12 @@ def kv_append_rotary(q, k, v, positions, slot_mapping, cos_tab, sin_tab, k_cache
     _check(rc, "ms_kv_append_rotary")
 
 
+def check_sinks(sinks, H_q: int) -> None:
+    import torch
+    if sinks is not None:
+        _dev(sinks, "sinks", torch.float32, (H_q,))
+
+
 def _span_args(q, k_cache, v_cache, cu_seqlens_q, block_tables, bt_offsets, out, workspace):
     """The checks that the windowed and the cross attention share; returns (T, H_q, D, H_kv, rows, stride, bt_len)."""
     import torch
@@ -1069,8 +1075,7 @@ def mixed_step_attention_window(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_p
                                                     workspace)
     _dev(q_start_pos, "q_start_pos", torch.int32, min_numel=S)
     _dev(context_lens, "context_lens", torch.int32, min_numel=S)
-    if sinks is not None:
-        _dev(sinks, "sinks", torch.float32, (H_q,))
+    check_sinks(sinks, H_q)
     st = _stream_of(stream, "q_rot k_cache v_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace "
                     "sinks", q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out,
                     workspace, sinks)

@@ -10,8 +10,8 @@ import dataclasses
 
 import numpy as np
 
-from . import (attention_workspace_size, build_batch_metadata_device, kv_append_rope_q4, kv_append_rotary, mixed_step,
-               mixed_step_attention, mixed_step_attention_q4, mixed_step_attention_ragged, mixed_step_attention_window,
+from . import (attention_workspace_size, build_batch_metadata_device, check_sinks, kv_append_rope_q4, kv_append_rotary,
+               mixed_step, mixed_step_attention, mixed_step_attention_q4, mixed_step_attention_ragged, mixed_step_attention_window,
                mixed_step_cross_attention, q4_block_bytes, rope_table, rotary_frequencies, rotary_table_device)
 
 META_KEYS = ("cu_seqlens_q", "q_start_pos", "context_lens", "positions", "slot_mapping", "block_tables")
@@ -250,6 +250,9 @@ def run_step(q, k, v, batch: DeviceBatch, cos, sin, k_cache, v_cache, out, works
         q_rot = q
     T, D = batch.num_tokens, q.shape[2]
     check_rotary_tables(cos, sin, D, rotary_dim, interleaved)
+    if window is not None and window < 1:  # here, and the sinks too: ahead of the append, which changes the pools
+        raise ValueError(f"window must be at least 1, got {window}")
+    check_sinks(sinks, q.shape[1])
     rows = (q[:T], k[:T], v[:T])
     if interleaved or cos is None or 2 * cos.shape[1] != D or not all(x.is_contiguous() for x in rows):
         kv_append_rotary(*rows, batch.positions, batch.slot_mapping, cos, sin, k_cache, v_cache, q_rot=q_rot[:T],

@@ -242,6 +242,21 @@ def test_step_refuses_tables_of_another_width(ms):
         step.run_step(a[0].flatten(1), *a[1:], tab(64), tab(64), *b)
 
 
+def test_step_refuses_bad_forms_before_it_appends(ms):
+    """A window or sinks that the attention refuses leave the pools and q as they were."""
+    torch, step, a, b = _host_step(ms)
+    tab, seen = torch.zeros(10, 64), []
+    keep, step.kv_append_rotary = step.kv_append_rotary, lambda *args, **kw: seen.append(args)
+    try:
+        for kw in ({"window": 0}, {"window": -3}, {"sinks": torch.zeros(3)}, {"sinks": torch.zeros(4, dtype=torch.float64)},
+                   {"sinks": torch.zeros(8)[::2]}, {"window": 8, "sinks": torch.zeros(4, 1)}):
+            with pytest.raises(ValueError, match="window|sinks"):
+                step.run_step(*a, tab, tab, *b, **kw)
+    finally:
+        step.kv_append_rotary = keep
+    assert not seen
+
+
 def test_round_driver_refuses_tables_of_another_width(ms):
     torch = pytest.importorskip("torch")
     from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
