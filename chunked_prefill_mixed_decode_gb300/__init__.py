@@ -226,6 +226,14 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _int32(x, name: str) -> int:
+    """A whole number of which ctypes would pass the low 32 bits whatever lies above them."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _stream(stream) -> int:
     if stream is None:
         import torch
@@ -516,7 +524,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict = N
     (ms_rotary_frequencies).  ``scaling``: None, or a dict of ``kind`` ("plain", "linear", "base", "bands" or "ramp"),
     ``factor`` and, for bands and ramp, ``original_len``, ``low`` and ``high`` (turns over the original length); for
     ramp also ``amplitude``, by default 0.1 ln(factor) + 1."""
-    freq = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    rotary_dim = _int32(rotary_dim, "rotary_dim")
+    freq = (ctypes.c_double * min(max(rotary_dim // 2, 1), 64))()  # no more are written: larger ones are refused
     amplitude = ctypes.c_double(1.0)
     sc = None
     if scaling is not None:
@@ -528,9 +537,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict = N
         given = set(d) - ({"amplitude"} if kind == "ramp" else set())
         if given != names:
             raise ValueError(f"scaling {kind!r} takes {sorted(names)}, got {sorted(given)}")
-        sc = RotaryScaling(_ROTARY_KINDS[kind], int(d.get("original_len", 0)), float(d.get("factor", 1.0)),
+        sc = RotaryScaling(_ROTARY_KINDS[kind], _int32(d.get("original_len", 0), "original_len"), float(d.get("factor", 1.0)),
                            float(d.get("low", 0.0)), float(d.get("high", 0.0)), float(d.get("amplitude") or 0.0))
-    _check(lib().ms_rotary_frequencies(int(rotary_dim), float(base), None if sc is None else ctypes.byref(sc),
+    _check(lib().ms_rotary_frequencies(rotary_dim, float(base), None if sc is None else ctypes.byref(sc),
                                        freq, ctypes.addressof(amplitude)), "ms_rotary_frequencies")
     return np.frombuffer(freq), amplitude.value
 
@@ -956,10 +965,11 @@ def rotary_table_device(freq, cos_tab, sin_tab, amplitude: float = 1.0, first_po
     freq = np.ascontiguousarray(freq, dtype=np.float64)
     if freq.ndim != 1 or cos_tab.dim() != 2:
         raise ValueError("freq must be 1-D and cos_tab [n, pairs]")
+    first_pos, n = _int32(first_pos, "first_pos"), _int32(cos_tab.shape[0], "the number of rows")
     _dev(cos_tab, "cos_tab", torch.float32, (cos_tab.shape[0], freq.shape[0]))
     _dev(sin_tab, "sin_tab", torch.float32, cos_tab.shape)
     st = _stream_of(stream, "cos_tab sin_tab", cos_tab, sin_tab)
-    _check(lib().ms_rotary_table_device(freq.tobytes(), freq.shape[0], float(amplitude), int(first_pos), cos_tab.shape[0],
+    _check(lib().ms_rotary_table_device(freq.tobytes(), freq.shape[0], float(amplitude), first_pos, n,
                                         cos_tab.data_ptr(), sin_tab.data_ptr(), st), "ms_rotary_table_device")
 
 
@@ -1076,6 +1086,7 @@ def mixed_step_attention_window(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_p
     _dev(q_start_pos, "q_start_pos", torch.int32, min_numel=S)
     _dev(context_lens, "context_lens", torch.int32, min_numel=S)
     check_sinks(sinks, H_q)
+    window = _int32(min(window, 2 ** 31 - 1), "window")
     st = _stream_of(stream, "q_rot k_cache v_cache cu_seqlens_q q_start_pos context_lens block_tables bt_offsets out workspace "
                     "sinks", q_rot, k_cache, v_cache, cu_seqlens_q, q_start_pos, context_lens, block_tables, bt_offsets, out,
                     workspace, sinks)
@@ -1083,7 +1094,7 @@ def mixed_step_attention_window(q_rot, k_cache, v_cache, cu_seqlens_q, q_start_p
         q_rot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], cu_seqlens_q.data_ptr(),
         q_start_pos.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(), _ptr(bt_offsets), bt_len, stride, S, T,
         int(context_total), H_q, H_kv, D, PAGE_SIZE, float(D) ** -0.5 if scale is None else float(scale),
-        min(int(window), 2 ** 31 - 1), _ptr(sinks), out.data_ptr(), workspace.data_ptr(),
+        window, _ptr(sinks), out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), st)
     _check(rc, "ms_mixed_step_attention_window")
 

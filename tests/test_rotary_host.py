@@ -257,6 +257,29 @@ def test_step_refuses_bad_forms_before_it_appends(ms):
     assert not seen
 
 
+def test_whole_numbers_beyond_32_bits_are_refused(ms):
+    """ctypes passes a whole number's low 32 bits: the binding refuses what does not fit, where it would have taken another."""
+    torch = pytest.importorskip("torch")
+    for dim in (2 ** 32 + 64, 64 - 2 ** 32):
+        with pytest.raises(ValueError, match="rotary_dim"):
+            ms.rotary_frequencies(dim)
+    for kind in ("bands", "ramp"):
+        with pytest.raises(ValueError, match="original_len"):
+            ms.rotary_frequencies(64, 1e4, {"kind": kind, "factor": 2.0, "original_len": 2 ** 32 + 4096, "low": 1.0, "high": 4.0})
+    tab = torch.zeros(10, 16)
+    for first in (2 ** 32, 2 ** 31, -2 ** 32 + 5):
+        with pytest.raises(ValueError, match="first_pos"):
+            ms.rotary_table_device(np.zeros(16), tab, tab.clone(), first_pos=first)
+    bf, i32 = torch.bfloat16, torch.int32
+    q, pool, one = torch.zeros(1, 4, 64, dtype=bf), torch.zeros(2, 2, 16, 64, dtype=bf), torch.zeros(2, dtype=i32)
+    with pytest.raises(ValueError, match="window"):
+        ms.mixed_step_attention_window(q, pool, pool.clone(), one, one, one, one.view(1, 2), 1, q.clone(), torch.zeros(4096, dtype=torch.uint8),
+                                       16 - 2 ** 32)
+    for dim in (0, -2, 3, 130, 2 ** 31 - 2):  # what fits is the C side's to refuse, and nothing is written past an array
+        with pytest.raises(ms.MixedStepError):
+            ms.rotary_frequencies(dim)
+
+
 def test_round_driver_refuses_tables_of_another_width(ms):
     torch = pytest.importorskip("torch")
     from chunked_prefill_mixed_decode_gb300.driver import RoundDriver
