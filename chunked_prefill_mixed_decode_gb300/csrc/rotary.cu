@@ -327,14 +327,15 @@ extern "C" MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, con
     }
   }
   if (kind == MS_ROTARY_BASE) base *= std::pow(s, R / (R - 2.0));
+  if (!(base > 0.0) || !std::isfinite(base)) return MS_ERR_ARG;
   double lo = 0.0, hi = 0.0;
   if (kind == MS_ROTARY_RAMP) {
     lo = std::fmax(std::floor(pair_of_turns(high, n, base, R)), 0.0);
     hi = std::fmax(std::fmin(std::ceil(pair_of_turns(low, n, base, R)), R - 1.0), lo);
     if (hi == lo) hi += 0.001;
   }
-  *amplitude = 1.0;
-  if (kind == MS_ROTARY_RAMP) *amplitude = scaling->amplitude > 0.0 ? scaling->amplitude : s > 1.0 ? 0.1 * std::log(s) + 1.0 : 1.0;
+  double amp = 1.0, scaled[kMaxPairs];
+  if (kind == MS_ROTARY_RAMP) amp = scaling->amplitude > 0.0 ? scaling->amplitude : s > 1.0 ? 0.1 * std::log(s) + 1.0 : 1.0;
   for (int i = 0; i < R / 2; ++i) {
     const double f = std::pow(base, -2.0 * i / R);
     double g = f;
@@ -347,8 +348,11 @@ extern "C" MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, con
       const double stretch = std::fmin(1.0, std::fmax(0.0, (i - lo) / (hi - lo)));
       g = stretch * (f / s) + (1.0 - stretch) * f;
     }
-    freq[i] = g;
+    if (!std::isfinite(g)) return MS_ERR_ARG;
+    scaled[i] = g;
   }
+  for (int i = 0; i < R / 2; ++i) freq[i] = scaled[i];
+  *amplitude = amp;
   return MS_OK;
 }
 

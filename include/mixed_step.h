@@ -566,7 +566,8 @@ typedef struct {
 /* ms_rotary_frequencies -- host: the scaled frequencies of rotary_dim = R elements
  * into freq [R/2] (radians a position) and the factor of the cosines and sines into
  * *amplitude, in double precision.  scaling NULL is MS_ROTARY_PLAIN.
- * Errors: MS_ERR_ARG (R odd, < 2 or > 128, base <= 0, a bad scaling). */
+ * Errors: MS_ERR_ARG (R odd, < 2 or > 128, base <= 0, a bad scaling, frequencies that
+ * a double does not hold), with nothing written. */
 MS_API int ms_rotary_frequencies(int32_t rotary_dim, double base, const ms_rotary_scaling* scaling, double* freq,
                                  double* amplitude);
 

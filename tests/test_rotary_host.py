@@ -102,6 +102,20 @@ def test_frequency_refusals(ms):
         ms.rotary_frequencies(64, 1e4, {"kind": "linear", "factor": -2.0})
 
 
+def test_frequencies_beyond_what_doubles_hold_are_refused(ms):
+    """A base or factor whose frequencies overflow gives an error and not infinities, NaN or zeros; nothing is written."""
+    f, amp = np.full(64, 7.0), ctypes.c_double(7.0)
+    call = ms.lib().ms_rotary_frequencies
+    tiny = 1e-320
+    for base, sc in ((1e300, (2, 0, 1e30, 0, 0, 0)), (1e-300, (2, 0, 1e-30, 0, 0, 0)), (1e4, (1, 0, tiny, 0, 0, 0)),
+                     (1e4, (3, 8192, tiny, 1, 4, 0)), (1e4, (4, 8192, tiny, 1, 4, 0)), (5e-324, None)):
+        s = None if sc is None else ctypes.byref(ms.RotaryScaling(*sc))
+        assert call(64, base, s, f.ctypes.data, ctypes.addressof(amp)) == ms.MS_ERR_ARG, (base, sc)
+        assert (f == 7.0).all() and amp.value == 7.0
+    assert call(64, 1e300, ctypes.byref(ms.RotaryScaling(2, 0, 1e3, 0, 0, 0)), f.ctypes.data, ctypes.addressof(amp)) == ms.MS_OK
+    assert np.isfinite(f).all() and (f[:32] > 0).all()
+
+
 P = 4096  # an aligned address that no refused call may touch
 
 
