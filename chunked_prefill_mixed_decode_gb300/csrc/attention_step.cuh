@@ -50,6 +50,7 @@ enum {
   H_CLOCK_MHZ = 10,  // SM clock the last call ran at (kept across calls; 0 in a fresh workspace)
   H_TEAM = 11,       // warps that share a decode item, where the kernel runs them in teams
   H_CH_TILES = 12,   // KV tiles to a part of a chunk item (0: items are whole), where the kernel splits them
+  H_KV_FORM = 13,    // spans: how the chunk tiles get K and V (KvForm), for whoever looks
   H_WORDS = 64
 };
 
@@ -723,6 +724,7 @@ __device__ __forceinline__ void prologue_warp(const AttnParams& p) {
     hdr[H_SPLIT] = split;
     if (Teams) hdr[H_TEAM] = plan.team;
     if (Parts) hdr[H_CH_TILES] = part_tiles;
+    if (Span) hdr[H_KV_FORM] = p.kv_form;
     hdr[H_CHUNK_CTAS] = sp.chunk_ctas;
   }
 }
@@ -976,6 +978,7 @@ __device__ __forceinline__ void prologue_body(const AttnParams& p) {
       hdr[H_SPLIT] = static_cast<int32_t>(split);
       if (Teams) hdr[H_TEAM] = plan.team;
       if (Parts) hdr[H_CH_TILES] = part_tiles;
+      if (Span) hdr[H_KV_FORM] = p.kv_form;
       hdr[H_CHUNK_CTAS] = s_split.chunk_ctas;
     }
   }

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 ALL = 2 ** 31 - 1
 CH_TILES, CH_ITEMS = 12, 6  # words of the workspace header: KV tiles to a part, chunk items
-SPLIT = 7  # pages to a decode split
+SPLIT, KV_FORM = 7, 13  # pages to a decode split; how K and V of a page come to the chunk tiles (KvForm)
 
 
 @pytest.fixture(scope="module")
@@ -464,6 +464,25 @@ def test_pools_in_any_place(env, H_q, H_kv, D, where):
             a.k, a.v = k, v
         a.call()
         a.check()
+
+
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64), (8, 1, 64)])
+@pytest.mark.parametrize("where,form", [("k first", 1), ("v first", 2), ("one pool", 0)])
+def test_which_boxes_the_pages_came_in(env, H_q, H_kv, D, where, form):
+    """The header says how a page of K and of V came: as one box with the lower pool's half first, or as two."""
+    torch = env[0]
+    for window in (70, None):
+        a = Span(env, [(333, 130), (40, 1), (1000, 3), (17, 17)], H_q, H_kv, D, window, 1.0 if window else None, seed=12)
+        n = a.k.numel()
+        both = torch.empty(2 * n + 16, dtype=torch.bfloat16, device="cuda")
+        if where == "one pool":
+            a.v = a.k
+        else:
+            k, v = (both[n + 16:], both[:n]) if where == "v first" else (both[:n], both[n + 16:])
+            a.k, a.v = k.view(a.k.shape).copy_(a.k), v.view(a.v.shape).copy_(a.v)
+        a.call()
+        a.check()
+        assert a.word(KV_FORM) == form
 
 
 @pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 128), (4, 4, 64)])
