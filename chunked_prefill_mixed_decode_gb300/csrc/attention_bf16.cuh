@@ -271,10 +271,13 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
     // a register transpose; O^T = V^T P^T accumulates D x 8.
     constexpr int NK = D / 16;  // 16-column steps of a K row, and 16-row blocks of O^T
     const int gq = lane >> 2, tq = lane & 3;
-    // Over spans with up to 4 heads, free columns of the product hold the heads again with what the weights' rounding to
-    // bf16 leaves out, kRest columns from the weights, and O is the sum of the two: of the errors only the output's rounding
-    // is left (256 rows over 1024 keys: 1.7e-3, 2.3e-3 without), for 0.3 % more time.
+    // Over spans the weights are two bf16 numbers, what their rounding leaves out the second, so that of the errors only the
+    // output's rounding is left.  With up to 4 heads, free columns of the product hold the heads again with those, kRest
+    // columns from the weights, and O is the sum of the two (256 rows over 1024 keys, 32 / 8 heads: 2.3e-3 -> 1.7e-3 for
+    // 0.3 % more time).  With 8 heads no column is free, and each fragment of V meets a second product (2.2e-3 -> 1.7e-3; 256
+    // rows over 1024 keys, 64 / 8 heads: 198.9 -> 200.9 us at D = 128, 120.5 -> 120.0 at D = 64).
     constexpr int kRest = !Span || G == 8 ? 0 : G == 1 ? 1 : 4;
+    constexpr bool kTwice = Span && G == 8;
     const int qh = kRest == 1 ? gq >> 1 : kRest == 4 ? gq & 3 : gq;  // head of the lane's Q words
     const int h0 = kRest == 4 ? 2 * (tq & 1) : 2 * tq, h1 = kRest == 1 ? h0 : h0 + 1;  // heads of its scores
     const float rest0 = kRest == 4 && tq >= 2 ? -1.f : 0.f, rest1 = kRest == 1 ? -1.f : rest0;
@@ -357,6 +360,13 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
       // P^T as the B operand: lane holds (tokens 2 tq, 2 tq + 1 | + 8, head gq)
       const uint32_t b0 = movmatrix_trans(*reinterpret_cast<uint32_t*>(&h01));
       const uint32_t b1 = movmatrix_trans(*reinterpret_cast<uint32_t*>(&h23));
+      uint32_t r0 = 0, r1 = 0;
+      if constexpr (kTwice) {  // what the rounding of the weights leaves out
+        const float2 f01 = __bfloat1622float2(h01), f23 = __bfloat1622float2(h23);
+        const __nv_bfloat162 e01 = __floats2bfloat162_rn(p0 - f01.x, p1 - f01.y), e23 = __floats2bfloat162_rn(p2 - f23.x, p3 - f23.y);
+        r0 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&e01));
+        r1 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&e23));
+      }
       if (nv < kPage) {
         // rows past the context in the last page may hold stale (even non-finite) data:
         // zero them in V so that P = 0 times V stays 0
@@ -383,6 +393,7 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
         uint32_t a[4];
         ldsm_x4_trans(vb + (j >> 2) * 2048 + r * 128 + ((chunk ^ (r & 7)) << 4), a);
         mma_16816_bf16(acc[j], a, b0, b1);
+        if constexpr (kTwice) mma_16816_bf16(acc[j], a, r0, r1);
       }
       __syncwarp();
       ++seq_con;

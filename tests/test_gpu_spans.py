@@ -165,6 +165,18 @@ def test_decode_weights_keep_what_rounding_leaves(env, H_q, H_kv, D, window, sin
     assert ((a.out.double() - ref).abs() / bound).max().item() <= 1
 
 
+@pytest.mark.parametrize("H_q,H_kv,D", [x for x in SHAPES if x[0] == 8 * x[1]])
+@pytest.mark.parametrize("window,sinks", [(16, 2.0), (100, None), (1500, 1.0), (ALL, None), (None, None)])
+def test_decode_weights_of_8_heads_keep_what_rounding_leaves(env, H_q, H_kv, D, window, sinks):
+    """The same bound with 8 heads to a KV head, whose remainders take a product of their own."""
+    a = Span(env, [(c + (window is None), 1) for c in CTX], H_q, H_kv, D, window, sinks, seed=3 * D + H_q)
+    a.call()
+    a.check()
+    ref, A = a.reference()
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -16 + 2.0 ** -10) * A + 1e-30
+    assert ((a.out.double() - ref).abs() / bound).max().item() <= 1
+
+
 @pytest.mark.parametrize("H_q,H_kv,D", SHAPES)
 @pytest.mark.parametrize("window,sinks,ragged", [(1, 2.0, False), (7, None, True), (64, None, False), (129, 2.0, True),
                                                  (400, None, False), (ALL, 1.0, False)])
