@@ -91,14 +91,6 @@ __device__ __forceinline__ DecItem describe_dec(const AttnParams& p, int item, i
   return it;
 }
 
-
-// Decode phase: each worker warp of the CTA (12, or 10 at D = 128, G = 8) is
-// independent, with its own ring of page stages, pulling decode items until
-// the queue is empty.  Per page it runs mma.sync m16n8k16 on ldmatrix
-// fragments: 16 tokens against the G query heads (padded to 8).  tcgen05 does
-// not fit here: its M is at least 64 rows, while a decode page is 16 rows per
-// warp and a row's G query heads fill only part of N.
-
 // merge_splits for a KV head's G heads at once, sixteen 16-byte loads of a lane in flight: a lane looks after
 // the weights of head lane % G and every (32 / G)th split, and owns D / 32 columns of every head.  (Head after
 // head, two splits of eight heads took 10 us to join where their pages took 9.)  Records of splits past the
@@ -173,6 +165,12 @@ __device__ __noinline__ void merge_heads(const AttnParams& p, int k, int h0, int
   }
 }
 
+// Decode phase: each worker warp of the CTA (12, or 10 at D = 128, G = 8) is
+// independent, with its own ring of page stages, pulling decode items until
+// the queue is empty.  Per page it runs mma.sync m16n8k16 on ldmatrix
+// fragments: 16 tokens against the G query heads (padded to 8).  tcgen05 does
+// not fit here: its M is at least 64 rows, while a decode page is 16 rows per
+// warp and a row's G query heads fill only part of N.
 // Out of line, as is chunk_phase: each phase gets its own register allocation
 // (inlined into one kernel body the two spill).
 template <int D, int G, bool Span = false>
@@ -267,8 +265,8 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
 
   while (true) {
     // Tensor-core MMAs (mma.sync m16n8k16) on each page.  S^T = K Q^T holds
-    // 16 tokens x 8 query heads (heads past G are zero); P^T goes back through
-    // a register transpose; O^T = V^T P^T accumulates D x 8.
+    // 16 tokens x 8 columns, a query head each (columns past G are zero, or heads again, below);
+    // P^T goes back through a register transpose; O^T = V^T P^T accumulates D x 8.
     constexpr int NK = D / 16;  // 16-column steps of a K row, and 16-row blocks of O^T
     const int gq = lane >> 2, tq = lane & 3;
     // Over spans the weights are two bf16 numbers, what their rounding leaves out the second, so that of the errors only the
@@ -312,7 +310,7 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
       }
       const int tok0 = (cur.p0 + pi) * kPage;
       const int nv = min(kPage, cur.ctx - tok0);  // valid keys in this page (>= 1)
-      // S^T: lane holds (token gq, heads 2 tq, 2 tq + 1) and (token gq + 8, same heads)
+      // S^T: lane holds (token gq, columns 2 tq, 2 tq + 1: heads h0, h1) and (token gq + 8, same columns)
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
@@ -357,7 +355,7 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
         h01 = __floats2bfloat162_rn(fmaf(rest0, f01.x, p0), fmaf(rest1, f01.y, p1));
         h23 = __floats2bfloat162_rn(fmaf(rest0, f23.x, p2), fmaf(rest1, f23.y, p3));
       }
-      // P^T as the B operand: lane holds (tokens 2 tq, 2 tq + 1 | + 8, head gq)
+      // P^T as the B operand: lane holds (tokens 2 tq, 2 tq + 1 | + 8, column gq)
       const uint32_t b0 = movmatrix_trans(*reinterpret_cast<uint32_t*>(&h01));
       const uint32_t b1 = movmatrix_trans(*reinterpret_cast<uint32_t*>(&h23));
       uint32_t r0 = 0, r1 = 0;
@@ -409,7 +407,7 @@ __device__ __noinline__ void decode_phase(const AttnParams& p, uint8_t* dsmem, c
           else if (e % 2 == 0) acc[j][e] += acc[j][e + 1];
         }
     }
-    // O^T: lane holds (d 16 j + gq, heads 2 tq, 2 tq + 1) and (d 16 j + gq + 8, same heads)
+    // O^T: lane holds (d 16 j + gq, columns 2 tq, 2 tq + 1) and (d 16 j + gq + 8, same columns); column g < G is head g
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, o);

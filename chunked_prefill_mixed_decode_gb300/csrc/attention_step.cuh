@@ -435,10 +435,14 @@ __device__ __forceinline__ DecPlan decode_plan(const AttnParams& p, int64_t dec_
 // and of ts with every warp at the memory's rate,
 //     floor(x) L max(tp, ts) + max(s tp, frac(x) L ts) + 6.5 ceil(x) + (2 + 0.1 G splits where there is a join)
 // us, s: pages of a split, L: of an item on average.  Fitted to sweeps over 29 steps (1 to 512 rows of 1 to 40 KV
-// heads, 1 to 6251 pages, 14 to 500 us) in a build that forced the split for the purpose: its choices took 0.2 %
-// longer than the best of each sweep, 2.2 % the worst.  warps: those that decode rows get beside chunk rows.
+// heads, 1 to 6251 pages, 14 to 500 us) in a build that forced the split for the purpose: the estimate's own choices took
+// 0.2 % longer than the best of each sweep, 2.2 % the worst.  warps: those that decode rows get beside chunk rows.
+// What runs is the best of the counts that the workspace has places for, and it has one split per 32 pages of
+// context_total and two a row (ws_layout): few rows whose context_total is just their contexts' sum get fewer splits than the
+// estimate wants.  One row over 1024 keys, 32 / 8 heads: 3 splits, 30 us, where a context_total of 20000 gives 13 and 20;
+// one over 1500 states, 20 heads of 64, 31 and 17 us; twenty over 2000 states, 8 heads of 64, 41 us, 33 at 60000 and 29 at 200000.
 // Rows of up to kWholePages pages are not split (nor does the prologue, which runs from a cold instruction cache,
-// then come here: 2 us).  Called by whole warps.
+// then come here: 2 us), a single row of 18 pages included (21 us).  Called by whole warps.
 constexpr int kWholePages = 18;
 
 __device__ __noinline__ int span_split(const AttnParams& p, int64_t dec_pages, int n_dec, int max_pages, float warps) {

@@ -243,7 +243,8 @@ def run_step(q, k, v, batch: DeviceBatch, cos, sin, k_cache, v_cache, out, works
     then the attention, with the prologue inside the append's launch on small steps).  With a ``rotary_dim`` of less than
     the head (0, with tables of None: nothing turns), ``interleaved`` pairs, or q, k, v whose tokens' rows lie apart, the
     append is kv_append_rotary; with a ``window`` or ``sinks`` the attention is mixed_step_attention_window.  Tables of
-    another width than ``rotary_dim`` says (check_rotary_tables) are refused."""
+    another width than ``rotary_dim`` says (check_rotary_tables) are refused.  The append and the attention are then two
+    calls: what the attention alone refuses (a workspace too small, a count of heads) is refused behind the append."""
     if q.dim() != 3:
         raise ValueError(f"q must be [T, H_q, D], got {tuple(q.shape)}")
     if q_rot is None:

@@ -621,9 +621,12 @@ MS_API int ms_kv_append_rotary(const void* q, int64_t q_stride, const void* k, i
  * no token of the row sees do not matter, infinities and NaN included.
  *   window     >= 1; a window of a row's length or more changes nothing
  *   sinks      device fp32 [H_q] or NULL; any finite value, or -infinity (no sink)
- *   workspace  as for ms_mixed_step_attention; with one of
- *              ms_attention_workspace_size_q4 bytes few long chunk items are cut into
- *              parts that run at once
+ *   workspace  as for ms_mixed_step_attention, for whole contexts and not for what the
+ *              windows show of them; with one of ms_attention_workspace_size_q4 bytes few
+ *              long chunk items are cut into parts that run at once.  It has places for
+ *              one decode split per 512 keys of context_total and two a row: few decode rows
+ *              are faster with a larger context_total (and the workspace for it) than their
+ *              contexts' sum (one row over 1024 keys, 32 / 8 heads: 30 us, 20 with 20000)
  * Errors: MS_ERR_ARG, MS_ERR_CUDA. */
 MS_API int ms_mixed_step_attention_window(const void* q_rot, const void* k_cache, const void* v_cache, int32_t num_pages,
                                           const int32_t* cu_seqlens_q, const int32_t* q_start_pos,
@@ -638,7 +641,8 @@ MS_API int ms_mixed_step_attention_window(const void* q_rot, const void* k_cache
  * keys in the row's pages (an encoder's states, put there by ms_kv_append_rotary with
  * R = 0), whatever its position: rows of one and of more tokens in one call, as
  * packed for the step's self-attention.  The tokens of a row with key_lens[s] = 0 get
- * zeros.  key_total bounds the sum of key_lens (pad rows' too).  Tables, workspace,
+ * zeros.  key_total bounds the sum of key_lens (pad rows' too); a larger one leaves few
+ * decode rows more splits, as context_total does there.  Tables, workspace,
  * status bits, limits and errors as ms_mixed_step_attention_window; a row needs
  * ceil(key_lens[s] / 16) pages.  Errors: MS_ERR_ARG, MS_ERR_CUDA. */
 MS_API int ms_mixed_step_cross_attention(const void* q, const void* k_cache, const void* v_cache, int32_t num_pages,
