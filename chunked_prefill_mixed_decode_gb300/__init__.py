@@ -1040,9 +1040,10 @@ def kv_append_rotary(q, k, v, positions, slot_mapping, cos_tab, sin_tab, k_cache
 
 
 def check_sinks(sinks, H_q: int) -> None:
+    if sinks is None:
+        return
     import torch
-    if sinks is not None:
-        _dev(sinks, "sinks", torch.float32, (H_q,))
+    _dev(sinks, "sinks", torch.float32, (H_q,))
 
 
 def _span_args(q, k_cache, v_cache, cu_seqlens_q, block_tables, bt_offsets, out, workspace):

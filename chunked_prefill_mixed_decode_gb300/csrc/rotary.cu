@@ -53,15 +53,16 @@ uint64_t turns_fixed(double f) {
 // table (device)
 // ----------------------------------------------------------------------------
 //
-// The angle of (position p, pair i) is p * turns[i] modulo 1 in 64-bit whole numbers, off by the frequency's
-// last bit p times, (p + 1) 2^-65 turns at most.  It is split into the nearest quarter turn and a rest x of at most
-// pi / 4, in two floats: of the rest's 62 bits the upper 45 are taken (2 pi 2^-47 left out), and the small
-// part's own roundings are below that too, so that x is off by 2 pi 2^-46 at most beside the angle's error.  Cosine
-// and sine of x by their Taylor series in fp32 (the first term left out is below 3e-9), with the leading terms kept
-// in two floats.  What the last rounding does not cause is the rounding of the cubic term's factors: 3.5 of them,
-// 2^-24 each, of at most 0.115 of a sine.  A result is off by at most 0.8 * 2^-23 of its size (0.5 + 0.2 + 0.03) and by the
-// angle's error times the amplitude, which shows where a sine is below 1e-6: there it is several of its steps, if 1e-13 in
-// all: a rotation passes absolute errors on, so the 17 bits below are not carried as a third float.  (FP64 has 1/64 of the fp32 rate on this GPU.)
+// The angle of (position p, pair i) is p * turns[i] modulo 1 in 64-bit whole numbers, off by p times the
+// frequency's last bit, (p + 1) 2^-65 turns at most.  It is split into the nearest quarter turn and a rest x
+// of at most pi / 4, in two floats: of the rest's 62 bits the upper 45 are taken (2 pi 2^-47 left out), and the
+// small part's own roundings are below that too, so that x is off by 2 pi 2^-46 at most beside the angle's error.
+// Cosine and sine of x by their Taylor series in fp32 (the first term left out is below 3e-9), with the leading
+// terms kept in two floats.  What the last rounding does not cause is the rounding of the cubic term's factors:
+// 3.5 of them, 2^-24 each, of at most 0.115 of a sine.  A result is off by at most 0.8 * 2^-23 of its size (0.5 +
+// 0.2 + 0.03) and by x's and the angle's error times the amplitude, which shows where a sine is below 1e-6: there
+// it is several of its steps, if 1e-13 in all.  A rotation passes absolute errors on, so the 17 bits below are not
+// carried in a third float.  (FP64 has 1/64 of the fp32 rate on this GPU.)
 
 // The amplitude m in two floats, and m times the Taylor coefficients.
 struct Series {

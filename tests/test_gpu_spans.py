@@ -211,6 +211,26 @@ def test_window_few_chunk_rows(env, H_q, H_kv, D, rows, window, sinks):
         a.check()
 
 
+@pytest.mark.parametrize("rows,H_q,H_kv,D,window", [([(1023, 1)], 32, 8, 128, 1024), ([(1500, 1)], 20, 20, 64, None), ([(1999, 1)] * 20, 8, 8, 64, ALL),
+                                                    ([(4095, 1)], 8, 1, 128, ALL)])
+def test_few_decode_rows_get_the_splits_that_the_bound_has_places_for(env, rows, H_q, H_kv, D, window):
+    """A bound above the contexts' sum, with the workspace for it, leaves room for more splits; the rows stay what they are."""
+    torch, ms, _ = env
+    a = Span(env, rows, H_q, H_kv, D, window, None if window is None else 1.0, seed=14)
+    a.call()
+    a.check()
+    split, total = a.word(SPLIT), a.total
+    pages = -(-max(a.ends) // 16)
+    assert -(-pages // split) <= total // 512 + 1 + 2 * len(rows)  # a split needs a place: one per 32 pages, two a row
+    a.total = total + 200000
+    ws = torch.zeros(ms.attention_workspace_size(len(rows), a.T, a.total, H_q, H_kv, D), dtype=torch.uint8, device="cuda")
+    a.out.fill_(5.0)
+    a.call(ws=ws)
+    a.total = total
+    assert int(ws[:256].view(torch.int32)[SPLIT]) < split and ms.read_status(ws) == 0
+    a.check()
+
+
 def test_some_of_the_few_rows_were_cut(env):
     for H_q, H_kv, D in SHAPES:
         for window in (9000, None):
